@@ -15,9 +15,11 @@
  * Around them: the main-attention prepare (qsa_main_prepare, or fused into
  * stage 1 through qsa_step_args.main), the k-step MTP draft whose later
  * steps reuse step 0's selection (qsa_mtp_steps), the fused qkv + indexer
- * projection GEMM that produces the step's inputs (qsa_qkv_index_proj), and
+ * projection GEMM that produces the step's inputs (qsa_qkv_index_proj),
  * stage 4 for callers that cannot give it a workspace
- * (qsa_sparse_gqa_noalloc).
+ * (qsa_sparse_gqa_noalloc), a KV cache with block scales (qsa_kv_append
+ * writes it, qsa_sparse_gqa_scaled is stage 4 over it) and window attention
+ * over any of the caches (qsa_window_gqa).
  *
  * Sources: "vllm.models.qwen4_exp.nvidia.qsa" (QSAIndexer.forward and its
  * unfused reference path, Qwen4ExpQSAImpl.forward), "vllm.models.qwen4_exp.
@@ -65,7 +67,11 @@ typedef enum qsa_status {
   QSA_ERR_DEVICE_FAULT = 7  /* device-side masked out-of-range accesses */
 } qsa_status;
 
-enum { QSA_DTYPE_BF16 = 0, QSA_DTYPE_E4M3 = 1 };
+/* QSA_DTYPE_E4M3_BLOCK is a KV cache type only: e4m3 codes with a power-of-two
+ * scale for each block of tokens and KV head (qsa_kv_scales).  The entry
+ * points that take a qsa_kv_scales accept it; the others answer
+ * QSA_ERR_DTYPE. */
+enum { QSA_DTYPE_BF16 = 0, QSA_DTYPE_E4M3 = 1, QSA_DTYPE_E4M3_BLOCK = 2 };
 
 /* Indexer configuration ("vllm.models.qwen4_exp.nvidia.qsa", QSAIndexer.__init__:
  * indexer_n_heads, indexer_head_dim, indexer_budget, indexer_compress_ratio,
@@ -385,6 +391,114 @@ qsa_status qsa_layer_step(const qsa_cfg* cfg, const qsa_gqa_cfg* gcfg,
 #define QSA_MTP_MAX_STEPS 16
 qsa_status qsa_mtp_steps(const qsa_cfg* cfg, const qsa_gqa_cfg* gcfg, const qsa_step_args* steps,
                          int32_t k, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The scales of a QSA_DTYPE_E4M3_BLOCK cache.  A token's K of one KV head is
+ * code * 2^(b - 127), b the K byte of its block of scale_block tokens, and V
+ * likewise.  Bytes stand for 2^-40 .. 2^40 (87 .. 167); others are read as
+ * the nearest of them.
+ *  scales       [num_blocks, Hkv, page_size / scale_block, 2] bytes: K, V;
+ *               4-byte aligned
+ *  scale_block  tokens per scale: 16, 32 or 64, a divisor of page_size
+ */
+typedef struct qsa_kv_scales {
+  void* scales;
+  int32_t scale_block;
+} qsa_kv_scales;
+
+/*
+ * qsa_kv_append -- a step's keys and values into the paged KV cache, with the
+ * norm and the position rotation applied on the way: qsa_main_prepare for
+ * every cache type, for K and V alone where m->q_out and m->gate_out are both
+ * NULL.  q, gate, bf16 and statically scaled caches get qsa_main_prepare's
+ * results.  No counterpart on the pages the method comes from for block
+ * scales: this is a library addition.
+ *
+ * With block scales (gcfg->kv_dtype QSA_DTYPE_E4M3_BLOCK; `scales` is NULL for
+ * the other types) a run of rows -- consecutive rows whose slots ascend inside
+ * one scale block -- shares one scale for K and one for V of each KV head.
+ * Let a be the largest finite |x| over the run and e_new the smallest e with
+ * a <= 448 * 2^e, within [-40, 40] (larger values saturate).  A run that
+ * begins its block sets e = e_new, whatever the block held; another takes
+ * e = max(e_old, e_new) and, where e > e_old, re-encodes the codes of the
+ * block's offsets before it as e4m3(code * 2^(e_old - e)).  Its own are
+ * e4m3(x * 2^-e) (ties to even; infinities saturate, a NaN stays a NaN).
+ * Offsets after the run keep their codes: they belong to no token yet.
+ *  - Slots < 0 write nothing for their row (padding); slots past the cache are
+ *    masked and counted.
+ *  - A row whose slot repeats its predecessor's or steps back inside one scale
+ *    block is not written, and counted.  Runs of one call that are not
+ *    neighbours must lie in different scale blocks: they would race.
+ *  - A scale block belongs to one sequence: sequences that share a page share
+ *    whole scale blocks that are full.
+ */
+qsa_status qsa_kv_append(const qsa_cfg* cfg, const qsa_gqa_cfg* gcfg, const qsa_main_prep* m,
+                         const qsa_kv_scales* scales, const int64_t* positions,
+                         const float* cos_sin, int32_t rows, void* stream);
+
+/*
+ * qsa_sparse_gqa_scaled -- qsa_sparse_gqa over a cache with block scales
+ * (gcfg->kv_dtype QSA_DTYPE_E4M3_BLOCK).  Arguments and results are those of
+ * qsa_sparse_gqa; each score takes its token's K scale and each value its
+ * token's V scale.  ws: qsa_workspace_bytes() bytes for this gcfg.
+ *  reqs   rows of block_table; a row whose token_to_req is outside [0, reqs)
+ *         is counted and gets zeros
+ */
+qsa_status qsa_sparse_gqa_scaled(const qsa_gqa_cfg* gcfg, const qsa_kv_scales* scales,
+                                 const void* q, const void* kv, const int32_t* block_table,
+                                 int32_t bt_stride, const int32_t* packed, int32_t packed_width,
+                                 const int32_t* token_to_req, const void* gate, void* out,
+                                 int32_t rows, int32_t reqs, void* ws, size_t ws_bytes,
+                                 void* stream);
+
+/*
+ * qsa_window_gqa -- grouped-query attention over the paged KV cache with a
+ * sliding window and a few first tokens that stay visible (sinks): the row of
+ * position p sees token t of its request iff
+ *     t <= p  and  (t > p - window  or  t < sinks),
+ * with scale D^-1/2, zero where it sees nothing (p < 0, or window and sinks
+ * both 0), and qsa_sparse_gqa's output gate.  A window that reaches back to
+ * token 0 is plain causal attention.  From a single row to a prefill chunk,
+ * ragged batches of both included.  No counterpart on the pages the method
+ * comes from: models that interleave sparse with window layers keep both
+ * kinds of layers in the same paged cache.
+ *  rows, reqs     rows [query_start_loc[r], query_start_loc[r + 1]) belong to
+ *                 request r and token_to_req names it; rows of no request
+ *                 (padding behind the last one) keep what `out` held
+ *  window, sinks  >= 0
+ *  max_context    an upper bound of p + 1 over the rows: it sizes the split of
+ *                 long rows over CTAs (a smaller value costs time, no more)
+ *  kv, scales     the cache in the gcfg's kv_dtype; scales as for
+ *                 qsa_kv_append (NULL unless QSA_DTYPE_E4M3_BLOCK)
+ *  block_table    [reqs, bt_stride]; entries of pages that no row of the call
+ *                 sees may be stale or -1, and tokens that no row sees may
+ *                 hold anything.  A visible token on a page outside the cache
+ *                 is left out of the sum and counted
+ *  ws             qsa_window_workspace_bytes() bytes, 256-byte aligned (NULL
+ *                 where that is 0); its contents need not be kept or cleared
+ */
+typedef struct qsa_window_args {
+  int32_t rows, reqs;
+  int32_t window, sinks;
+  int32_t max_context;
+  int32_t bt_stride;
+  const void* q;                    /* [rows, Hq, D] bf16 */
+  const void* kv;                   /* [num_blocks, Hkv, page, 2D] */
+  const qsa_kv_scales* scales;
+  const int32_t* block_table;       /* [reqs, bt_stride] */
+  const int32_t* token_to_req;      /* [rows] */
+  const int32_t* query_start_loc;   /* [reqs + 1] */
+  const int32_t* logical_positions; /* [rows] */
+  const void* gate;                 /* [rows, Hq, D] bf16 or NULL */
+  void* out;                        /* [rows, Hq, D] bf16 */
+} qsa_window_args;
+
+qsa_status qsa_window_gqa(const qsa_gqa_cfg* gcfg, const qsa_window_args* args, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/* Scratch bytes of qsa_window_gqa for these sizes (the pointers are not read;
+ * 0: none needed, or invalid sizes). */
+size_t qsa_window_workspace_bytes(const qsa_gqa_cfg* gcfg, const qsa_window_args* args);
 
 /* Scratch bytes needed by qsa_layer_step (and enough for every stage call)
  * for `rows` rows, `reqs` requests and V(p) <= max_visible.  The workspace

@@ -466,6 +466,178 @@ qsa_status do_gqa(const qsa_gqa_cfg* gcfg, const void* q, const void* kv,
   return cuda_status(launch_sparse_gqa(p, stream, pdl, !tickets_zeroed));
 }
 
+// The scales of a cache with block scales, or their absence for the others.
+qsa_status check_scales(const qsa_gqa_cfg* g, const qsa_kv_scales* s) {
+  if (g->kv_dtype != QSA_DTYPE_E4M3_BLOCK) return s == nullptr ? QSA_OK : QSA_ERR_INVALID_ARG;
+  if (s == nullptr || s->scales == nullptr) return QSA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(s->scales) & 3) return QSA_ERR_INVALID_ARG;
+  if (s->scale_block != 16 && s->scale_block != 32 && s->scale_block != 64)
+    return QSA_ERR_UNSUPPORTED;
+  return g->page_size % s->scale_block == 0 ? QSA_OK : QSA_ERR_SHAPE;
+}
+
+// Row ids of the cache, (block * Hkv + head) * page + offset, have 32 bits.
+qsa_status check_row_ids(const qsa_gqa_cfg* g) {
+  return static_cast<long long>(g->num_blocks) * g->num_kv_heads * g->page_size < (1ll << 32) - 1
+             ? QSA_OK
+             : QSA_ERR_SHAPE;
+}
+
+// Runs an entry point's body; a C++ exception (a failed host allocation)
+// becomes a status instead of leaving through C.
+template <typename F>
+qsa_status no_throw(F&& body) {
+  try {
+    return body();
+  } catch (...) {
+    return QSA_ERR_CUDA;
+  }
+}
+
+qsa_status do_append(const qsa_cfg* cfg, const qsa_gqa_cfg* g, const qsa_main_prep* m,
+                     const qsa_kv_scales* scales, const int64_t* positions, const float* cos_sin,
+                     int32_t rows, cudaStream_t stream) {
+  qsa_status st = check_cfg(cfg);
+  if (st != QSA_OK) return st;
+  st = check_gcfg(g, /*block_scales=*/true);
+  if (st != QSA_OK) return st;
+  if (rows < 0) return QSA_ERR_SHAPE;
+  if (m == nullptr) return QSA_ERR_INVALID_ARG;
+  if (rows == 0) return QSA_OK;
+  const bool query = m->q_out != nullptr;
+  if (query != (m->gate_out != nullptr)) return QSA_ERR_INVALID_ARG;
+  if (!m->qkv || (query && !m->q_norm_w) || !m->k_norm_w || !m->kv || !m->slot_mapping ||
+      !positions || !cos_sin)
+    return QSA_ERR_INVALID_ARG;
+  if (!(m->eps >= 0.f)) return QSA_ERR_INVALID_ARG;
+  const uintptr_t a16 = reinterpret_cast<uintptr_t>(m->qkv) | reinterpret_cast<uintptr_t>(m->q_norm_w) |
+                        reinterpret_cast<uintptr_t>(m->k_norm_w) | reinterpret_cast<uintptr_t>(m->q_out) |
+                        reinterpret_cast<uintptr_t>(m->gate_out) | reinterpret_cast<uintptr_t>(m->kv) |
+                        reinterpret_cast<uintptr_t>(cos_sin);
+  const uintptr_t a8 = reinterpret_cast<uintptr_t>(m->slot_mapping) | reinterpret_cast<uintptr_t>(positions);
+  if ((a16 & 15) || (a8 & 7)) return QSA_ERR_INVALID_ARG;
+  st = check_scales(g, scales);
+  if (st != QSA_OK) return st;
+  // (grid limits: a few CTAs per row)
+  if (static_cast<long long>(rows) * (g->num_kv_heads + 1) >= (1ll << 31)) return QSA_ERR_SHAPE;
+  AppendParams p{};
+  p.qkv = static_cast<const uint16_t*>(m->qkv);
+  p.q_norm_w = static_cast<const uint16_t*>(m->q_norm_w);
+  p.k_norm_w = static_cast<const uint16_t*>(m->k_norm_w);
+  p.q_out = static_cast<uint16_t*>(m->q_out);
+  p.gate_out = static_cast<uint16_t*>(m->gate_out);
+  p.kv = m->kv;
+  p.scales = scales != nullptr ? scales->scales : nullptr;
+  p.scale_block = scales != nullptr ? scales->scale_block : 0;
+  p.slots = m->slot_mapping;
+  p.positions = positions;
+  p.cos_sin = cos_sin;
+  p.rows = rows;
+  p.hq = g->num_q_heads;
+  p.hkv = g->num_kv_heads;
+  p.page = g->page_size;
+  p.num_blocks = g->num_blocks;
+  p.kv_dtype = g->kv_dtype;
+  p.max_pos = cfg->max_position;
+  p.mrope = (cfg->mrope_section[0] || cfg->mrope_section[1] || cfg->mrope_section[2]) ? 1 : 0;
+  p.sec_h = cfg->mrope_section[1];
+  p.sec_w = cfg->mrope_section[2];
+  p.eps = m->eps;
+  p.k_scale = g->k_scale;
+  p.v_scale = g->v_scale;
+  p.err = error_word();
+  if (p.err == nullptr) return QSA_ERR_CUDA;
+  return cuda_status(launch_kv_append(p, stream));
+}
+
+// The parts that the two row-attention entry points share.
+qsa_status fill_row_gqa(RowGqaParams* p, const qsa_gqa_cfg* g, const qsa_kv_scales* scales,
+                        const void* q, const void* kv, const int32_t* block_table,
+                        int32_t bt_stride, const int32_t* token_to_req, const void* gate, void* out,
+                        int32_t rows, int32_t reqs) {
+  if (!q || !kv || !block_table || !token_to_req || !out) return QSA_ERR_INVALID_ARG;
+  const uintptr_t a16 = reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(kv) |
+                        reinterpret_cast<uintptr_t>(gate) | reinterpret_cast<uintptr_t>(out);
+  if (a16 & 15) return QSA_ERR_INVALID_ARG;
+  if (bt_stride < 1 || reqs < 1) return QSA_ERR_SHAPE;
+  qsa_status st = check_scales(g, scales);
+  if (st != QSA_OK) return st;
+  st = check_row_ids(g);
+  if (st != QSA_OK) return st;
+  if (static_cast<long long>(rows) * g->num_kv_heads >= (1ll << 31)) return QSA_ERR_SHAPE;
+  p->q = static_cast<const uint16_t*>(q);
+  p->kv = kv;
+  p->scales = scales != nullptr ? static_cast<const uint8_t*>(scales->scales) : nullptr;
+  p->scale_block = scales != nullptr ? scales->scale_block : 0;
+  p->block_table = block_table;
+  p->token_to_req = token_to_req;
+  p->gate = static_cast<const uint16_t*>(gate);
+  p->out = static_cast<uint16_t*>(out);
+  p->bt_stride = bt_stride;
+  p->rows = rows;
+  p->reqs = reqs;
+  p->hq = g->num_q_heads;
+  p->hkv = g->num_kv_heads;
+  p->group = g->num_q_heads / g->num_kv_heads;
+  p->page = g->page_size;
+  p->num_blocks = g->num_blocks;
+  p->kv_dtype = g->kv_dtype;
+  p->k_scale = g->k_scale;
+  p->v_scale = g->v_scale;
+  p->err = error_word();
+  return p->err != nullptr ? QSA_OK : QSA_ERR_CUDA;
+}
+
+qsa_status do_sparse_scaled(const qsa_gqa_cfg* g, const qsa_kv_scales* scales, const void* q,
+                            const void* kv, const int32_t* block_table, int32_t bt_stride,
+                            const int32_t* packed, int32_t packed_width,
+                            const int32_t* token_to_req, const void* gate, void* out, int32_t rows,
+                            int32_t reqs, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  qsa_status st = check_gcfg(g, /*block_scales=*/true);
+  if (st != QSA_OK) return st;
+  if (g->kv_dtype != QSA_DTYPE_E4M3_BLOCK) return QSA_ERR_DTYPE;
+  if (rows < 0) return QSA_ERR_SHAPE;
+  if (rows == 0) return QSA_OK;
+  if (packed_width < 2) return QSA_ERR_SHAPE;
+  if (packed == nullptr) return QSA_ERR_INVALID_ARG;
+  (void)ws;
+  (void)ws_bytes;
+  RowGqaParams p{};
+  st = fill_row_gqa(&p, g, scales, q, kv, block_table, bt_stride, token_to_req, gate, out, rows, reqs);
+  if (st != QSA_OK) return st;
+  p.packed = packed;
+  p.packed_width = packed_width;
+  return cuda_status(launch_row_gqa(p, stream));
+}
+
+// Sizes of a window call, without its pointers.
+qsa_status check_window(const qsa_gqa_cfg* g, const qsa_window_args* a) {
+  const qsa_status st = check_gcfg(g, /*block_scales=*/true);
+  if (st != QSA_OK) return st;
+  if (a == nullptr) return QSA_ERR_INVALID_ARG;
+  if (a->rows < 0 || a->reqs < 0 || a->max_context < 0) return QSA_ERR_SHAPE;
+  if (a->window < 0 || a->sinks < 0) return QSA_ERR_INVALID_ARG;
+  return QSA_OK;
+}
+
+qsa_status do_window(const qsa_gqa_cfg* g, const qsa_window_args* a, void* ws, size_t ws_bytes,
+                     cudaStream_t stream) {
+  qsa_status st = check_window(g, a);
+  if (st != QSA_OK || a->rows == 0) return st;
+  if (!a->query_start_loc || !a->logical_positions) return QSA_ERR_INVALID_ARG;
+  (void)ws;
+  (void)ws_bytes;
+  RowGqaParams p{};
+  st = fill_row_gqa(&p, g, a->scales, a->q, a->kv, a->block_table, a->bt_stride, a->token_to_req,
+                    a->gate, a->out, a->rows, a->reqs);
+  if (st != QSA_OK) return st;
+  p.qsl = a->query_start_loc;
+  p.logical = a->logical_positions;
+  p.window = a->window;
+  p.sinks = a->sinks;
+  return cuda_status(launch_row_gqa(p, stream));
+}
+
 // Layer-step workspace regions.
 struct StepLayout {
   size_t q_idx, logits, logits_ws, gqa_ws, total;
@@ -474,7 +646,7 @@ struct StepLayout {
 
 bool step_layout(const qsa_cfg* c, const qsa_gqa_cfg* g, int rows, int reqs, int max_visible,
                  StepLayout* L) {
-  if (check_cfg(c) != QSA_OK || check_gcfg(g) != QSA_OK) return false;
+  if (check_cfg(c) != QSA_OK || check_gcfg(g, /*block_scales=*/true) != QSA_OK) return false;
   if (rows < 0 || reqs < 0 || max_visible < 0) return false;
   const int pw = c->token_topk + c->compress_ratio;
   L->ld = logits_ld(max_visible);
@@ -512,7 +684,7 @@ int sm_count() {
 
 // Validation of the main-attention configuration, shared by every entry
 // point that runs stage 4.
-qsa_status check_gcfg(const qsa_gqa_cfg* g) {
+qsa_status check_gcfg(const qsa_gqa_cfg* g, bool block_scales) {
   if (g == nullptr) return QSA_ERR_INVALID_ARG;
   if (g->head_dim != 128) return QSA_ERR_UNSUPPORTED;
   if (g->num_kv_heads < 1 || g->num_q_heads < g->num_kv_heads ||
@@ -522,7 +694,9 @@ qsa_status check_gcfg(const qsa_gqa_cfg* g) {
   if (group > 8 && group != 16) return QSA_ERR_UNSUPPORTED;
   if (g->page_size < 16 || g->page_size % 16 != 0) return QSA_ERR_SHAPE;
   if (g->num_blocks < 1) return QSA_ERR_SHAPE;
-  if (g->kv_dtype != QSA_DTYPE_BF16 && g->kv_dtype != QSA_DTYPE_E4M3) return QSA_ERR_DTYPE;
+  if (g->kv_dtype != QSA_DTYPE_BF16 && g->kv_dtype != QSA_DTYPE_E4M3 &&
+      !(block_scales && g->kv_dtype == QSA_DTYPE_E4M3_BLOCK))
+    return QSA_ERR_DTYPE;
   if (g->kv_dtype == QSA_DTYPE_E4M3 &&
       !(g->k_scale > 0.f && g->v_scale > 0.f && g->k_scale < 3.0e38f && g->v_scale < 3.0e38f))
     return QSA_ERR_INVALID_ARG;
@@ -707,6 +881,40 @@ qsa_status qsa_main_prepare(const qsa_cfg* cfg, const qsa_gqa_cfg* gcfg, const q
   return cuda_status(launch_main_prepare(p, static_cast<cudaStream_t>(stream)));
 }
 
+qsa_status qsa_kv_append(const qsa_cfg* cfg, const qsa_gqa_cfg* gcfg, const qsa_main_prep* m,
+                         const qsa_kv_scales* scales, const int64_t* positions,
+                         const float* cos_sin, int32_t rows, void* stream) {
+  return no_throw([&] {
+    return do_append(cfg, gcfg, m, scales, positions, cos_sin, rows,
+                     static_cast<cudaStream_t>(stream));
+  });
+}
+
+qsa_status qsa_sparse_gqa_scaled(const qsa_gqa_cfg* gcfg, const qsa_kv_scales* scales,
+                                 const void* q, const void* kv, const int32_t* block_table,
+                                 int32_t bt_stride, const int32_t* packed, int32_t packed_width,
+                                 const int32_t* token_to_req, const void* gate, void* out,
+                                 int32_t rows, int32_t reqs, void* ws, size_t ws_bytes,
+                                 void* stream) {
+  return no_throw([&] {
+    return do_sparse_scaled(gcfg, scales, q, kv, block_table, bt_stride, packed, packed_width,
+                            token_to_req, gate, out, rows, reqs, ws, ws_bytes,
+                            static_cast<cudaStream_t>(stream));
+  });
+}
+
+qsa_status qsa_window_gqa(const qsa_gqa_cfg* gcfg, const qsa_window_args* args, void* ws,
+                          size_t ws_bytes, void* stream) {
+  return no_throw([&] {
+    return do_window(gcfg, args, ws, ws_bytes, static_cast<cudaStream_t>(stream));
+  });
+}
+
+size_t qsa_window_workspace_bytes(const qsa_gqa_cfg* gcfg, const qsa_window_args* args) {
+  if (check_window(gcfg, args) != QSA_OK) return 0;
+  return 0;
+}
+
 qsa_status qsa_mtp_steps(const qsa_cfg* cfg, const qsa_gqa_cfg* gcfg, const qsa_step_args* steps,
                          int32_t k, void* ws, size_t ws_bytes, void* stream) {
   if (steps == nullptr || k < 1 || k > QSA_MTP_MAX_STEPS) return QSA_ERR_INVALID_ARG;
@@ -745,7 +953,7 @@ int32_t qsa_step_launches(const qsa_cfg* cfg, const qsa_gqa_cfg* gcfg, int32_t r
 }
 
 int32_t qsa_gqa_splits(const qsa_gqa_cfg* gcfg, int32_t rows, int32_t packed_width) {
-  if (check_gcfg(gcfg) != QSA_OK || rows <= 0 || packed_width < 2) return 0;
+  if (check_gcfg(gcfg, /*block_scales=*/true) != QSA_OK || rows <= 0 || packed_width < 2) return 0;
   return gqa_num_splits(rows, gcfg->num_kv_heads, packed_width, sm_count());
 }
 

@@ -1,0 +1,294 @@
+// qsa_kv_append: a step's keys and values into the paged KV cache, with the
+// norm and the position rotation applied on the way, and the main attention's
+// q and gate beside them when asked for.
+//
+// Mathematics.  Per row and KV head: k = RoPE(GemmaRMSNorm(k)), v as it is
+// (qsa_rope.cuh, fp32, one rounding to the cache's type).  bf16 caches store
+// them as they are, e4m3 caches with a static scale store e4m3(x / scale).
+// With block scales a run -- consecutive rows whose slots ascend inside one
+// block of B tokens -- shares one power of two for K and one for V of each KV
+// head: with a = max |x| over the run (finite values),
+//   e_new = the smallest e with a <= 448 * 2^e, within [-40, 40];
+//   e     = e_new if the run begins the block, else max(e_old, e_new);
+//   code  = e4m3(x * 2^-e), and the codes before the run become
+//           e4m3(code * 2^(e_old - e)) when e > e_old.
+// A power of two makes the re-encoding a shift of the exponent, exact but for
+// codes that fall among e4m3's subnormals, so a block that grows token by
+// token loses nothing to its history that one write would have kept.
+//
+// Bound: memory.  A row is read once and written once; the arithmetic is an
+// eighth of an instruction a byte.  Layout: half-warps hold a 128-dim head
+// (16 bytes a lane).  With block scales a CTA holds a run's keys and values
+// of one KV head in registers between the maximum and the rounding (B / 8
+// tokens a half-warp), so they are read once.
+#include "kv_scale.cuh"
+#include "qsa_device.cuh"
+#include "qsa_kernels.h"
+#include "qsa_launch.cuh"
+#include "qsa_rope.cuh"
+
+namespace qsa {
+namespace {
+
+constexpr int kD = 128;
+constexpr int kThreads = 128;
+
+__device__ __forceinline__ RopeParams rope_of(const AppendParams& P) {
+  return RopeParams{P.cos_sin, P.max_pos, P.mrope, P.sec_h, P.sec_w, P.err};
+}
+
+__device__ __forceinline__ void load_pos(const AppendParams& P, int row, int64_t (&pos)[3]) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) pos[k] = P.positions[static_cast<long long>(row) * 3 + (P.mrope ? k : 0)];
+}
+
+__device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
+  x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x);
+  x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
+  x[4] = bf16_lo(v.z); x[5] = bf16_hi(v.z);
+  x[6] = bf16_lo(v.w); x[7] = bf16_hi(v.w);
+}
+
+__device__ __forceinline__ uint4 pack8_bf16(const float (&x)[8]) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                    pack_bf16x2(x[6], x[7]));
+}
+
+__device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float s) {
+  uint2 v;
+  v.x = static_cast<uint32_t>(f32x2_to_e4m3x2(x[0] * s, x[1] * s)) |
+        (static_cast<uint32_t>(f32x2_to_e4m3x2(x[2] * s, x[3] * s)) << 16);
+  v.y = static_cast<uint32_t>(f32x2_to_e4m3x2(x[4] * s, x[5] * s)) |
+        (static_cast<uint32_t>(f32x2_to_e4m3x2(x[6] * s, x[7] * s)) << 16);
+  return v;
+}
+
+__device__ __forceinline__ void load_gain(const uint16_t* w, int lane16, float (&g)[8]) {
+  load8_bf16(w + 8 * lane16, g);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) g[e] += 1.0f;
+}
+
+// q = RoPE(GemmaRMSNorm(q)) and the gate of one row; the 8 half-warps take
+// its heads in turn.
+__device__ __forceinline__ void query_row(const AppendParams& P, int row, const float (&g)[8]) {
+  const int hw = threadIdx.x >> 4, lane16 = threadIdx.x & 15;
+  const uint16_t* x = P.qkv + static_cast<long long>(row) * (2 * P.hq + 2 * P.hkv) * kD;
+  int64_t pos[3];
+  load_pos(P, row, pos);
+  float c[8], s[8];
+  rope_coeffs(rope_of(P), lane16, pos, c, s);
+  for (int base = 0; base < P.hq; base += 8) {  // (the norm's shuffles span the warp)
+    const int h = base + hw;
+    const bool act = h < P.hq;
+    float xq[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    uint4 gv = make_uint4(0u, 0u, 0u, 0u);
+    if (act) {
+      load8_bf16(x + (2 * h) * kD + 8 * lane16, xq);
+      gv = *reinterpret_cast<const uint4*>(x + (2 * h + 1) * kD + 8 * lane16);
+    }
+    norm_rope(xq, g, P.eps, lane16, c, s);
+    if (act) {
+      const long long o = (static_cast<long long>(row) * P.hq + h) * kD + 8 * lane16;
+      *reinterpret_cast<uint4*>(P.q_out + o) = pack8_bf16(xq);
+      *reinterpret_cast<uint4*>(P.gate_out + o) = gv;
+    }
+  }
+}
+
+// K and V rows of a bf16 or statically scaled cache: one row, all KV heads.
+__device__ __forceinline__ void plain_kv_row(const AppendParams& P, int row) {
+  const int hw = threadIdx.x >> 4, lane16 = threadIdx.x & 15;
+  const long long slot = P.slots[row];
+  if (slot < 0) return;
+  const long long blk = slot / P.page, off = slot - blk * P.page;
+  if (blk >= P.num_blocks) {
+    if (threadIdx.x == 0) flag_error(P.err);
+    return;
+  }
+  const uint16_t* x = P.qkv + (static_cast<long long>(row) * (2 * P.hq + 2 * P.hkv) + 2 * P.hq) * kD;
+  int64_t pos[3];
+  load_pos(P, row, pos);
+  float c[8], s[8], g[8];
+  rope_coeffs(rope_of(P), lane16, pos, c, s);
+  load_gain(P.k_norm_w, lane16, g);
+  for (int base = 0; base < P.hkv; base += 8) {
+    const int h = base + hw;
+    const bool act = h < P.hkv;
+    float xk[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    uint4 vv = make_uint4(0u, 0u, 0u, 0u);
+    if (act) {
+      load8_bf16(x + h * kD + 8 * lane16, xk);
+      vv = *reinterpret_cast<const uint4*>(x + (P.hkv + h) * kD + 8 * lane16);
+    }
+    norm_rope(xk, g, P.eps, lane16, c, s);
+    if (!act) continue;
+    const long long r = (blk * P.hkv + h) * P.page + off;
+    if (P.kv_dtype == QSA_DTYPE_BF16) {
+      uint16_t* dst = static_cast<uint16_t*>(P.kv) + r * 256;
+      *reinterpret_cast<uint4*>(dst + 8 * lane16) = pack8_bf16(xk);
+      *reinterpret_cast<uint4*>(dst + 128 + 8 * lane16) = vv;
+    } else {
+      uint8_t* dst = static_cast<uint8_t*>(P.kv) + r * 256;
+      float xv[8];
+      unpack8(vv, xv);
+      *reinterpret_cast<uint2*>(dst + 8 * lane16) = pack8_e4m3(xk, 1.0f / P.k_scale);
+      *reinterpret_cast<uint2*>(dst + 128 + 8 * lane16) = pack8_e4m3(xv, 1.0f / P.v_scale);
+    }
+  }
+}
+
+// Whether row i + 1 goes on with row i's run.
+__device__ __forceinline__ bool goes_on(const AppendParams& P, int i) {
+  if (i < 0 || i + 1 >= P.rows) return false;
+  const long long a = P.slots[i], b = P.slots[i + 1];
+  return a >= 0 && b > a && a / P.scale_block == b / P.scale_block;
+}
+
+// The run that begins at row i, one KV head, into a cache with block scales.
+// NT: tokens of a block per half-warp (B / 8).
+template <int NT>
+__device__ __forceinline__ void scaled_run(const AppendParams& P, int i, int h, const float (&g)[8]) {
+  __shared__ float s_peak[8][2];
+  const int hw = threadIdx.x >> 4, lane16 = threadIdx.x & 15, lane = threadIdx.x & 31;
+  constexpr int B = 8 * NT;
+  const long long slot = P.slots[i];
+  const long long blk = slot / P.page;
+  // a row that repeats its predecessor's place or steps back inside one
+  // block would race with that run
+  const bool back = i > 0 && P.slots[i - 1] >= slot && P.slots[i - 1] / B == slot / B;
+  if (blk >= P.num_blocks || back) {
+    if (h == 0 && threadIdx.x == 0) flag_error(P.err);
+    return;
+  }
+  // the run's length: every warp looks at all B rows
+  int m = 0;
+#pragma unroll
+  for (int w = 0; w < (B + 31) / 32; ++w) {
+    const unsigned on = __ballot_sync(0xffffffffu, goes_on(P, i + 32 * w + lane));
+    if (m == 32 * w) m += on == 0xffffffffu ? 32 : __ffs(~on) - 1;
+  }
+  m = min(m + 1, B);
+  const int off = static_cast<int>(slot - blk * P.page), f = off % B;
+  const long long row0 = (blk * P.hkv + h) * P.page + off;
+  uint8_t* sc = static_cast<uint8_t*>(P.scales) + 2 * ((row0 - f) / B);
+  uint8_t* kv = static_cast<uint8_t*>(P.kv);
+  const int ek_old = scale_exp(sc[0]), ev_old = scale_exp(sc[1]);
+
+  float k[NT][8];
+  uint4 v[NT];
+  float pk = 0.f, pv = 0.f;
+#pragma unroll
+  for (int u = 0; u < NT; ++u) {
+    const int j = hw + 8 * u;
+    if (8 * u >= m) continue;  // (the same for the whole CTA)
+    const int row = i + min(j, m - 1);
+    const uint16_t* x = P.qkv + (static_cast<long long>(row) * (2 * P.hq + 2 * P.hkv) + 2 * P.hq + h) * kD;
+    int64_t pos[3];
+    load_pos(P, row, pos);
+    load8_bf16(x + 8 * lane16, k[u]);
+    v[u] = *reinterpret_cast<const uint4*>(x + P.hkv * kD + 8 * lane16);
+    float c[8], s[8], xv[8];
+    rope_coeffs(rope_of(P), lane16, pos, c, s);
+    norm_rope(k[u], g, P.eps, lane16, c, s);
+    unpack8(v[u], xv);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      pk = fmaxf(pk, finite_abs(k[u][e]));
+      pv = fmaxf(pv, finite_abs(xv[e]));
+    }
+  }
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) {
+    pk = fmaxf(pk, __shfl_xor_sync(0xffffffffu, pk, o));
+    pv = fmaxf(pv, __shfl_xor_sync(0xffffffffu, pv, o));
+  }
+  __syncthreads();  // the previous run's peaks are read
+  if (lane16 == 0) {
+    s_peak[hw][0] = pk;
+    s_peak[hw][1] = pv;
+  }
+  __syncthreads();  // (also: every thread has read the old scales)
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    pk = fmaxf(pk, s_peak[w][0]);
+    pv = fmaxf(pv, s_peak[w][1]);
+  }
+  int ek = scale_exp_for(pk), ev = scale_exp_for(pv);
+  if (f > 0) {
+    ek = max(ek, ek_old);
+    ev = max(ev, ev_old);
+    if (ek > ek_old || ev > ev_old) {  // the block's earlier tokens, 16 codes a thread
+      const float fk = exp2i(ek_old - ek), fv = exp2i(ev_old - ev);
+      for (int c = threadIdx.x; c < f * 16; c += kThreads) {
+        uint4* p = reinterpret_cast<uint4*>(kv + (row0 - f) * 256) + c;
+        *p = rescale16((c & 15) < 8 ? fk : fv, *p);
+      }
+    }
+  }
+  if (threadIdx.x == 0) {
+    sc[0] = static_cast<uint8_t>(ek + 127);
+    sc[1] = static_cast<uint8_t>(ev + 127);
+  }
+  const float sk = exp2i(-ek), sv = exp2i(-ev);
+#pragma unroll
+  for (int u = 0; u < NT; ++u) {
+    const int j = hw + 8 * u;
+    if (j >= m) continue;
+    // (ascending slots inside the block, not necessarily adjacent)
+    const long long r = row0 + (P.slots[i + j] - slot);
+    float xv[8];
+    unpack8(v[u], xv);
+    *reinterpret_cast<uint2*>(kv + r * 256 + 8 * lane16) = pack8_e4m3(k[u], sk);
+    *reinterpret_cast<uint2*>(kv + r * 256 + 128 + 8 * lane16) = pack8_e4m3(xv, sv);
+  }
+}
+
+// CTAs [0, kv_ctas) write K and V: with block scales CTA (c, h) the runs of
+// KV head h that begin in rows [c * chunk, (c + 1) * chunk), otherwise CTA c
+// those rows.  The others prepare queries, row by row.
+// NT: B / 8 with block scales, 0 without.
+template <int NT>
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams P) {
+  const int lane16 = threadIdx.x & 15;
+  int cta = blockIdx.x;
+  if (cta < P.kv_ctas) {
+    const int h = NT > 0 ? cta % P.hkv : 0;
+    const int i0 = (NT > 0 ? cta / P.hkv : cta) * P.chunk;
+    const int i1 = min(i0 + P.chunk, P.rows);
+    if constexpr (NT > 0) {
+      float g[8];
+      load_gain(P.k_norm_w, lane16, g);
+      for (int i = i0; i < i1; ++i)
+        if (P.slots[i] >= 0 && !goes_on(P, i - 1)) scaled_run<NT>(P, i, h, g);
+    } else {
+      for (int i = i0; i < i1; ++i) plain_kv_row(P, i);
+    }
+    return;
+  }
+  cta -= P.kv_ctas;
+  float g[8];
+  load_gain(P.q_norm_w, lane16, g);
+  for (int row = cta; row < P.rows; row += P.q_ctas) query_row(P, row, g);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(AppendParams p, cudaStream_t stream) {
+  if (p.rows == 0) return cudaSuccess;
+  const bool scaled = p.kv_dtype == QSA_DTYPE_E4M3_BLOCK;
+  p.chunk = scaled && p.rows >= 1024 ? p.scale_block : 1;
+  const int chunks = (p.rows + p.chunk - 1) / p.chunk;
+  p.kv_ctas = scaled ? chunks * p.hkv : chunks;
+  p.q_ctas = p.q_out != nullptr ? p.rows : 0;
+  const dim3 grid(p.kv_ctas + p.q_ctas);
+  switch (scaled ? p.scale_block : 0) {
+    case 0: return launch_kernel(append_kernel<0>, grid, dim3(kThreads), 0, stream, false, p);
+    case 16: return launch_kernel(append_kernel<2>, grid, dim3(kThreads), 0, stream, false, p);
+    case 32: return launch_kernel(append_kernel<4>, grid, dim3(kThreads), 0, stream, false, p);
+    case 64: return launch_kernel(append_kernel<8>, grid, dim3(kThreads), 0, stream, false, p);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace qsa

@@ -12,7 +12,9 @@ namespace qsa {
 
 // Defined in abi.cu, shared by the entry points of other files.
 int sm_count();                                // multiprocessors of the current device
-qsa_status check_gcfg(const qsa_gqa_cfg* g);   // main-attention configuration checks
+// Main-attention configuration checks.  block_scales: QSA_DTYPE_E4M3_BLOCK is
+// accepted too (entry points that take the scales).
+qsa_status check_gcfg(const qsa_gqa_cfg* g, bool block_scales = false);
 unsigned long long* internal_error_word();     // device error word of the current device
 
 struct CompressParams {
@@ -130,6 +132,48 @@ int gqa_num_splits(int rows, int hkv, int packed_width, int sms);
 // of the same step already did).
 cudaError_t launch_sparse_gqa(const GqaParams& p, cudaStream_t stream, bool pdl,
                               bool zero_tickets = true);
+
+// Attention of single rows: over the packed selection (packed != null) or
+// over the last `window` tokens and the first `sinks`.
+struct RowGqaParams {
+  const uint16_t* q;       // [rows, Hq, 128]
+  const void* kv;          // [blocks, Hkv, page, 256] in kv_dtype
+  const uint8_t* scales;   // [blocks, Hkv, page / scale_block, 2] (block scales)
+  const int32_t* block_table;
+  const int32_t* packed;
+  const int32_t* token_to_req;
+  const int32_t* qsl;      // window only: rows outside their request are left
+  const int32_t* logical;  // window only
+  const uint16_t* gate;    // nullable
+  uint16_t* out;
+  int bt_stride, packed_width;
+  int rows, reqs, hq, hkv, group, page, num_blocks, scale_block;
+  int kv_dtype;
+  float k_scale, v_scale;
+  int window, sinks;
+  unsigned long long* err;
+};
+cudaError_t launch_row_gqa(const RowGqaParams& p, cudaStream_t stream);
+
+// Keys and values into the paged cache, q and gate beside them.
+struct AppendParams {
+  const uint16_t* qkv;      // [rows, (2 Hq + 2 Hkv) * 128]
+  const uint16_t* q_norm_w;
+  const uint16_t* k_norm_w;
+  uint16_t* q_out;          // [rows, Hq, 128], null: K and V only
+  uint16_t* gate_out;
+  void* kv;                 // [blocks, Hkv, page, 256] in kv_dtype
+  void* scales;             // [blocks, Hkv, page / scale_block, 2] (block scales)
+  const int64_t* slots;     // [rows] block * page + offset, < 0: no write
+  const int64_t* positions; // [rows, 3]
+  const float* cos_sin;     // [max_pos, 64]
+  int rows, hq, hkv, page, num_blocks, scale_block, kv_dtype;
+  int max_pos, mrope, sec_h, sec_w;
+  float eps, k_scale, v_scale;
+  int chunk, kv_ctas, q_ctas;  // set by the launch: rows per K/V CTA, CTAs of each kind
+  unsigned long long* err;
+};
+cudaError_t launch_kv_append(AppendParams p, cudaStream_t stream);
 
 // The fused projection GEMM: y = x . w^T (bf16 in, fp32 accumulate, bf16
 // out), output columns routed to the main qkv rows, then the indexer's query

@@ -21,6 +21,7 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "shape", 3: "dtype", 4: "unsupporte
           5: "workspace", 6: "cuda", 7: "device fault"}
 DTYPE_BF16 = 0
 DTYPE_E4M3 = 1
+DTYPE_E4M3_BLOCK = 2  # KV cache only: e4m3 codes with block scales (kv_scales)
 
 _c_int = ctypes.c_int32
 _p = ctypes.c_void_p
@@ -62,6 +63,17 @@ class QsaStepArgs(ctypes.Structure):
                 ("main", _p)]
 
 
+class QsaKvScales(ctypes.Structure):
+    _fields_ = [("scales", _p), ("scale_block", _c_int)]
+
+
+class QsaWindowArgs(ctypes.Structure):
+    _fields_ = [("rows", _c_int), ("reqs", _c_int), ("window", _c_int), ("sinks", _c_int),
+                ("max_context", _c_int), ("bt_stride", _c_int), ("q", _p), ("kv", _p),
+                ("scales", _p), ("block_table", _p), ("token_to_req", _p),
+                ("query_start_loc", _p), ("logical_positions", _p), ("gate", _p), ("out", _p)]
+
+
 _LIB = None
 
 
@@ -95,12 +107,17 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "qsa_version": [],
         "qsa_step_launches": [P, P, I, I, I],
         "qsa_gqa_splits": [P, I, I],
+        "qsa_kv_append": [P, P, P, P, P, P, I, P],
+        "qsa_sparse_gqa_scaled": [P, P, P, P, P, I, P, I, P, P, P, I, I, P, Z, P],
+        "qsa_window_gqa": [P, P, P, Z, P],
+        "qsa_window_workspace_bytes": [P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
         f.argtypes = args
         f.restype = ctypes.c_int
     lib.qsa_workspace_bytes.restype = ctypes.c_size_t
+    lib.qsa_window_workspace_bytes.restype = ctypes.c_size_t
     lib.qsa_status_string.restype = ctypes.c_char_p
     lib.qsa_version.restype = ctypes.c_char_p
     _LIB = lib
@@ -231,14 +248,15 @@ def workspace_bytes(cfg, gcfg, rows, reqs, max_visible) -> int:
 def main_prep(t: dict, eps: float = 1e-6) -> QsaMainPrep:
     """The main-attention prepare's argument struct from named CUDA tensors
     (main_qkv, main_q_norm_w, main_k_norm_w, main_q_out, main_gate_out, kv,
-    slot_mapping) and the norms' epsilon."""
+    slot_mapping) and the norms' epsilon.  Without main_q_out and
+    main_gate_out (and then main_q_norm_w) it is kv_append's K and V alone."""
     m = QsaMainPrep()
     m.qkv = _ptr(t["main_qkv"], torch.bfloat16, "main_qkv")
-    m.q_norm_w = _ptr(t["main_q_norm_w"], torch.bfloat16)
+    m.q_norm_w = _ptr(t.get("main_q_norm_w"), torch.bfloat16)
     m.k_norm_w = _ptr(t["main_k_norm_w"], torch.bfloat16)
     m.eps = float(eps)
-    m.q_out = _ptr(t["main_q_out"], torch.bfloat16, "main_q_out")
-    m.gate_out = _ptr(t["main_gate_out"], torch.bfloat16, "main_gate_out")
+    m.q_out = _ptr(t.get("main_q_out"), torch.bfloat16, "main_q_out")
+    m.gate_out = _ptr(t.get("main_gate_out"), torch.bfloat16, "main_gate_out")
     m.kv = _ptr(t["kv"], _IDX)
     m.slot_mapping = _ptr(t["slot_mapping"], torch.int64, "slot_mapping")
     m._tensors = dict(t)
@@ -325,6 +343,106 @@ def qkv_index_proj(x, w, qkv_out, index_q_out, index_k_out, stream=None):
         _ptr(qkv_out, torch.bfloat16), _ptr(index_q_out, torch.bfloat16),
         _ptr(index_k_out, torch.bfloat16), _stream(stream))
     _check("qsa_qkv_index_proj", st)
+
+
+def kv_scales(scales, scale_block: int) -> QsaKvScales:
+    """The block scales of an e4m3 KV cache: uint8 [num_blocks, Hkv, page /
+    scale_block, 2] (K, V), byte b standing for 2^(b - 127)."""
+    s = QsaKvScales()
+    s.scales = _ptr(scales, torch.uint8, "scales")
+    s.scale_block = scale_block
+    s._tensors = scales
+    return s
+
+
+def _scales_fit(gcfg, scales):
+    """A scales tensor that is smaller than the cache's would be read past its end."""
+    if scales is None or scales.scale_block <= 0:
+        return
+    need = gcfg.num_blocks * gcfg.num_kv_heads * (gcfg.page_size // scales.scale_block) * 2
+    if scales._tensors.numel() < need:
+        raise ValueError(f"scales has {scales._tensors.numel()} entries, the cache needs {need}")
+
+
+def _same_device(*tensors):
+    """The device all tensors are on (None ones left out)."""
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+    return devs.pop()
+
+
+def kv_append(cfg, gcfg, m: QsaMainPrep, positions, cos_sin, scales: QsaKvScales | None = None,
+              stream=None):
+    """Keys and values into the paged cache, normalised and rotated on the way,
+    with q and gate beside them where `m` has them (qsa_kv_append)."""
+    _scales_fit(gcfg, scales)
+    with torch.cuda.device(_same_device(positions, cos_sin, m._tensors["kv"])):
+        st = load().qsa_kv_append(
+            ctypes.byref(cfg), ctypes.byref(gcfg), ctypes.byref(m),
+            None if scales is None else ctypes.byref(scales), _ptr(positions, torch.int64),
+            _ptr(cos_sin, torch.float32), positions.shape[0], _stream(stream))
+    _check("qsa_kv_append", st)
+
+
+def sparse_gqa_scaled(gcfg, scales: QsaKvScales, q, kv, block_table, packed, token_to_req, gate,
+                      out, ws, stream=None):
+    """Stage 4 over a cache with block scales (qsa_sparse_gqa_scaled)."""
+    _scales_fit(gcfg, scales)
+    with torch.cuda.device(_same_device(q, kv, block_table, packed, token_to_req, gate, out, ws)):
+        st = load().qsa_sparse_gqa_scaled(
+            ctypes.byref(gcfg), ctypes.byref(scales), _ptr(q, torch.bfloat16),
+            _ptr(kv, torch.uint8), _ptr(block_table, torch.int32), block_table.shape[1],
+            _ptr(packed, torch.int32), packed.shape[1], _ptr(token_to_req, torch.int32),
+            _ptr(gate, torch.bfloat16), _ptr(out, torch.bfloat16), q.shape[0],
+            block_table.shape[0], _ptr(ws, torch.uint8), 0 if ws is None else ws.numel(),
+            _stream(stream))
+    _check("qsa_sparse_gqa_scaled", st)
+
+
+def window_args(q, kv, block_table, token_to_req, query_start_loc, logical_positions, out, window,
+                sinks, max_context, gate=None, scales: QsaKvScales | None = None) -> QsaWindowArgs:
+    """The argument struct of window_gqa: q and out [rows, Hq, D], the cache
+    and its table, the rows' requests and positions, the window and the number
+    of first tokens that stay visible."""
+    a = QsaWindowArgs()
+    a._device = _same_device(q, kv, block_table, token_to_req, query_start_loc, logical_positions,
+                             out, gate, None if scales is None else scales._tensors)
+    a.rows, a.reqs = q.shape[0], query_start_loc.shape[0] - 1
+    if out.shape != q.shape or (gate is not None and gate.shape != q.shape):
+        raise ValueError("out and gate must have q's shape")
+    if token_to_req.shape[0] < a.rows or logical_positions.shape[0] < a.rows:
+        raise ValueError("token_to_req and logical_positions must cover the rows of q")
+    if block_table.shape[0] < a.reqs:
+        raise ValueError("block_table must have a row for each request")
+    a.window, a.sinks, a.max_context = window, sinks, max_context
+    a.bt_stride = block_table.shape[1]
+    a.q = _ptr(q, torch.bfloat16, "q")
+    a.kv = _ptr(kv, _IDX, "kv")
+    a.scales = None if scales is None else ctypes.addressof(scales)
+    a.block_table = _ptr(block_table, torch.int32, "block_table")
+    a.token_to_req = _ptr(token_to_req, torch.int32, "token_to_req")
+    a.query_start_loc = _ptr(query_start_loc, torch.int32, "query_start_loc")
+    a.logical_positions = _ptr(logical_positions, torch.int32, "logical_positions")
+    a.gate = _ptr(gate, torch.bfloat16, "gate")
+    a.out = _ptr(out, torch.bfloat16, "out")
+    a._tensors = (q, kv, block_table, token_to_req, query_start_loc, logical_positions, gate, out)
+    a._scales = scales
+    return a
+
+
+def window_workspace_bytes(gcfg, args: QsaWindowArgs) -> int:
+    return int(load().qsa_window_workspace_bytes(ctypes.byref(gcfg), ctypes.byref(args)))
+
+
+def window_gqa(gcfg, args: QsaWindowArgs, ws=None, stream=None):
+    """Attention over the last `window` tokens and the first `sinks`
+    (qsa_window_gqa); ws: uint8, window_workspace_bytes() long."""
+    _scales_fit(gcfg, args._scales)
+    with torch.cuda.device(args._device):
+        st = load().qsa_window_gqa(ctypes.byref(gcfg), ctypes.byref(args), _ptr(ws, torch.uint8),
+                                   0 if ws is None else ws.numel(), _stream(stream))
+    _check("qsa_window_gqa", st)
 
 
 def step_launches(cfg, gcfg, rows, reqs, skip_topk=False) -> int:

@@ -625,3 +625,84 @@ def layer_step(cfg: QsaConfig, *, projected_q, raw_keys, positions, cos_sin,
         out[row] = sparse_gqa_row(q[row], kv, block_table[req], packed[row, :n], page,
                                   None if gate is None else gate[row], k_scale, v_scale)
     return q_idx, packed, out
+
+
+# --------------------------------------------------------------------------
+# KV cache with block scales, window attention
+
+SCALE_EXP_MAX = 40
+
+
+def scale_exponent(peak: float) -> int:
+    """Smallest e in [-40, 40] with peak <= 448 * 2^e."""
+    e = -SCALE_EXP_MAX
+    while e < SCALE_EXP_MAX and peak > 448.0 * 2.0 ** e:
+        e += 1
+    return e
+
+
+def scale_value(byte) -> np.ndarray:
+    """What a scale byte stands for: 2^(b - 127), held within 2^+-40."""
+    e = np.asarray(byte, dtype=np.int64) - 127
+    return 2.0 ** np.clip(e, -SCALE_EXP_MAX, SCALE_EXP_MAX).astype(np.float64)
+
+
+def dequantise_block_kv(codes, scales, scale_block: int) -> np.ndarray:
+    """[blocks, Hkv, page, 2D] codes and [blocks, Hkv, page / B, 2] scale
+    bytes -> float64 values."""
+    x = e4m3_decode(codes)
+    s = np.repeat(scale_value(scales), scale_block, axis=2)  # [blocks, Hkv, page, 2]
+    return x * np.repeat(s, x.shape[-1] // 2, axis=3)
+
+
+def append_runs(slots, scale_block: int) -> list:
+    """[(first row, rows)] of the runs of consecutive rows whose slots ascend
+    inside one scale block; rows without a slot are in none, and neither are
+    rows that repeat or step back inside their predecessor's block."""
+    runs, i, n = [], 0, len(slots)
+    while i < n:
+        s = int(slots[i])
+        j = i + 1
+        while j < n and s >= 0 and int(slots[j]) > int(slots[j - 1]) and int(slots[j]) // scale_block == s // scale_block:
+            j += 1
+        back = i > 0 and int(slots[i - 1]) >= s and int(slots[i - 1]) // scale_block == s // scale_block
+        if s >= 0 and not back:
+            runs.append((i, j - i))
+        i = j
+    return runs
+
+
+def append_block_kv(codes, scales, slots, k, v, page: int, scale_block: int) -> None:
+    """Rows k, v [rows, Hkv, D] (float64, normalised and rotated) into codes
+    (uint8) and scales (uint8), in place; slots must lie in the cache."""
+    D = k.shape[-1]
+    for i, m in append_runs(slots, scale_block):
+        blk, off = int(slots[i]) // page, int(slots[i]) % page
+        sub, f = off // scale_block, off % scale_block
+        base = off - f
+        for h in range(k.shape[1]):
+            for which, x in enumerate((k, v)):
+                col = slice(which * D, (which + 1) * D)
+                val = x[i:i + m, h]
+                fin = np.abs(val[np.isfinite(val)])
+                e = scale_exponent(float(fin.max(initial=0.0)))
+                if f > 0:
+                    old = int(np.clip(int(scales[blk, h, sub, which]) - 127, -SCALE_EXP_MAX, SCALE_EXP_MAX))
+                    e = max(e, old)
+                    if e > old:
+                        past = e4m3_decode(codes[blk, h, base:off, col])
+                        nan = np.isnan(past)
+                        c = e4m3_encode(np.where(nan, 0.0, past) * 2.0 ** (old - e))
+                        codes[blk, h, base:off, col] = np.where(nan, 0x7F, c)
+                scales[blk, h, sub, which] = e + 127
+                for j in range(m):
+                    o = int(slots[i + j]) % page
+                    nan = np.isnan(val[j])
+                    c = e4m3_encode(np.where(nan, 0.0, val[j]) * 2.0 ** -e)
+                    codes[blk, h, o, col] = np.where(nan, 0x7F, c)
+
+
+def window_tokens(p: int, window: int, sinks: int) -> np.ndarray:
+    """Tokens that a row at position p sees, ascending."""
+    t = np.arange(p + 1)
+    return t[(t > p - window) | (t < sinks)]
