@@ -159,7 +159,19 @@ GqaLayout gqa_layout(const qsa_gqa_cfg* g, int rows, int packed_width) {
   return L;
 }
 
+// Split partials of the row attention: fp32 outputs, then log-sum-exps.
+size_t row_partial_bytes(const qsa_gqa_cfg* g, int rows, int splits) {
+  return align256(static_cast<size_t>(splits) * rows * g->num_q_heads * 128 * sizeof(float));
+}
+size_t row_ws_bytes(const qsa_gqa_cfg* g, int rows, int splits) {
+  if (splits <= 1) return 0;
+  return row_partial_bytes(g, rows, splits) +
+         align256(static_cast<size_t>(splits) * rows * g->num_q_heads * sizeof(float));
+}
+
 size_t gqa_ws_bytes(const qsa_gqa_cfg* g, int rows, int packed_width) {
+  if (g->kv_dtype == QSA_DTYPE_E4M3_BLOCK)
+    return row_ws_bytes(g, rows, row_gqa_splits(rows, g->num_kv_heads, packed_width - 1, g->kv_dtype, sm_count()));
   return gqa_layout(g, rows, packed_width).total;
 }
 
@@ -588,6 +600,17 @@ qsa_status fill_row_gqa(RowGqaParams* p, const qsa_gqa_cfg* g, const qsa_kv_scal
   return p->err != nullptr ? QSA_OK : QSA_ERR_CUDA;
 }
 
+// The split of the rows and its partials in ws.
+qsa_status place_splits(RowGqaParams* p, const qsa_gqa_cfg* g, int splits, void* ws, size_t ws_bytes) {
+  p->splits = splits;
+  const size_t need = row_ws_bytes(g, p->rows, splits);
+  if (need == 0) return QSA_OK;
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < need) return QSA_ERR_WORKSPACE;
+  p->part_o = static_cast<float*>(ws);
+  p->part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + row_partial_bytes(g, p->rows, splits));
+  return QSA_OK;
+}
+
 qsa_status do_sparse_scaled(const qsa_gqa_cfg* g, const qsa_kv_scales* scales, const void* q,
                             const void* kv, const int32_t* block_table, int32_t bt_stride,
                             const int32_t* packed, int32_t packed_width,
@@ -600,13 +623,13 @@ qsa_status do_sparse_scaled(const qsa_gqa_cfg* g, const qsa_kv_scales* scales, c
   if (rows == 0) return QSA_OK;
   if (packed_width < 2) return QSA_ERR_SHAPE;
   if (packed == nullptr) return QSA_ERR_INVALID_ARG;
-  (void)ws;
-  (void)ws_bytes;
   RowGqaParams p{};
   st = fill_row_gqa(&p, g, scales, q, kv, block_table, bt_stride, token_to_req, gate, out, rows, reqs);
   if (st != QSA_OK) return st;
   p.packed = packed;
   p.packed_width = packed_width;
+  st = place_splits(&p, g, row_gqa_splits(rows, p.hkv, packed_width - 1, p.kv_dtype, sm_count()), ws, ws_bytes);
+  if (st != QSA_OK) return st;
   return cuda_status(launch_row_gqa(p, stream));
 }
 
@@ -620,13 +643,21 @@ qsa_status check_window(const qsa_gqa_cfg* g, const qsa_window_args* a) {
   return QSA_OK;
 }
 
+// Tokens that a row sees at the most.
+long long window_tokens(const qsa_window_args* a) {
+  const long long n = static_cast<long long>(a->window) + a->sinks;
+  return n < a->max_context ? n : a->max_context;
+}
+
+int window_splits(const qsa_gqa_cfg* g, const qsa_window_args* a) {
+  return row_gqa_splits(a->rows, g->num_kv_heads, window_tokens(a), g->kv_dtype, sm_count());
+}
+
 qsa_status do_window(const qsa_gqa_cfg* g, const qsa_window_args* a, void* ws, size_t ws_bytes,
                      cudaStream_t stream) {
   qsa_status st = check_window(g, a);
   if (st != QSA_OK || a->rows == 0) return st;
   if (!a->query_start_loc || !a->logical_positions) return QSA_ERR_INVALID_ARG;
-  (void)ws;
-  (void)ws_bytes;
   RowGqaParams p{};
   st = fill_row_gqa(&p, g, a->scales, a->q, a->kv, a->block_table, a->bt_stride, a->token_to_req,
                     a->gate, a->out, a->rows, a->reqs);
@@ -635,6 +666,8 @@ qsa_status do_window(const qsa_gqa_cfg* g, const qsa_window_args* a, void* ws, s
   p.logical = a->logical_positions;
   p.window = a->window;
   p.sinks = a->sinks;
+  st = place_splits(&p, g, window_splits(g, a), ws, ws_bytes);
+  if (st != QSA_OK) return st;
   return cuda_status(launch_row_gqa(p, stream));
 }
 
@@ -911,8 +944,8 @@ qsa_status qsa_window_gqa(const qsa_gqa_cfg* gcfg, const qsa_window_args* args, 
 }
 
 size_t qsa_window_workspace_bytes(const qsa_gqa_cfg* gcfg, const qsa_window_args* args) {
-  if (check_window(gcfg, args) != QSA_OK) return 0;
-  return 0;
+  if (check_window(gcfg, args) != QSA_OK || args->rows == 0) return 0;
+  return row_ws_bytes(gcfg, args->rows, window_splits(gcfg, args));
 }
 
 qsa_status qsa_mtp_steps(const qsa_cfg* cfg, const qsa_gqa_cfg* gcfg, const qsa_step_args* steps,

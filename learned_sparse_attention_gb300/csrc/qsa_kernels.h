@@ -151,8 +151,14 @@ struct RowGqaParams {
   int kv_dtype;
   float k_scale, v_scale;
   int window, sinks;
+  int splits;
+  float* part_o;           // [splits, rows, Hq, 128] (splits > 1)
+  float* part_lse;         // [splits, rows, Hq]
   unsigned long long* err;
 };
+// Splits of rows of up to max_tokens tokens on a device with `sms`
+// multiprocessors.
+int row_gqa_splits(int rows, int hkv, long long max_tokens, int kv_dtype, int sms);
 cudaError_t launch_row_gqa(const RowGqaParams& p, cudaStream_t stream);
 
 // Keys and values into the paged cache, q and gate beside them.

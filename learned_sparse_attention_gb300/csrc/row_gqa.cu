@@ -1,16 +1,32 @@
 // Attention of single rows over the paged KV cache: the packed selection over
-// a cache with block scales (qsa_sparse_gqa_scaled) and window attention
-// (qsa_window_gqa).
+// a cache with block scales (qsa_sparse_gqa_scaled) and window attention of
+// few rows per request (qsa_window_gqa).
 //
-// Mathematics.  For row i and query head h of KV head h / G:
-//   s_t = (q . k_t) * D^-1/2 * ks_t,  out = sum_t softmax(s)_t vs_t v_t
-// over the row's tokens, ks_t / vs_t the scales of the token's block (or the
-// cache's static scales, or 1), zero when the row sees nothing; then
-// out = bf16(bf16(out) * sigmoid(gate)).  One pass over the tokens with the
-// running maximum and sum in fp32.
+// Mathematics.  For row i and query head h of KV head h / G, over the row's
+// tokens t with scales ks_t, vs_t (of the token's block, static, or 1):
+//   s_t = (q . k_t) * D^-1/2 * ks_t,   out = sum_t softmax(s)_t vs_t v_t,
+// zero when the row sees nothing, then out = bf16(bf16(out) * sigmoid(gate)).
+// One pass over the tokens.  The exponentials are taken against a reference m
+// that moves only when a score passes it by a margin; with block scales the
+// weight that meets v_t is p_t = 2^(s_t log2 e + log2 vs_t - m), and the sum
+// of the softmax adds p_t / vs_t, so neither scale costs a multiplication of
+// the K or V tile.
 //
-// One CTA per (row, KV head); warps take the tokens in turn, a lane four
-// dims of every head of the group; the warps are merged in shared memory.
+// 8-bit caches are multiplied as they are: the e4m3 codes are the B operand
+// of m16n8k32 MMAs, and q and p are each split into two e4m3 terms, x = hi +
+// lo / 32, whose 8 significant bits are those of a bf16 operand (q, a bf16
+// value, loses nothing).  The terms are the two halves of the MMA's 16 rows:
+// rows 0-7 the hi of up to 8 heads, rows 8-15 their lo.  So no code is ever
+// converted, and V is transposed by ldmatrix alone.
+//
+// Bound: HBM (256 or 512 contiguous bytes of each token and KV head).  One CTA
+// per (row, KV head, split), four warps, each with its own cp.async ring over
+// slabs of 16 (bf16) or 32 tokens; a warp finds its slabs' cache rows itself,
+// two slabs ahead of their copies, so the loop has no block barrier.  Both
+// products have the heads on M and the tokens (S = Q K^T) or dims (O = P V)
+// on N, so a lane's scores are the P fragment it needs next; for m16n8k32 that
+// takes K's rows in the order tau (below).  Splits leave fp32 partials that a
+// second kernel joins in a fixed order.
 #include "kv_scale.cuh"
 #include "qsa_device.cuh"
 #include "qsa_kernels.h"
@@ -21,14 +37,132 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr uint32_t kBadRow = 0xFFFFFFFFu;
+constexpr float kLog2e = 1.4426950408889634f;
 
-template <int GM, int KVT>
+// D(16x8 fp32) += A(16x32 e4m3, row) * B(32x8 e4m3, col)
+__device__ __forceinline__ void mma_e4m3_16832(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two 16x16 byte matrices, transposed: lanes 0-15 point at the rows of the
+// first, 16-31 of the second.  Lane (g, t) gets, of each, the four bytes of
+// rows 4t .. 4t+3 in column g (r[0], r[2]) and in column g + 8 (r[1], r[3]).
+__device__ __forceinline__ void ldmatrix_b8_trans(uint32_t (&r)[4], const void* p) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_addr(p)));
+}
+__device__ __forceinline__ uint16_t f16x2_to_e4m3x2(uint32_t v) {
+  uint16_t out;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(out) : "r"(v));
+  return out;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
+  uint32_t out;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(out) : "h"(v));
+  return out;
+}
+__device__ __forceinline__ float ex2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 4-byte asynchronous copy of src_bytes bytes, the rest zero.
+__device__ __forceinline__ void cp_async4(void* dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src),
+               "r"(src_bytes)
+               : "memory");
+}
+
+// x0, x1 (f16x2, at most 256) as two e4m3 terms, hi + lo / 32.
+__device__ __forceinline__ void split_e4m3x2(uint32_t x, uint16_t& hi, uint16_t& lo) {
+  hi = f16x2_to_e4m3x2(x);
+  const uint32_t back = e4m3x2_to_f16x2(hi);
+  const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&back)),
+                            __float2half2_rn(32.0f));
+  lo = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&r));
+}
+__device__ __forceinline__ uint32_t pack16(uint16_t a, uint16_t b) {
+  return static_cast<uint32_t>(a) | (static_cast<uint32_t>(b) << 16);
+}
+
+// Layout by cache type: KVT 0 bf16, 1 e4m3 with static scales, 2 e4m3 with
+// block scales.  TS: tokens of a slab.
+template <int KVT>
+struct RowPlan {
+  static constexpr bool kE4m3 = KVT != 0;
+  static constexpr int TS = kE4m3 ? 32 : 16;
+  static constexpr int kRowB = kE4m3 ? 128 : 256;     // bytes of a token's K (or V)
+  static constexpr int kSlab = TS * kRowB * 2;        // 8 KB: K rows, then V rows
+  static constexpr int kStages = 3;
+  // the margin by which a weight may pass the reference, and where a new
+  // reference puts the largest weight (log2): f16/e4m3 terms up to 2^8
+  static constexpr float kUp = 8.0f;
+  static constexpr float kTop = kE4m3 ? 4.0f : 0.0f;
+  static constexpr int kSmem = kWarps * kStages * kSlab;
+};
+
+// K rows are swizzled so that the 8 rows of one ldmatrix matrix (e4m3: rows
+// tau(nb, 0..7)) fall on different banks, V rows by their own 8 neighbours.
+template <int KVT>
+__device__ __forceinline__ int swz_k(int tok) {
+  return KVT == 0 ? tok & 7 : (tok & 1) | ((tok >> 1) & 6);
+}
+
+__device__ __forceinline__ bool row_live(const RowGqaParams& P, int row, int req) {
+  return req >= 0 && req < P.reqs && row >= P.qsl[req] && row < P.qsl[req + 1];
+}
+
+__device__ __forceinline__ float sigmoid_of(uint32_t bf16_bits) {
+  return 1.0f / (1.0f + __expf(-__uint_as_float(bf16_bits << 16)));
+}
+
+// out[8 dims] = bf16(bf16(x) * sigmoid(gate)), or bf16(x) without a gate.
+__device__ __forceinline__ void store_gated8(const RowGqaParams& P, long long at, const float (&x)[8], uint4 g) {
+  const uint32_t gv[4] = {g.x, g.y, g.z, g.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float a = bf16_round(x[2 * e]), b = bf16_round(x[2 * e + 1]);
+    if (P.gate != nullptr) {
+      a *= sigmoid_of(gv[e] & 0xFFFFu);
+      b *= sigmoid_of(gv[e] >> 16);
+    }
+    o[e] = pack_bf16x2(a, b);
+  }
+  *reinterpret_cast<uint4*>(P.out + at) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ uint4 load_gate(const RowGqaParams& P, long long at) {
+  return P.gate != nullptr ? *reinterpret_cast<const uint4*>(P.gate + at) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+// HB: blocks of 8 query heads (groups of 16: 2).  bf16 holds both on one M
+// of 16; e4m3 takes an M of 16 (hi and lo) for each.
+template <int KVT, int HB>
 __global__ void __launch_bounds__(kThreads) row_gqa_kernel(const RowGqaParams P) {
-  __shared__ float s_m[kWarps][GM], s_l[kWarps][GM];
-  __shared__ float s_o[kWarps][GM][128];
+  using RP = RowPlan<KVT>;
+  constexpr int TS = RP::TS, ST = RP::kStages;
+  constexpr int MB = RP::kE4m3 ? HB : 1;     // MMA row blocks
+  constexpr int NS = RP::kE4m3 ? 1 : HB;     // heads of a lane in each of them
+  constexpr int NBK = TS / 8;                // column blocks of S
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint32_t s_raw[kWarps][ST][KVT == 2 ? 32 : 1];  // scale words as copied
+  __shared__ float4 s_scl[kWarps][3][KVT == 2 ? 8 : 1];      // ks, log2 vs, 1 / vs of a slab
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kvh = blockIdx.x / P.rows, row = blockIdx.x % P.rows;
+  const int g = lane >> 2, t = lane & 3;
+  // KV-head-major order: rows of one request that share tokens meet in L2
+  const int kvh = static_cast<int>(blockIdx.x) / P.rows, row = static_cast<int>(blockIdx.x) % P.rows;
+  const int split = blockIdx.y;
+  const int G = P.group;
   const int req = P.token_to_req[row];
+  griddep_launch_dependents();
+
+  // ---- the row's tokens: entries of the packed row, or the sinks and the window
   int n, ns = 0, lo = 0;
   const int32_t* prow = nullptr;
   if (P.packed != nullptr) {
@@ -39,117 +173,484 @@ __global__ void __launch_bounds__(kThreads) row_gqa_kernel(const RowGqaParams P)
       n = 0;
     }
   } else {
-    if (req < 0 || req >= P.reqs || row < P.qsl[req] || row >= P.qsl[req + 1]) return;
+    if (!row_live(P, row, req)) return;
     const int p = P.logical[row];
     ns = min(P.sinks, p + 1);
     lo = max(ns, p - P.window + 1);
     n = p < 0 ? 0 : ns + max(0, p + 1 - lo);
   }
-  const int G = P.group;
-  float q[GM][4], o[GM][4], m[GM], l[GM];
-#pragma unroll
-  for (int h = 0; h < GM; ++h) {
-    m[h] = -INFINITY;
-    l[h] = 0.f;
-    const uint16_t* qh = P.q + (static_cast<long long>(row) * P.hq + kvh * G + min(h, G - 1)) * 128 + 4 * lane;
-    const uint2 v = *reinterpret_cast<const uint2*>(qh);
-    q[h][0] = bf16_lo(v.x); q[h][1] = bf16_hi(v.x); q[h][2] = bf16_lo(v.y); q[h][3] = bf16_hi(v.y);
-    o[h][0] = o[h][1] = o[h][2] = o[h][3] = 0.f;
-  }
+  const int nslab = (n + TS - 1) / TS;
+  const int per = (nslab + P.splits - 1) / P.splits;
+  const int sb = split * per, se = min(nslab, sb + per);
+  const int cnt = se > sb + warp ? (se - sb - warp + kWarps - 1) / kWarps : 0;  // slabs of this warp
+  const int32_t* bt_row = P.block_table + static_cast<long long>(n > 0 ? req : 0) * P.bt_stride;
+  const bool page_pow2 = (P.page & (P.page - 1)) == 0;
+  const int page_shift = __ffs(P.page) - 1;
+  // the tokens and pages of a warp's slab i: lane l < TS its l-th token
+  auto fetch_tok = [&](int i) -> int {
+    const int at = (sb + warp + kWarps * i) * TS + lane;
+    if (i >= cnt || lane >= TS || at >= n) return -1;
+    if (prow == nullptr) return at < ns ? at : lo + at - ns;
+    const int e = prow[at];
+    return e < 0 ? -2 : e;  // (-1: no token; -2: an entry that is none)
+  };
+  auto block_of = [&](int tok) { return page_pow2 ? tok >> page_shift : tok / P.page; };
+  auto fetch_page = [&](int tok) -> int {
+    if (tok < 0) return -1;
+    const int blk = block_of(tok);
+    return blk < P.bt_stride ? bt_row[blk] : -1;
+  };
   bool bad = false;
-  for (int i = warp; i < n; i += kWarps) {
-    const int t = prow != nullptr ? prow[i] : i < ns ? i : lo + i - ns;
-    const int blk = t < 0 ? -1 : t / P.page;
-    const int pid = blk >= 0 && blk < P.bt_stride ? P.block_table[static_cast<long long>(req) * P.bt_stride + blk] : -1;
-    if (pid < 0 || pid >= P.num_blocks) {
+  auto row_id = [&](int tok, int page) -> uint32_t {
+    if (tok == -1) return kBadRow;
+    if (tok < 0 || page < 0 || page >= P.num_blocks) {
       bad = true;
-      continue;
+      return kBadRow;
     }
-    const long long r = (static_cast<long long>(pid) * P.hkv + kvh) * P.page + t % P.page;
-    float k[4], v[4], ks = 1.f, vs = 1.f;
-    if (KVT == QSA_DTYPE_BF16) {
-      const uint16_t* x = static_cast<const uint16_t*>(P.kv) + r * 256 + 4 * lane;
-      const uint2 a = *reinterpret_cast<const uint2*>(x), b = *reinterpret_cast<const uint2*>(x + 128);
-      k[0] = bf16_lo(a.x); k[1] = bf16_hi(a.x); k[2] = bf16_lo(a.y); k[3] = bf16_hi(a.y);
-      v[0] = bf16_lo(b.x); v[1] = bf16_hi(b.x); v[2] = bf16_lo(b.y); v[3] = bf16_hi(b.y);
-    } else {
-      const uint8_t* x = static_cast<const uint8_t*>(P.kv) + r * 256 + 4 * lane;
-      uint32_t lo2, hi2;
-      e4m3x4_to_f16x2x2(*reinterpret_cast<const uint32_t*>(x), lo2, hi2);
-      float2 a = __half22float2(*reinterpret_cast<__half2*>(&lo2)), b = __half22float2(*reinterpret_cast<__half2*>(&hi2));
-      k[0] = a.x; k[1] = a.y; k[2] = b.x; k[3] = b.y;
-      e4m3x4_to_f16x2x2(*reinterpret_cast<const uint32_t*>(x + 128), lo2, hi2);
-      a = __half22float2(*reinterpret_cast<__half2*>(&lo2));
-      b = __half22float2(*reinterpret_cast<__half2*>(&hi2));
-      v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
-      if (KVT == QSA_DTYPE_E4M3) {
-        ks = P.k_scale;
-        vs = P.v_scale;
-      } else {
-        const uint8_t* sc = P.scales + 2 * (r / P.scale_block);
-        ks = exp2i(scale_exp(sc[0]));
-        vs = exp2i(scale_exp(sc[1]));
+    return (static_cast<uint32_t>(page) * P.hkv + kvh) * static_cast<uint32_t>(P.page) + (tok - block_of(tok) * P.page);
+  };
+  int tok[ST + 1], pg[ST];
+#pragma unroll
+  for (int i = 0; i <= ST; ++i) tok[i] = fetch_tok(i);
+
+  // ---- Q as A fragments: row g of block mb is head 8 mb + g; rows g + 8 are
+  // heads 8 .. 15 (bf16) or the lo terms of rows g (e4m3)
+  constexpr int KK = RP::kE4m3 ? 4 : 8;
+  uint32_t qa[MB][KK][4];
+  float qs[MB];  // e4m3: what a block's scores are multiplied by
+  if constexpr (RP::kE4m3) {
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      const int h = 8 * mb + g;
+      const uint16_t* qh = P.q + (static_cast<long long>(row) * P.hq + kvh * G + min(h, G - 1)) * 128;
+      uint2 v[KK][2];
+      float peak = 0.f;
+      bool odd = false;  // an infinity or a NaN
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          v[kk][u] = h < G ? *reinterpret_cast<const uint2*>(qh + 32 * kk + 16 * u + 4 * t) : make_uint2(0u, 0u);
+          const float x[4] = {bf16_lo(v[kk][u].x), bf16_hi(v[kk][u].x), bf16_lo(v[kk][u].y), bf16_hi(v[kk][u].y)};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            odd |= !(fabsf(x[e]) <= 3.39e38f);
+            peak = fmaxf(peak, fabsf(x[e]));
+          }
+        }
+#pragma unroll
+      for (int o = 1; o <= 2; o <<= 1) {
+        peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, o));
+        odd |= __shfl_xor_sync(0xffffffffu, odd, o);
+      }
+      // a power of two that brings the head's largest |q| into [128, 256)
+      // (two factors: 2^e itself may leave fp32)
+      const int e = peak > 0.f ? max(__float_as_int(peak) >> 23, 1) - 127 - 7 : 0;
+      const float f0 = exp2i(-(e / 2)), f1 = exp2i(-(e - e / 2));
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint16_t h0, l0, h1, l1;
+          split_e4m3x2(pack_f16x2(bf16_lo(v[kk][u].x) * f0 * f1, bf16_hi(v[kk][u].x) * f0 * f1), h0, l0);
+          split_e4m3x2(pack_f16x2(bf16_lo(v[kk][u].y) * f0 * f1, bf16_hi(v[kk][u].y) * f0 * f1), h1, l1);
+          qa[mb][kk][2 * u] = pack16(h0, h1);
+          qa[mb][kk][2 * u + 1] = pack16(l0, l1);
+        }
+      // D^-1/2 log2 e and the static K scale with it; block scales come per token
+      qs[mb] = odd ? __int_as_float(0x7fffffff)
+                   : exp2i(e / 2) * (0.08838834764831845f * kLog2e * (KVT == 1 ? P.k_scale : 1.0f)) * exp2i(e - e / 2);
+    }
+  } else {
+    qs[0] = 0.08838834764831845f * kLog2e;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int h = 8 * s + g;
+      const uint16_t* qh = P.q + (static_cast<long long>(row) * P.hq + kvh * G + min(h, G - 1)) * 128;
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          qa[0][kk][2 * u + s] =
+              s < HB && h < G ? *reinterpret_cast<const uint32_t*>(qh + 16 * kk + 8 * u + 2 * t) : 0u;
+    }
+  }
+
+  // ---- the ring
+  uint8_t* ring = smem + warp * ST * RP::kSlab;
+  uint32_t vmask[ST];   // valid tokens of the slabs in flight, oldest first
+  uint32_t odd_pair[ST];  // (block scales) which half of its scale word a token takes
+  const uint8_t* kvb = static_cast<const uint8_t*>(P.kv);
+  const long long scale_bytes =
+      KVT == 2 ? 2ll * P.num_blocks * P.hkv * (P.page / P.scale_block) : 0;
+  const int scale_shift = KVT == 2 ? __ffs(P.scale_block) - 1 : 0;
+  auto issue = [&](int stage, uint32_t rid, uint32_t& vm, uint32_t& odd) {
+    vm = __ballot_sync(0xffffffffu, rid != kBadRow);
+    uint8_t* dst = ring + stage * RP::kSlab;
+    // a lane copies 16 bytes of K or V of one token in each instruction
+    constexpr int LPR = 2 * RP::kRowB / 16;  // lanes of a token's row: 32 or 16
+    const int c = lane % LPR, is_v = c >= LPR / 2 ? 1 : 0, chunk = c % (LPR / 2), sub = lane / LPR;
+    const uint8_t* src = kvb + c * 16;
+    uint8_t* dl = dst + is_v * TS * RP::kRowB;
+    constexpr uint32_t kFull = TS == 32 ? 0xffffffffu : 0xffffu;
+    if (vm == kFull) {
+#pragma unroll
+      for (int j0 = 0; j0 < TS; j0 += 32 / LPR) {
+        const int j = j0 + sub;
+        const uint32_t r = __shfl_sync(0xffffffffu, rid, j);
+        cp_async16_full(dl + j * RP::kRowB + ((chunk ^ (is_v ? j & 7 : swz_k<KVT>(j))) << 4),
+                        src + static_cast<long long>(r) * (2 * RP::kRowB));
+      }
+    } else {  // masked tokens become zeros
+#pragma unroll
+      for (int j0 = 0; j0 < TS; j0 += 32 / LPR) {
+        const int j = j0 + sub;
+        const uint32_t r = __shfl_sync(0xffffffffu, rid, j);
+        const bool ok = (vm >> j) & 1u;
+        cp_async16(dl + j * RP::kRowB + ((chunk ^ (is_v ? j & 7 : swz_k<KVT>(j))) << 4),
+                   src + static_cast<long long>(ok ? r : 0u) * (2 * RP::kRowB), ok ? 16u : 0u);
       }
     }
-    ks *= 0.08838834764831845f;
-#pragma unroll
-    for (int h = 0; h < GM; ++h) {
-      float s = q[h][0] * k[0] + q[h][1] * k[1] + q[h][2] * k[2] + q[h][3] * k[3];
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      s *= ks;
-      const float mn = fmaxf(m[h], s);
-      const float ref = mn == -INFINITY ? 0.f : mn;
-      const float al = __expf(m[h] - ref), p = __expf(s - ref);
-      m[h] = mn;
-      l[h] = l[h] * al + p;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[h][e] = o[h][e] * al + p * vs * v[e];
+    if constexpr (KVT == 2) {
+      // the aligned word around the token's two scale bytes (the last word of
+      // an odd number of pairs holds one)
+      const bool ok = rid != kBadRow;
+      const uint32_t pair = ok ? rid >> scale_shift : 0u;
+      const long long at = 2ll * (pair & ~1u);
+      cp_async4(&s_raw[warp][stage][lane], P.scales + at,
+                ok ? static_cast<uint32_t>(min(4ll, scale_bytes - at)) : 0u);
+      odd = __ballot_sync(0xffffffffu, pair & 1u);
     }
+  };
+#pragma unroll
+  for (int i = 0; i < ST; ++i) pg[i] = fetch_page(tok[i]);
+#pragma unroll
+  for (int i = 0; i < ST; ++i) vmask[i] = odd_pair[i] = 0u;
+#pragma unroll
+  for (int i = 0; i < ST - 1; ++i) {
+    if (i < cnt) issue(i, row_id(tok[i], pg[i]), vmask[i], odd_pair[i]);
+    cp_async_commit();
   }
-  if (bad && lane == 0) flag_error(P.err);
+  // the slab to copy next, and the one after it
+  int tok_n = tok[ST - 1], pg_n = pg[ST - 1], tok_nn = tok[ST];
+
+  float o[MB][16][4];
+  float m[MB][NS], l[MB][NS];
 #pragma unroll
-  for (int h = 0; h < GM; ++h) {
-    s_m[warp][h] = m[h];
-    s_l[warp][h] = l[h];
+  for (int mb = 0; mb < MB; ++mb) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s_o[warp][h][4 * lane + e] = o[h][e];
+    for (int s = 0; s < NS; ++s) {
+      m[mb][s] = -INFINITY;
+      l[mb][s] = 0.f;
+    }
+#pragma unroll
+    for (int nb = 0; nb < 16; ++nb) o[mb][nb][0] = o[mb][nb][1] = o[mb][nb][2] = o[mb][nb][3] = 0.f;
+  }
+
+  int stage = 0;
+  for (int it = 0; it < cnt; ++it) {
+    cp_async_wait<ST - 2>();
+    __syncwarp();  // slab it has landed for every lane; slab it - 1 is free
+    {
+      int nst = stage + ST - 1;
+      if (nst >= ST) nst -= ST;
+      if (it + ST - 1 < cnt) issue(nst, row_id(tok_n, pg_n), vmask[ST - 1], odd_pair[ST - 1]);
+      cp_async_commit();
+      tok_n = tok_nn;
+      pg_n = fetch_page(tok_n);
+      tok_nn = fetch_tok(it + ST + 1);
+    }
+    const uint8_t* sK = ring + stage * RP::kSlab;
+    const uint8_t* sV = sK + TS * RP::kRowB;
+    const uint32_t vm = vmask[0];
+    float ks[2 * NBK], lv[2 * NBK], iv[2 * NBK];  // of the lane's tokens (block scales)
+    if constexpr (KVT == 2) {
+      const uint32_t w = s_raw[warp][stage][lane] >> ((odd_pair[0] >> lane & 1u) * 16);
+      const int ek = scale_exp(w & 0xFFu), ev = scale_exp((w >> 8) & 0xFFu);
+      reinterpret_cast<float*>(s_scl[warp][0])[lane] = exp2i(ek);
+      reinterpret_cast<float*>(s_scl[warp][1])[lane] = static_cast<float>(ev);
+      reinterpret_cast<float*>(s_scl[warp][2])[lane] = exp2i(-ev);
+      __syncwarp();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float4 a = s_scl[warp][0][4 * u + t], b = s_scl[warp][1][4 * u + t], c = s_scl[warp][2][4 * u + t];
+        ks[4 * u] = a.x; ks[4 * u + 1] = a.y; ks[4 * u + 2] = a.z; ks[4 * u + 3] = a.w;
+        lv[4 * u] = b.x; lv[4 * u + 1] = b.y; lv[4 * u + 2] = b.z; lv[4 * u + 3] = b.w;
+        iv[4 * u] = c.x; iv[4 * u + 1] = c.y; iv[4 * u + 2] = c.z; iv[4 * u + 3] = c.w;
+      }
+    }
+
+    // ---- S = Q K^T.  Column c of block nb is token tau(nb, c):
+    //   bf16   8 nb + c;   e4m3  16 (nb / 2) + 4 (c / 2) + 2 (nb % 2) + c % 2
+    // so that a lane's columns 2t, 2t + 1 are the tokens of its P fragment.
+    float s[MB][NBK][4];
+#pragma unroll
+    for (int nb = 0; nb < NBK; ++nb) {
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) s[mb][nb][0] = s[mb][nb][1] = s[mb][nb][2] = s[mb][nb][3] = 0.f;
+      const int c = lane & 7;
+      const int tk = RP::kE4m3 ? 16 * (nb >> 1) + 4 * (c >> 1) + 2 * (nb & 1) + (c & 1) : 8 * nb + c;
+#pragma unroll
+      for (int j = 0; j < KK / 2; ++j) {  // four 16-byte chunks: two MMA steps
+        uint32_t b[4];
+        ldmatrix_x4(b, sK + tk * RP::kRowB + (((4 * j + (lane >> 3)) ^ swz_k<KVT>(tk)) << 4));
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          if constexpr (RP::kE4m3) {
+            mma_e4m3_16832(s[mb][nb], qa[mb][2 * j], b[0], b[1]);
+            mma_e4m3_16832(s[mb][nb], qa[mb][2 * j + 1], b[2], b[3]);
+          } else {
+            mma_bf16_16816(s[mb][nb], qa[mb][2 * j], b[0], b[1]);
+            mma_bf16_16816(s[mb][nb], qa[mb][2 * j + 1], b[2], b[3]);
+          }
+        }
+      }
+    }
+
+    // ---- weights.  Entry e of block nb: the lane's token number 2 nb + e
+    uint32_t pa[MB][4];
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+#pragma unroll
+      for (int sI = 0; sI < NS; ++sI) {
+        float z[2 * NBK];  // exponents (log2) without the reference
+#pragma unroll
+        for (int i = 0; i < 2 * NBK; ++i) {
+          const int nb = i >> 1, e = i & 1;
+          if constexpr (RP::kE4m3) {
+            z[i] = fmaf(s[mb][nb][2 + e], 0.03125f, s[mb][nb][e]) * qs[mb];
+            if constexpr (KVT == 2) z[i] = fmaf(z[i], ks[i], lv[i]);
+          } else {
+            z[i] = s[0][nb][2 * sI + e] * qs[0];
+          }
+        }
+        constexpr uint32_t kFull = TS == 32 ? 0xffffffffu : 0xffffu;
+        if (vm != kFull) {
+#pragma unroll
+          for (int i = 0; i < 2 * NBK; ++i) {
+            const int tk = RP::kE4m3 ? 16 * (i >> 2) + 4 * t + (i & 3) : 8 * (i >> 1) + 2 * t + (i & 1);
+            if (!((vm >> tk) & 1u)) z[i] = -INFINITY;
+          }
+        }
+        float mx = z[0];
+#pragma unroll
+        for (int i = 1; i < 2 * NBK; ++i) mx = fmaxf(mx, z[i]);
+        float& mr = m[mb][sI];
+        // (no reference yet: any score passes it)
+        if (__any_sync(0xffffffffu, mx > mr + RP::kUp)) {
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float mn = fmaxf(mr, mx - RP::kTop);
+          const float al = ex2_ftz(mr - (mn == -INFINITY ? 0.f : mn));
+          l[mb][sI] *= al;
+#pragma unroll
+          for (int nb = 0; nb < 16; ++nb) {
+            o[mb][nb][2 * sI] *= al;
+            o[mb][nb][2 * sI + 1] *= al;
+            if constexpr (RP::kE4m3) {
+              o[mb][nb][2] *= al;
+              o[mb][nb][3] *= al;
+            }
+          }
+          mr = mn;
+        }
+        const float ref = mr == -INFINITY ? 0.f : mr;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2 * NBK; ++i) {
+          z[i] = ex2_ftz(z[i] - ref);
+          sum = KVT == 2 ? fmaf(z[i], iv[i], sum) : sum + z[i];
+        }
+        l[mb][sI] += sum;
+        if constexpr (RP::kE4m3) {
+          uint16_t hi[NBK], lw[NBK];
+#pragma unroll
+          for (int nb = 0; nb < NBK; ++nb) split_e4m3x2(pack_f16x2(z[2 * nb], z[2 * nb + 1]), hi[nb], lw[nb]);
+          pa[mb][0] = pack16(hi[0], hi[1]);
+          pa[mb][1] = pack16(lw[0], lw[1]);
+          pa[mb][2] = pack16(hi[NBK - 2], hi[NBK - 1]);
+          pa[mb][3] = pack16(lw[NBK - 2], lw[NBK - 1]);
+        } else {
+          pa[0][sI] = pack_bf16x2(z[0], z[1]);
+          pa[0][2 + sI] = pack_bf16x2(z[2], z[3]);
+          if constexpr (NS == 1) pa[0][1] = pa[0][3] = 0u;
+        }
+      }
+    }
+
+    // ---- O += P V
+    if constexpr (RP::kE4m3) {
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {  // 16 dims
+        uint32_t b[4];
+        ldmatrix_b8_trans(b, sV + lane * 128 + ((d ^ (lane & 7)) << 4));
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          mma_e4m3_16832(o[mb][2 * d], pa[mb], b[0], b[2]);
+          mma_e4m3_16832(o[mb][2 * d + 1], pa[mb], b[1], b[3]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        uint32_t b[4];
+        const int tk = lane & 15;
+        ldmatrix_x4_trans(b, sV + tk * 256 + (((2 * d + (lane >> 4)) ^ (tk & 7)) << 4));
+        mma_bf16_16816(o[0][2 * d], pa[0], b[0], b[1]);
+        mma_bf16_16816(o[0][2 * d + 1], pa[0], b[2], b[3]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i + 1 < ST; ++i) {
+      vmask[i] = vmask[i + 1];
+      odd_pair[i] = odd_pair[i + 1];
+    }
+    if (++stage == ST) stage = 0;
+  }
+  cp_async_wait<0>();
+  if (__any_sync(0xffffffffu, bad) && lane == 0) flag_error(P.err);
+
+  // ---- join the warps: [head][warp] references and sums, [warp][head][dim]
+  __syncthreads();
+  constexpr int HN = 8 * HB;
+  constexpr int LD = 128 + 4;  // (head rows a few banks apart)
+  float* cm = reinterpret_cast<float*>(smem);
+  float* cl = cm + kWarps * HN;
+  float* co = cl + kWarps * HN;
+#pragma unroll
+  for (int hb = 0; hb < HB; ++hb) {
+    constexpr bool kE = RP::kE4m3;
+    const int mb = kE ? hb : 0, sI = kE ? 0 : hb;
+    float sum = l[mb][sI];
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    const int at = warp * HN + 8 * hb + g;
+    if (t == 0) {
+      cm[at] = m[mb][sI];
+      cl[at] = sum;
+    }
+#pragma unroll
+    for (int nb = 0; nb < 16; ++nb) {
+      float2 v;
+      v.x = kE ? fmaf(o[mb][nb][2], 0.03125f, o[mb][nb][0]) : o[mb][nb][2 * sI];
+      v.y = kE ? fmaf(o[mb][nb][3], 0.03125f, o[mb][nb][1]) : o[mb][nb][2 * sI + 1];
+      *reinterpret_cast<float2*>(co + at * LD + 8 * nb + 2 * t) = v;
+    }
   }
   __syncthreads();
-  for (int h = 0; h < G; ++h) {
-    const int d = threadIdx.x;
-    float M = -INFINITY, L = 0.f, a = 0.f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][h]);
-    if (M == -INFINITY) M = 0.f;
+  const int d0 = (threadIdx.x & 15) * 8;
+#pragma unroll
+  for (int hb = 0; hb < HB; ++hb) {
+    const int h = (threadIdx.x >> 4) + 8 * hb;
+    if (h >= G) continue;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, cm[w * HN + h]);
+    float L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float wt = __expf(s_m[w][h] - M);
-      L += wt * s_l[w][h];
-      a += wt * s_o[w][h][d];
+      const float mw = cm[w * HN + h];
+      const float wt = mw == -INFINITY ? 0.f : ex2_ftz(mw - M);
+      L = fmaf(cl[w * HN + h], wt, L);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(co[(w * HN + h) * LD + d0 + e], wt, acc[e]);
     }
-    const long long at = (static_cast<long long>(row) * P.hq + kvh * G + h) * 128 + d;
     // (a NaN sum is not an empty row)
-    float y = bf16_round(L == 0.f ? 0.f : a / L);
-    if (P.gate != nullptr) y = y / (1.0f + __expf(-__uint_as_float(static_cast<uint32_t>(P.gate[at]) << 16)));
-    const __nv_bfloat16 b = __float2bfloat16_rn(y);
-    P.out[at] = *reinterpret_cast<const uint16_t*>(&b);
+    const float inv = L == 0.f ? 0.f : (KVT == 1 ? P.v_scale : 1.0f) / L;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] *= inv;
+    const long long head = static_cast<long long>(row) * P.hq + kvh * G + h;
+    if (P.splits == 1) {
+      store_gated8(P, head * 128 + d0, acc, load_gate(P, head * 128 + d0));
+      continue;
+    }
+    const long long ph = static_cast<long long>(split) * P.rows * P.hq + head;
+    float4* po = reinterpret_cast<float4*>(P.part_o + ph * 128 + d0);
+    po[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    po[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    if (d0 == 0) P.part_lse[ph] = L == 0.f ? -INFINITY : M + log2f(L);
   }
 }
 
-template <int GM>
-cudaError_t launch_group(const RowGqaParams& p, cudaStream_t stream) {
-  const dim3 grid(p.rows * p.hkv), block(kThreads);
-  switch (p.kv_dtype) {
-    case QSA_DTYPE_BF16: return launch_kernel(row_gqa_kernel<GM, QSA_DTYPE_BF16>, grid, block, 0, stream, false, p);
-    case QSA_DTYPE_E4M3: return launch_kernel(row_gqa_kernel<GM, QSA_DTYPE_E4M3>, grid, block, 0, stream, false, p);
-    default: return launch_kernel(row_gqa_kernel<GM, QSA_DTYPE_E4M3_BLOCK>, grid, block, 0, stream, false, p);
+// Joins the splits of each (row, head), 8 dims a thread, in split order.
+__global__ void __launch_bounds__(256) row_merge_kernel(const RowGqaParams P) {
+  griddep_wait();  // every split's partials are written
+  const long long idx = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const long long head = idx >> 4;
+  if (head >= static_cast<long long>(P.rows) * P.hq) return;
+  const int row = static_cast<int>(head / P.hq), d0 = (static_cast<int>(idx) & 15) * 8;
+  if (P.packed == nullptr && !row_live(P, row, P.token_to_req[row])) return;
+  const uint4 gate = load_gate(P, head * 128 + d0);
+  const long long stride = static_cast<long long>(P.rows) * P.hq;
+  float M = -INFINITY;
+  bool nan = false;
+  for (int s = 0; s < P.splits; ++s) {
+    const float v = __ldcg(P.part_lse + s * stride + head);
+    nan |= v != v;
+    M = fmaxf(M, v);
   }
+  float W = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < P.splits; ++s) {
+    const float lse = __ldcg(P.part_lse + s * stride + head);
+    if (lse == -INFINITY) continue;
+    const float w = ex2_ftz(lse - M);
+    W += w;
+    const float4* po = reinterpret_cast<const float4*>(P.part_o + (s * stride + head) * 128 + d0);
+    const float4 a = __ldcg(po), b = __ldcg(po + 1);
+    acc[0] = fmaf(w, a.x, acc[0]); acc[1] = fmaf(w, a.y, acc[1]);
+    acc[2] = fmaf(w, a.z, acc[2]); acc[3] = fmaf(w, a.w, acc[3]);
+    acc[4] = fmaf(w, b.x, acc[4]); acc[5] = fmaf(w, b.y, acc[5]);
+    acc[6] = fmaf(w, b.z, acc[6]); acc[7] = fmaf(w, b.w, acc[7]);
+  }
+  const float inv = nan ? __int_as_float(0x7fffffff) : W == 0.f ? 0.f : 1.0f / W;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] *= inv;
+  store_gated8(P, head * 128 + d0, acc, gate);
+}
+
+template <int KVT, int HB>
+cudaError_t launch_kind(const RowGqaParams& p, cudaStream_t stream) {
+  using RP = RowPlan<KVT>;
+  constexpr int kMerge = kWarps * 8 * HB * (128 + 4 + 2) * 4;
+  constexpr int kSmem = RP::kSmem > kMerge ? RP::kSmem : kMerge;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(row_gqa_kernel<KVT, HB>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  return launch_kernel(row_gqa_kernel<KVT, HB>, dim3(p.rows * p.hkv, p.splits), dim3(kThreads), kSmem,
+                       stream, false, p);
 }
 
 }  // namespace
 
+int row_gqa_splits(int rows, int hkv, long long max_tokens, int kv_dtype, int sms) {
+  const long long base = static_cast<long long>(rows) * hkv;
+  if (base <= 0) return 1;
+  const int least = (kv_dtype == QSA_DTYPE_BF16 ? 16 : 32) * kWarps * 2;  // two slabs a warp
+  long long s = 4ll * sms / base;
+  const long long most = (max_tokens + least - 1) / least;
+  if (s > most) s = most;
+  if (s > 128) s = 128;
+  return s < 1 ? 1 : static_cast<int>(s);
+}
+
 cudaError_t launch_row_gqa(const RowGqaParams& p, cudaStream_t stream) {
   if (p.rows == 0) return cudaSuccess;
-  return p.group <= 8 ? launch_group<8>(p, stream) : launch_group<16>(p, stream);
+  const bool wide = p.group > 8;
+  cudaError_t e;
+  switch (p.kv_dtype) {
+    case QSA_DTYPE_BF16: e = wide ? launch_kind<0, 2>(p, stream) : launch_kind<0, 1>(p, stream); break;
+    case QSA_DTYPE_E4M3: e = wide ? launch_kind<1, 2>(p, stream) : launch_kind<1, 1>(p, stream); break;
+    default: e = wide ? launch_kind<2, 2>(p, stream) : launch_kind<2, 1>(p, stream); break;
+  }
+  if (e != cudaSuccess || p.splits == 1) return e;
+  const long long items = static_cast<long long>(p.rows) * p.hq * 16;
+  return launch_kernel(row_merge_kernel, dim3(static_cast<unsigned>((items + 255) / 256)), dim3(256), 0, stream, true, p);
 }
 
 }  // namespace qsa
