@@ -649,8 +649,17 @@ long long window_tokens(const qsa_window_args* a) {
   return n < a->max_context ? n : a->max_context;
 }
 
-int window_splits(const qsa_gqa_cfg* g, const qsa_window_args* a) {
-  return row_gqa_splits(a->rows, g->num_kv_heads, window_tokens(a), g->kv_dtype, sm_count());
+// Tiles or single rows, and how many splits of them.
+struct WindowPlan {
+  bool tile;
+  int splits;
+};
+WindowPlan window_plan(const qsa_gqa_cfg* g, const qsa_window_args* a) {
+  const int group = g->num_q_heads / g->num_kv_heads;
+  const long long n = window_tokens(a);
+  if (static_cast<long long>(a->rows) * group >= 16ll * a->reqs)
+    return {true, window_tile_splits(a->rows, g->num_kv_heads, group, n, sm_count())};
+  return {false, row_gqa_splits(a->rows, g->num_kv_heads, n, g->kv_dtype, sm_count())};
 }
 
 qsa_status do_window(const qsa_gqa_cfg* g, const qsa_window_args* a, void* ws, size_t ws_bytes,
@@ -666,9 +675,10 @@ qsa_status do_window(const qsa_gqa_cfg* g, const qsa_window_args* a, void* ws, s
   p.logical = a->logical_positions;
   p.window = a->window;
   p.sinks = a->sinks;
-  st = place_splits(&p, g, window_splits(g, a), ws, ws_bytes);
+  const WindowPlan plan = window_plan(g, a);
+  st = place_splits(&p, g, plan.splits, ws, ws_bytes);
   if (st != QSA_OK) return st;
-  return cuda_status(launch_row_gqa(p, stream));
+  return cuda_status(plan.tile ? launch_window_tile(p, stream) : launch_row_gqa(p, stream));
 }
 
 // Layer-step workspace regions.
@@ -945,7 +955,7 @@ qsa_status qsa_window_gqa(const qsa_gqa_cfg* gcfg, const qsa_window_args* args, 
 
 size_t qsa_window_workspace_bytes(const qsa_gqa_cfg* gcfg, const qsa_window_args* args) {
   if (check_window(gcfg, args) != QSA_OK || args->rows == 0) return 0;
-  return row_ws_bytes(gcfg, args->rows, window_splits(gcfg, args));
+  return row_ws_bytes(gcfg, args->rows, window_plan(gcfg, args).splits);
 }
 
 qsa_status qsa_mtp_steps(const qsa_cfg* cfg, const qsa_gqa_cfg* gcfg, const qsa_step_args* steps,

@@ -160,6 +160,12 @@ struct RowGqaParams {
 // multiprocessors.
 int row_gqa_splits(int rows, int hkv, long long max_tokens, int kv_dtype, int sms);
 cudaError_t launch_row_gqa(const RowGqaParams& p, cudaStream_t stream);
+// Joins the splits that p's launch left in part_o and part_lse.
+cudaError_t launch_row_merge(const RowGqaParams& p, cudaStream_t stream);
+// Window attention by tiles of 128 (row, head) pairs of one request.
+int window_tile_rows(int group);  // rows of a CTA
+int window_tile_splits(int rows, int hkv, int group, long long max_tokens, int sms);
+cudaError_t launch_window_tile(const RowGqaParams& p, cudaStream_t stream);
 
 // Keys and values into the paged cache, q and gate beside them.
 struct AppendParams {

@@ -31,6 +31,7 @@
 #include "qsa_device.cuh"
 #include "qsa_kernels.h"
 #include "qsa_launch.cuh"
+#include "row_output.cuh"
 
 namespace qsa {
 namespace {
@@ -38,7 +39,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kBadRow = 0xFFFFFFFFu;
-constexpr float kLog2e = 1.4426950408889634f;
 
 // D(16x8 fp32) += A(16x32 e4m3, row) * B(32x8 e4m3, col)
 __device__ __forceinline__ void mma_e4m3_16832(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -66,11 +66,6 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
   uint32_t out;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(out) : "h"(v));
   return out;
-}
-__device__ __forceinline__ float ex2_ftz(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 // 4-byte asynchronous copy of src_bytes bytes, the rest zero.
 __device__ __forceinline__ void cp_async4(void* dst, const void* src, uint32_t src_bytes) {
@@ -112,33 +107,6 @@ struct RowPlan {
 template <int KVT>
 __device__ __forceinline__ int swz_k(int tok) {
   return KVT == 0 ? tok & 7 : (tok & 1) | ((tok >> 1) & 6);
-}
-
-__device__ __forceinline__ bool row_live(const RowGqaParams& P, int row, int req) {
-  return req >= 0 && req < P.reqs && row >= P.qsl[req] && row < P.qsl[req + 1];
-}
-
-__device__ __forceinline__ float sigmoid_of(uint32_t bf16_bits) {
-  return 1.0f / (1.0f + __expf(-__uint_as_float(bf16_bits << 16)));
-}
-
-// out[8 dims] = bf16(bf16(x) * sigmoid(gate)), or bf16(x) without a gate.
-__device__ __forceinline__ void store_gated8(const RowGqaParams& P, long long at, const float (&x)[8], uint4 g) {
-  const uint32_t gv[4] = {g.x, g.y, g.z, g.w};
-  uint32_t o[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    float a = bf16_round(x[2 * e]), b = bf16_round(x[2 * e + 1]);
-    if (P.gate != nullptr) {
-      a *= sigmoid_of(gv[e] & 0xFFFFu);
-      b *= sigmoid_of(gv[e] >> 16);
-    }
-    o[e] = pack_bf16x2(a, b);
-  }
-  *reinterpret_cast<uint4*>(P.out + at) = make_uint4(o[0], o[1], o[2], o[3]);
-}
-__device__ __forceinline__ uint4 load_gate(const RowGqaParams& P, long long at) {
-  return P.gate != nullptr ? *reinterpret_cast<const uint4*>(P.gate + at) : make_uint4(0u, 0u, 0u, 0u);
 }
 
 // HB: blocks of 8 query heads (groups of 16: 2).  bf16 holds both on one M
@@ -649,6 +617,10 @@ cudaError_t launch_row_gqa(const RowGqaParams& p, cudaStream_t stream) {
     default: e = wide ? launch_kind<2, 2>(p, stream) : launch_kind<2, 1>(p, stream); break;
   }
   if (e != cudaSuccess || p.splits == 1) return e;
+  return launch_row_merge(p, stream);
+}
+
+cudaError_t launch_row_merge(const RowGqaParams& p, cudaStream_t stream) {
   const long long items = static_cast<long long>(p.rows) * p.hq * 16;
   return launch_kernel(row_merge_kernel, dim3(static_cast<unsigned>((items + 255) / 256)), dim3(256), 0, stream, true, p);
 }
