@@ -678,7 +678,16 @@ qsa_status do_window(const qsa_gqa_cfg* g, const qsa_window_args* a, void* ws, s
   const WindowPlan plan = window_plan(g, a);
   st = place_splits(&p, g, plan.splits, ws, ws_bytes);
   if (st != QSA_OK) return st;
-  return cuda_status(plan.tile ? launch_window_tile(p, stream) : launch_row_gqa(p, stream));
+  if (!plan.tile) return cuda_status(launch_row_gqa(p, stream));
+  // boxes of the page's keys, up to a tile: pages of a multiple of 32 (row
+  // coordinates are int32)
+  CUtensorMap tmap{};
+  const long long cache_rows = static_cast<long long>(p.num_blocks) * p.hkv * p.page;
+  if (p.kv_dtype == QSA_DTYPE_BF16 && p.page % 32 == 0 && cache_rows < (1ll << 31)) {
+    p.box = p.page % 128 == 0 ? 128 : p.page % 64 == 0 ? 64 : 32;
+    if (!encode_bf16_2d(&tmap, a->kv, 256, cache_rows, p.box)) return QSA_ERR_CUDA;
+  }
+  return cuda_status(launch_window_tile(p, tmap, stream));
 }
 
 // Layer-step workspace regions.

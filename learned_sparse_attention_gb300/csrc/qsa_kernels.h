@@ -151,6 +151,7 @@ struct RowGqaParams {
   int kv_dtype;
   float k_scale, v_scale;
   int window, sinks;
+  int box;                 // keys of a TMA box of the window tiles, 0: no TMA
   int splits;
   float* part_o;           // [splits, rows, Hq, 128] (splits > 1)
   float* part_lse;         // [splits, rows, Hq]
@@ -165,7 +166,9 @@ cudaError_t launch_row_merge(const RowGqaParams& p, cudaStream_t stream);
 // Window attention by tiles of 128 (row, head) pairs of one request.
 int window_tile_rows(int group);  // rows of a CTA
 int window_tile_splits(int rows, int hkv, int group, long long max_tokens, int sms);
-cudaError_t launch_window_tile(const RowGqaParams& p, cudaStream_t stream);
+// tmap: the bf16 cache as [blocks * Hkv * page, 256] with a box of 64 x p.box
+// (128-byte swizzle), read when p.box != 0.
+cudaError_t launch_window_tile(const RowGqaParams& p, const CUtensorMap& tmap, cudaStream_t stream);
 
 // Keys and values into the paged cache, q and gate beside them.
 struct AppendParams {

@@ -13,8 +13,8 @@
 //   0-3, 4-7  softmax of tile A, B: S from TMEM, masks on the tiles that need
 //             them, P back over S's columns, at the end the gated output;
 //   8-11      load K and V tiles of 128 keys through the block table into a
-//             ring (128-byte swizzle): bf16 by cp.async; e4m3 codes through
-//             registers, as f16 (exact).  Keys that no row of the CTA sees
+//             ring (128-byte swizzle): bf16 by TMA or cp.async; e4m3 codes
+//             through registers, as f16 (exact).  Keys that no row of the CTA sees
 //             become zeros, whatever the cache holds there;
 //   12        issues the MMAs: S_A(j+1) right after O_A(j), so the softmax of
 //             one tile runs under the products of the other.
@@ -82,6 +82,16 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+// Registers of a warpgroup's threads, which together keep to the launch's 128
+// a thread: all four warps of the group execute it.
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 // Byte of 16-byte chunk c (8 dims) of row r in a swizzled two-atom tile.
 __device__ __forceinline__ int tile_byte(int r, int c) {
   return (c >> 3) * kAtom + r * 128 + (((c & 7) ^ (r & 7)) << 4);
@@ -95,13 +105,15 @@ struct Tiles {
 
 // KVT 0 bf16, 1 e4m3 with static scales, 2 e4m3 with block scales
 template <int KVT>
-__global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const RowGqaParams P) {
+__global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_constant__ CUtensorMap tmap, const RowGqaParams P) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_pmin, s_pmax, s_neg;
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   uint8_t* sQ = smem_raw + pad;
   uint8_t* sKV = sQ + 2 * kTileBytes;
   TileShared& sh = *reinterpret_cast<TileShared*>(sKV + kBufs * kTileBytes);
+  constexpr int kSoftmaxRegs = KVT == 0 ? 192 : 176, kLoadRegs = KVT == 0 ? 80 : 112, kMmaRegs = 48;
+  static_assert(2 * kSoftmaxRegs + kLoadRegs + kMmaRegs <= 4 * 128, "the launch's registers");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int kvh = blockIdx.y, split = blockIdx.z;
   const int G = P.group, R = 128 / G;
@@ -225,26 +237,28 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const RowGqaPa
 
   if (warp >= 8 && warp < 12) {
     // ------------------------------------------------------------ loads
+    regs_down<kLoadRegs>();
     const int lt = tid - 256;  // 0 .. 127
     const int32_t* bt_row = P.block_table + static_cast<long long>(req) * P.bt_stride;
     const uint8_t* kvb = static_cast<const uint8_t*>(P.kv);
     const bool page_pow2 = (P.page & (P.page - 1)) == 0;
     const int page_shift = __ffs(P.page) - 1;
     auto seen = [&](int key) { return key <= pmax && (key >= wlo || key < P.sinks); };
-    // cache row of the first key of 16-key block (lane & 7) of tile j, or -1:
-    // nothing to see there, -2: a page that is none
-    auto fetch_rows = [&](int j) -> long long {
+    // cache row of the first key of 16-key block (lane & 7) of tile j, or
+    // kUnseen: nothing to see there, or kNoPage: a page that is none
+    constexpr uint32_t kUnseen = 0xFFFFFFFFu, kNoPage = 0xFFFFFFFEu;
+    auto fetch_rows = [&](int j) -> uint32_t {
       const int k0 = T.first_key(j) + 16 * (lane & 7);
-      if (!(k0 <= pmax && (k0 + 15 >= wlo || k0 < P.sinks))) return -1;
+      if (!(k0 <= pmax && (k0 + 15 >= wlo || k0 < P.sinks))) return kUnseen;
       const int blk = page_pow2 ? k0 >> page_shift : k0 / P.page;
       const int pid = blk < P.bt_stride ? bt_row[blk] : -1;
-      if (pid < 0 || pid >= P.num_blocks) return -2;
-      return (static_cast<long long>(pid) * P.hkv + kvh) * P.page + (k0 - blk * P.page);
+      if (pid < 0 || pid >= P.num_blocks) return kNoPage;
+      return (static_cast<uint32_t>(pid) * P.hkv + kvh) * static_cast<uint32_t>(P.page) + (k0 - blk * P.page);
     };
     // the masks and scales of tile j, by one warp, before its K is announced
-    auto publish = [&](int j, long long rows) {
+    auto publish = [&](int j, uint32_t rows) {
       const int slot = (j - j0) % kSlots;
-      const unsigned bad = __ballot_sync(0xffffffffu, rows == -2) & 0xFFu;
+      const unsigned bad = __ballot_sync(0xffffffffu, rows == kNoPage) & 0xFFu;
       if (lane < 4) {
         const unsigned two_blocks = (bad >> (2 * lane)) & 3u;
         sh.valid[slot][lane] = ~(((two_blocks & 1u) ? 0xFFFFu : 0u) | ((two_blocks & 2u) ? 0xFFFF0000u : 0u));
@@ -255,8 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const RowGqaPa
       }
       if (KVT == 2 && lane < 8) {
         int ek = 0, ev = 0;
-        if (rows >= 0) {
-          const uint16_t w = *reinterpret_cast<const uint16_t*>(P.scales + 2 * (rows / P.scale_block));
+        if (rows < kNoPage) {
+          const uint16_t w = *reinterpret_cast<const uint16_t*>(P.scales + 2ll * (rows / P.scale_block));
           ek = scale_exp(w & 0xFF);
           ev = scale_exp(w >> 8);
         }
@@ -281,8 +295,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const RowGqaPa
     };
 
     if constexpr (KVT == 0) {
+      // Tiles that every row sees come by TMA where a box holds at least 32
+      // keys of a page (P.box; the SM's TMA unit takes ~90 cycles a box,
+      // whatever its size, and a K and V tile have 2048 cycles between them);
+      // the others by cp.async, which zeroes what is not seen.
       constexpr int LAG = 2;  // tiles in flight behind the one being issued
-      long long rows = fetch_rows(j0), rows_next = -1;
+      uint32_t rows = fetch_rows(j0), rows_next = kUnseen;
       auto finish = [&](int s) {  // tile s has landed
         const int j = j0 + (s >> 1), b = s % kBufs;
         if ((s & 1) && tile_masked(j)) {
@@ -313,55 +331,88 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const RowGqaPa
         fence_proxy_async_smem();
         mbar_arrive(&sh.full[b]);
       };
+      int done = 0;  // tiles announced
+      const int dst0 = tile_byte(lt >> 4, lt & 15);
       for (int s = 0; s < 2 * nt; ++s) {
         const int j = j0 + (s >> 1), b = s % kBufs, is_v = s & 1;
         if (!is_v) {
           if (s > 0) rows = rows_next;
-          rows_next = (s >> 1) + 1 < nt ? fetch_rows(j + 1) : -1;
+          rows_next = (s >> 1) + 1 < nt ? fetch_rows(j + 1) : kUnseen;
+        }
+        const int kb = T.first_key(j);
+        const bool masked = tile_masked(j);
+        const bool tma = P.box != 0 && !masked && __all_sync(0xffffffffu, rows < kNoPage);
+        if (tma && done < s) {
+          cp_async_wait<0>();
+          for (; done < s; ++done) finish(done);
         }
         if (!__all_sync(0xffffffffu, mbar_wait(&sh.empty[b], ((s / kBufs) & 1) ^ 1, P.err))) break;
         if (!is_v && warp == 8) publish(j, rows);
-        const int kb = T.first_key(j);
-        const uint8_t* src = kvb + is_v * 256 + (lt & 15) * 16;
         uint8_t* dst = sKV + b * kTileBytes;
+        if (tma) {
+          if (lt == 0)
+            mbar_arrive_expect_tx(&sh.full[b], kTileBytes);
+          else
+            mbar_arrive(&sh.full[b]);
+          if (warp == 8) {
+            // a lane per box: 64 dims of P.box keys
+            const int per = 128 / P.box, k = lane % per, atom = lane / per;
+            const uint32_t r = __shfl_sync(0xffffffffu, rows, (k * P.box) >> 4);
+            __syncwarp();
+            if (atom < 2)
+              tma_load_2d(dst + atom * kAtom + k * P.box * 128, &tmap, is_v * 128 + atom * 64,
+                          static_cast<int>(r), &sh.full[b]);
+          }
+          done = s + 1;
+          continue;
+        }
+        const uint8_t* src = kvb + is_v * 256 + (lt & 15) * 16;
+        uint32_t base[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) base[i] = __shfl_sync(0xffffffffu, rows, i);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int key = 8 * i + (lt >> 4);
-          const long long base = __shfl_sync(0xffffffffu, rows, i >> 1);
-          const bool ok = base >= 0 && seen(kb + key);
-          cp_async16(dst + tile_byte(key, lt & 15), src + (ok ? base + (key & 15) : 0ll) * 512, ok ? 16u : 0u);
+          const uint32_t r = base[i >> 1];
+          const bool ok = r < kNoPage && (!masked || seen(kb + key));
+          cp_async16(dst + dst0 + i * 1024, src + static_cast<unsigned long long>(ok ? r + (key & 15) : 0u) * 512,
+                     ok ? 16u : 0u);
         }
         cp_async_commit();
-        if (s >= LAG) {
+        if (s - done >= LAG) {
           cp_async_wait<LAG>();
-          finish(s - LAG);
+          finish(done++);
         }
       }
       cp_async_wait<0>();
-      for (int s = max(0, 2 * nt - LAG); s < 2 * nt; ++s) finish(s);
+      for (; done < 2 * nt; ++done) finish(done);
     } else {
       // 16 codes a lane and load; the next tile's codes are in flight while
       // this one's are converted
-      auto load = [&](int s, long long rows, uint4 (&v)[8]) {
-        const int kb = T.first_key(j0 + (s >> 1));
+      auto load = [&](int s, uint32_t rows, uint4 (&v)[8]) {
+        const int j = j0 + (s >> 1), kb = T.first_key(j);
+        const bool masked = tile_masked(j);
         const uint8_t* src = kvb + (s & 1) * 128 + (lt & 7) * 16;
+        uint32_t base[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) base[i] = __shfl_sync(0xffffffffu, rows, i);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int key = 16 * i + (lt >> 3);
-          const long long base = __shfl_sync(0xffffffffu, rows, i);
+          const bool ok = base[i] < kNoPage && (!masked || seen(kb + 16 * i + (lt >> 3)));
           v[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (base >= 0 && seen(kb + key)) v[i] = *reinterpret_cast<const uint4*>(src + (base + (key & 15)) * 256);
+          if (ok) v[i] = *reinterpret_cast<const uint4*>(src + static_cast<unsigned long long>(base[i] + (lt >> 3)) * 256);
         }
       };
-      long long rows = fetch_rows(j0), rows_next = nt > 1 ? fetch_rows(j0 + 1) : -1;
+      uint32_t rows = fetch_rows(j0), rows_next = nt > 1 ? fetch_rows(j0 + 1) : kUnseen;
       uint4 cur[8], nxt[8];
       load(0, rows, cur);
+      const int dst0 = tile_byte(lt >> 3, 2 * (lt & 7)), dst1 = tile_byte(lt >> 3, 2 * (lt & 7) + 1);
       for (int s = 0; s < 2 * nt; ++s) {
         const int j = j0 + (s >> 1), b = s % kBufs, is_v = s & 1;
-        const long long rows_here = rows;
+        const uint32_t rows_here = rows;
         if (is_v) {  // the next load is the next tile's K
           rows = rows_next;
-          rows_next = (s >> 1) + 2 < nt ? fetch_rows(j + 2) : -1;
+          rows_next = (s >> 1) + 2 < nt ? fetch_rows(j + 2) : kUnseen;
         }
         if (s + 1 < 2 * nt) load(s + 1, rows, nxt);
         if (!__all_sync(0xffffffffu, mbar_wait(&sh.empty[b], ((s / kBufs) & 1) ^ 1, P.err))) break;
@@ -371,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const RowGqaPa
         uint8_t* dst = sKV + b * kTileBytes;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int key = 16 * i + (lt >> 3), c = 2 * (lt & 7);
+          const int key = 16 * i + (lt >> 3);
           uint32_t w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w}, h[8];
           if (slot >= 0) {
             bool odd = false;
@@ -387,8 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const RowGqaPa
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) e4m3x4_to_f16x2x2(w[e], h[2 * e], h[2 * e + 1]);
-          *reinterpret_cast<uint4*>(dst + tile_byte(key, c)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(dst + tile_byte(key, c + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+          *reinterpret_cast<uint4*>(dst + dst0 + 2048 * i) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst + dst1 + 2048 * i) = make_uint4(h[4], h[5], h[6], h[7]);
         }
         fence_proxy_async_smem();
         mbar_arrive(&sh.full[b]);
@@ -398,9 +449,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const RowGqaPa
     }
     if (lt == 0) sh.poison_n = min(masked_n, kPoison);
     mbar_arrive(&sh.loads_done);
-  } else if (warp == 12) {
+  } else if (warp >= 12) {
     // ------------------------------------------------------------ MMA
-    if (lane == 0) {
+    regs_down<kMmaRegs>();
+    if (warp == 12 && lane == 0) {
       constexpr uint32_t fmt = KVT == 0 ? 1u : 0u;  // bf16 or f16
       const uint32_t id_s = umma_idesc(fmt, 128, 128);
       const uint32_t id_o = id_s | (1u << 16);      // B is N-major
@@ -469,8 +521,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const RowGqaPa
       umma_commit(&sh.o_full);
     }
     __syncwarp();
-  } else if (warp < 8 && (warp < 4 || two)) {
+  } else if (warp < 4 || two) {
     // ------------------------------------------------------------ softmax
+    regs_up<kSoftmaxRegs>();
     const int x = warp >> 2, m = tid;  // M row m & 127 of tile x
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + 128 * x + lanes, to = tmem + 256 + 128 * x + lanes;
@@ -633,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const RowGqaPa
 }
 
 template <int KVT>
-cudaError_t launch_kind(const RowGqaParams& p, const dim3& grid, cudaStream_t stream) {
+cudaError_t launch_kind(const RowGqaParams& p, const CUtensorMap& tmap, const dim3& grid, cudaStream_t stream) {
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -643,7 +696,7 @@ cudaError_t launch_kind(const RowGqaParams& p, const dim3& grid, cudaStream_t st
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  return launch_kernel(window_tile_kernel<KVT>, grid, dim3(kThreads), kSmem, stream, false, p);
+  return launch_kernel(window_tile_kernel<KVT>, grid, dim3(kThreads), kSmem, stream, false, tmap, p);
 }
 
 }  // namespace
@@ -661,16 +714,16 @@ int window_tile_splits(int rows, int hkv, int group, long long max_tokens, int s
   return s < 1 ? 1 : static_cast<int>(s);
 }
 
-cudaError_t launch_window_tile(const RowGqaParams& p, cudaStream_t stream) {
+cudaError_t launch_window_tile(const RowGqaParams& p, const CUtensorMap& tmap, cudaStream_t stream) {
   if (p.rows == 0) return cudaSuccess;
   long long groups = static_cast<long long>(p.rows) / window_tile_rows(p.group) + p.reqs;
   if (groups > p.rows) groups = p.rows;
   const dim3 grid(static_cast<unsigned>(groups), p.hkv, p.splits);
   cudaError_t e;
   switch (p.kv_dtype) {
-    case QSA_DTYPE_BF16: e = launch_kind<0>(p, grid, stream); break;
-    case QSA_DTYPE_E4M3: e = launch_kind<1>(p, grid, stream); break;
-    default: e = launch_kind<2>(p, grid, stream); break;
+    case QSA_DTYPE_BF16: e = launch_kind<0>(p, tmap, grid, stream); break;
+    case QSA_DTYPE_E4M3: e = launch_kind<1>(p, tmap, grid, stream); break;
+    default: e = launch_kind<2>(p, tmap, grid, stream); break;
   }
   if (e != cudaSuccess || p.splits == 1) return e;
   return launch_row_merge(p, stream);
