@@ -63,14 +63,49 @@ struct TileShared {
 constexpr int kSmem = 1024 + 2 * kTileBytes + kBufs * kTileBytes + static_cast<int>(sizeof(TileShared));
 
 // ---------------------------------------------------------------- tcgen05
-// D[tmem] (+)= A[tmem] * B[smem], 16-bit inputs, fp32 accumulate
-__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// The MMAs and commits below are executed by a whole converged warp and issued
+// by the lane that elect.sync names (always the same one): their operands
+// then stay in uniform registers, and an issue costs a few cycles instead of
+// the ~120 that a lone lane's took (measured: as long as the MMA itself).
+// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit inputs, fp32 accumulate
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_addr(bar))
+      : "memory");
+}
+// The largest of three.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ unsigned long long f32x2_fma(unsigned long long a, unsigned long long b,
+                                                        unsigned long long c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ void f32x2_unpack(unsigned long long a, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a));
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -97,6 +132,8 @@ __device__ __forceinline__ int tile_byte(int r, int c) {
   return (c >> 3) * kAtom + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
+__device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
+
 // The key tiles of a CTA: those of the sinks, then those of the window.
 struct Tiles {
   int ns, w0, n;  // sink tiles, first window tile, all
@@ -114,7 +151,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   TileShared& sh = *reinterpret_cast<TileShared*>(sKV + kBufs * kTileBytes);
   constexpr int kSoftmaxRegs = KVT == 0 ? 192 : 176, kLoadRegs = KVT == 0 ? 80 : 112, kMmaRegs = 48;
   static_assert(2 * kSoftmaxRegs + kLoadRegs + kMmaRegs <= 4 * 128, "the launch's registers");
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be uniform)
   const int kvh = blockIdx.y, split = blockIdx.z;
   const int G = P.group, R = 128 / G;
   griddep_launch_dependents();
@@ -346,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           cp_async_wait<0>();
           for (; done < s; ++done) finish(done);
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(&sh.empty[b], ((s / kBufs) & 1) ^ 1, P.err))) break;
+        if (!all_ok(mbar_wait(&sh.empty[b], ((s / kBufs) & 1) ^ 1, P.err))) break;
         if (!is_v && warp == 8) publish(j, rows);
         uint8_t* dst = sKV + b * kTileBytes;
         if (tma) {
@@ -415,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           rows_next = (s >> 1) + 2 < nt ? fetch_rows(j + 2) : kUnseen;
         }
         if (s + 1 < 2 * nt) load(s + 1, rows, nxt);
-        if (!__all_sync(0xffffffffu, mbar_wait(&sh.empty[b], ((s / kBufs) & 1) ^ 1, P.err))) break;
+        if (!all_ok(mbar_wait(&sh.empty[b], ((s / kBufs) & 1) ^ 1, P.err))) break;
         if (!is_v && warp == 8) publish(j, rows_here);
         int slot = -1;
         if (is_v && tile_masked(j)) slot = open_poison(j);
@@ -452,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   } else if (warp >= 12) {
     // ------------------------------------------------------------ MMA
     regs_down<kMmaRegs>();
-    if (warp == 12 && lane == 0) {
+    if (warp == 12) {
       constexpr uint32_t fmt = KVT == 0 ? 1u : 0u;  // bf16 or f16
       const uint32_t id_s = umma_idesc(fmt, 128, 128);
       const uint32_t id_o = id_s | (1u << 16);      // B is N-major
@@ -465,35 +503,35 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
           const int off = ((kk >> 2) * kAtom + (kk & 3) * 32) >> 4;
-          umma_f16(tmem + 128 * x, a + off, b + off, id_s, kk != 0 ? 1u : 0u);
+          mma_ss(tmem + 128 * x, a + off, b + off, id_s, kk != 0 ? 1u : 0u);
         }
       };
       auto values = [&](int x, int s, bool first) {
         const uint64_t b = v0 + (((s % kBufs) * kTileBytes) >> 4);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          umma_f16_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * kk, b + ((kk * 2048) >> 4), id_o,
+          mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * kk, b + ((kk * 2048) >> 4), id_o,
                       first && kk == 0 ? 0u : 1u);
       };
       auto wait_full = [&](int s) {
-        const bool ok = mbar_wait(&sh.full[s % kBufs], (s / kBufs) & 1, P.err);
+        const bool ok = all_ok(mbar_wait(&sh.full[s % kBufs], (s / kBufs) & 1, P.err));
         tc_fence_after_sync();
         return ok;
       };
       bool ok = wait_full(0);
       if (ok) {
         scores(0, 0);
-        umma_commit(&sh.s_full[0]);
+        mma_commit(&sh.s_full[0]);
         if (two) {
           scores(1, 0);
-          umma_commit(&sh.s_full[1]);
+          mma_commit(&sh.s_full[1]);
         }
-        umma_commit(&sh.empty[0]);
+        mma_commit(&sh.empty[0]);
       }
       for (int j = 0; j < nt && ok; ++j) {
         const int sv = 2 * j + 1, sk = 2 * j + 2;
         const bool more = j + 1 < nt;
-        ok = wait_full(sv) && mbar_wait(&sh.p_ready[0], j & 1, P.err);
+        ok = wait_full(sv) && all_ok(mbar_wait(&sh.p_ready[0], j & 1, P.err));
         if (!ok) break;
         tc_fence_after_sync();
         values(0, sv, j == 0);
@@ -501,26 +539,25 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           ok = wait_full(sk);
           if (!ok) break;
           scores(0, sk);
-          umma_commit(&sh.s_full[0]);
+          mma_commit(&sh.s_full[0]);
         }
         if (two) {
-          ok = mbar_wait(&sh.p_ready[1], j & 1, P.err);
+          ok = all_ok(mbar_wait(&sh.p_ready[1], j & 1, P.err));
           if (!ok) break;
           tc_fence_after_sync();
           values(1, sv, j == 0);
         }
-        umma_commit(&sh.empty[sv % kBufs]);
+        mma_commit(&sh.empty[sv % kBufs]);
         if (more) {
           if (two) {
             scores(1, sk);
-            umma_commit(&sh.s_full[1]);
+            mma_commit(&sh.s_full[1]);
           }
-          umma_commit(&sh.empty[sk % kBufs]);
+          mma_commit(&sh.empty[sk % kBufs]);
         }
       }
-      umma_commit(&sh.o_full);
+      mma_commit(&sh.o_full);
     }
-    __syncwarp();
   } else if (warp < 4 || two) {
     // ------------------------------------------------------------ softmax
     regs_up<kSoftmaxRegs>();
@@ -539,8 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       // its masks and scales, then its scores.  (A slot's next tile is
       // published only after both softmaxes are done with this one: its K
       // waits for a ring buffer that S of tile j + 2 frees.)
-      ok = __all_sync(0xffffffffu, mbar_wait(&sh.info[slot], (j / kSlots) & 1, P.err) &&
-                                       mbar_wait(&sh.s_full[x], j & 1, P.err));
+      ok = all_ok(mbar_wait(&sh.info[slot], (j / kSlots) & 1, P.err) && mbar_wait(&sh.s_full[x], j & 1, P.err));
       if (!ok) break;
       tc_fence_after_sync();
       uint32_t r[4][32];
@@ -565,9 +601,15 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       float mx = -INFINITY;
 #pragma unroll
       for (int b = 0; b < 8; ++b) {
-        float bm = -INFINITY;
+        const uint32_t* rr = &r[b >> 1][(b & 1) * 16];
+        float bm = max3(__uint_as_float(rr[0]), __uint_as_float(rr[1]), __uint_as_float(rr[2]));
+        float b2 = max3(__uint_as_float(rr[3]), __uint_as_float(rr[4]), __uint_as_float(rr[5]));
 #pragma unroll
-        for (int i = 0; i < 16; ++i) bm = fmaxf(bm, __uint_as_float(r[b >> 1][(b & 1) * 16 + i]));
+        for (int i = 6; i < 14; i += 4) {
+          bm = max3(bm, __uint_as_float(rr[i]), __uint_as_float(rr[i + 1]));
+          b2 = max3(b2, __uint_as_float(rr[i + 2]), __uint_as_float(rr[i + 3]));
+        }
+        bm = fmaxf(max3(bm, __uint_as_float(rr[14]), __uint_as_float(rr[15])), b2);
         if constexpr (KVT == 2) {
           const float4 sc = sh.scale[slot][b];
           bm = fmaf(bm, fmaxf(qs * sc.x, kLeast), sc.y);
@@ -593,39 +635,46 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         ref = mn;
       }
       const float neg = ref == -INFINITY ? 0.f : -ref;
+      unsigned long long sum2 = 0ull;  // (two sums, of even and odd keys)
       float sum = 0.f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t pk[32];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          float c = qs, base = neg, bs = 0.f;
-          float inv_vs = 1.0f;
+          float c = qs, base = neg, inv_vs = 1.0f;
           if constexpr (KVT == 2) {
             const float4 sc = sh.scale[slot][4 * h + b];
             c = fmaxf(c * sc.x, kLeast);
             base += sc.y;
             inv_vs = sc.z;
           }
+          const unsigned long long c2 = f32x2_pack(c, c), base2 = f32x2_pack(base, base);
+          unsigned long long bs2 = KVT == 2 ? 0ull : sum2;
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
             const uint32_t* rr = &r[2 * h + (b >> 1)][(b & 1) * 16 + i];
-            const float p0 = ex2_ftz(fmaf(__uint_as_float(rr[0]), c, base));
-            const float p1 = ex2_ftz(fmaf(__uint_as_float(rr[1]), c, base));
-            bs += p0 + p1;
+            float p0, p1;
+            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(rr[0]), __uint_as_float(rr[1])), c2, base2), p0, p1);
+            p0 = ex2_ftz(p0);
+            p1 = ex2_ftz(p1);
+            bs2 = f32x2_add(bs2, f32x2_pack(p0, p1));
             pk[8 * b + (i >> 1)] = KVT == 0 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
           }
-          sum = fmaf(bs, inv_vs, sum);
+          if constexpr (KVT == 2)
+            sum = fmaf(f32x2_hsum(bs2), inv_vs, sum);
+          else
+            sum2 = bs2;
         }
         tmem_st32(ts + 32 * h, pk);
       }
-      l += sum;
+      l += KVT == 2 ? sum : f32x2_hsum(sum2);
       tmem_wait_st();
       tc_fence_before_sync();
       mbar_arrive(&sh.p_ready[x]);
     }
     // ---- output
-    ok = __all_sync(0xffffffffu, ok && mbar_wait(&sh.o_full, 0, P.err) && mbar_wait(&sh.loads_done, 0, P.err));
+    ok = all_ok(ok && mbar_wait(&sh.o_full, 0, P.err) && mbar_wait(&sh.loads_done, 0, P.err));
     tc_fence_after_sync();
     const int im = m & 127, rr = x * R + im / G;
     const bool act = ok && im < R * G && rr < nrows;
