@@ -92,6 +92,15 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
           smem_addr(bar))
       : "memory");
 }
+// One box of a 2-D map, issued likewise.
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int32_t x, int32_t y, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
 // The largest of three.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -392,14 +401,14 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
             mbar_arrive_expect_tx(&sh.full[b], kTileBytes);
           else
             mbar_arrive(&sh.full[b]);
+          __syncwarp();
           if (warp == 8) {
-            // a lane per box: 64 dims of P.box keys
-            const int per = 128 / P.box, k = lane % per, atom = lane / per;
-            const uint32_t r = __shfl_sync(0xffffffffu, rows, (k * P.box) >> 4);
-            __syncwarp();
-            if (atom < 2)
-              tma_load_2d(dst + atom * kAtom + k * P.box * 128, &tmap, is_v * 128 + atom * 64,
-                          static_cast<int>(r), &sh.full[b]);
+            // boxes of 64 dims of P.box keys
+            for (int k = 0; k < 128; k += P.box) {
+              const int r = static_cast<int>(__shfl_sync(0xffffffffu, rows, k >> 4));
+              tma_box(dst + k * 128, &tmap, is_v * 128, r, &sh.full[b]);
+              tma_box(dst + kAtom + k * 128, &tmap, is_v * 128 + 64, r, &sh.full[b]);
+            }
           }
           done = s + 1;
           continue;
