@@ -90,6 +90,20 @@ bool encode_bf16_2d(CUtensorMap* map, const void* base, long long inner, long lo
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 2-D map over [outer, 256 bytes] with a box of 128 bytes x box_rows rows,
+// 128-byte swizzle (an e4m3 cache: K, then V).
+bool encode_codes_2d(CUtensorMap* map, const void* base, long long outer, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {256, static_cast<cuuint64_t>(outer)};
+  cuuint64_t strides[1] = {256};
+  cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool pow2(long long x) { return x > 0 && (x & (x - 1)) == 0; }
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -679,13 +693,15 @@ qsa_status do_window(const qsa_gqa_cfg* g, const qsa_window_args* a, void* ws, s
   st = place_splits(&p, g, plan.splits, ws, ws_bytes);
   if (st != QSA_OK) return st;
   if (!plan.tile) return cuda_status(launch_row_gqa(p, stream));
-  // boxes of the page's keys, up to a tile: pages of a multiple of 32 (row
-  // coordinates are int32)
+  // boxes of the page's keys, up to a tile: pages of a multiple of 32 (the
+  // SM's TMA unit takes ~90 cycles a box; row coordinates are int32)
   CUtensorMap tmap{};
   const long long cache_rows = static_cast<long long>(p.num_blocks) * p.hkv * p.page;
-  if (p.kv_dtype == QSA_DTYPE_BF16 && p.page % 32 == 0 && cache_rows < (1ll << 31)) {
+  if (p.page % 32 == 0 && cache_rows < (1ll << 31)) {
     p.box = p.page % 128 == 0 ? 128 : p.page % 64 == 0 ? 64 : 32;
-    if (!encode_bf16_2d(&tmap, a->kv, 256, cache_rows, p.box)) return QSA_ERR_CUDA;
+    if (!(p.kv_dtype == QSA_DTYPE_BF16 ? encode_bf16_2d(&tmap, a->kv, 256, cache_rows, p.box)
+                                       : encode_codes_2d(&tmap, a->kv, cache_rows, p.box)))
+      return QSA_ERR_CUDA;
   }
   return cuda_status(launch_window_tile(p, tmap, stream));
 }

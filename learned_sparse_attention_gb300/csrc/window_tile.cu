@@ -12,21 +12,29 @@
 // Roles, 16 warps:
 //   0-3, 4-7  softmax of tile A, B: S from TMEM, masks on the tiles that need
 //             them, P back over S's columns, at the end the gated output;
-//   8-11      load K and V tiles of 128 keys through the block table into a
-//             ring (128-byte swizzle): bf16 by TMA or cp.async; e4m3 codes
-//             through registers, as f16 (exact).  Keys that no row of the CTA sees
-//             become zeros, whatever the cache holds there;
+//   8-11      load what needs a thread's hand: key tiles that some row does
+//             not see, or that lie on small pages (keys that no row of the
+//             CTA sees become zeros, whatever the cache holds there), and the
+//             V tiles of e4m3 caches, as f16 (exact);
 //   12        issues the MMAs: S_A(j+1) right after O_A(j), so the softmax of
-//             one tile runs under the products of the other.
+//             one tile runs under the products of the other;
+//   13        loads the other tiles by TMA.  It alone waits for K's ring buffers
+//             (bf16: V's too) to be free, in order, and hands the buffer of a
+//             tile that is not its own to warps 8-11.
 // TMEM: S_A, S_B, O_A, O_B of 128 columns each.  P is the A operand from
 // TMEM; V is the N-major B operand of the ring tile as it is stored.
-// e4m3 caches: Q enters as f16 times a power of two per row; K's block scales
-// multiply the scores and V's enter the exponent, as in row_gqa.cu.
+// e4m3 caches: K's codes are multiplied as they are, by q split into two e4m3
+// terms hi + lo (after a power of two per row that puts its largest |q| into
+// [128, 256): exact but for elements below 2^-10 of it, off by at most 2^-18
+// of it there); P and V are f16.  K's block scales multiply the scores and
+// V's enter the exponent, as in row_gqa.cu.
 //
 // A V element that is not finite in a tile that some rows do not see would
 // reach them as 0 * inf: such elements are zeroed in the ring, remembered by
 // key, and added to the rows that see them at the end.
 // Every wait is bounded (mbar_wait); a timeout sets the error word.
+#include <cuda_fp16.h>
+
 #include <climits>
 
 #include "kv_scale.cuh"
@@ -40,27 +48,36 @@ namespace qsa {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kTileBytes = 128 * 256;  // 128 rows of 128 16-bit values, two 64-dim atoms
+constexpr int kTile = 128 * 256;  // bytes of 128 rows of 128 16-bit values, two 64-dim atoms
 constexpr int kAtom = 128 * 128;
-constexpr int kBufs = 4;
 constexpr int kSlots = 4;        // tiles whose scales and page masks are kept
 constexpr int kPoison = 32;      // masked tiles that can remember odd V elements
 constexpr float kUp = 8.0f;
 constexpr float kLeast = 1.2e-38f;  // a score's factor is never 0: masked scores are -inf
 
+// The rings.  K tiles of e4m3 caches stay codes: half the size.
+template <int KVT>
+struct Rings {
+  static constexpr int NK = KVT == 0 ? 2 : 3, NV = KVT == 0 ? 2 : 3;
+  static constexpr int kKey = KVT == 0 ? kTile : kAtom;
+  static_assert(kSlots > NK, "a slot is rewritten only after its tile's softmax");
+};
+
 struct TileShared {
-  uint64_t full[kBufs], empty[kBufs], info[kSlots], s_full[2], p_ready[2], o_full, loads_done;
+  uint64_t kfull[3], kempty[3], kgo[3], vfull[3], vempty[3], vgo[3], info[kSlots], s_full[2], p_ready[2], q_ready, o_full, loads_done;
   uint32_t tmem;
   int poison_n;
   int poison_tile[kPoison];        // first key
   uint32_t poison[kPoison][4];     // keys with an odd V element
   uint32_t valid[kSlots][4];       // keys on pages of the cache
   int check[kSlots];               // some key is not
-  float4 scale[kSlots][8];         // ks, log2 vs, 1 / vs of each 16 keys
-  float qs[256];                   // per M row: what its scores are multiplied by
+  alignas(16) uint32_t scale[kSlots][8];  // of each 16 keys, two bf16: ks, and log2 vs above it
+  float qs[256];                   // per M row: what its scores are multiplied by (< 0: the row is a NaN)
   int pos[256];                    // its position (-1: before the start; INT_MIN: no row)
 };
-constexpr int kSmem = 1024 + 2 * kTileBytes + kBufs * kTileBytes + static_cast<int>(sizeof(TileShared));
+template <int KVT>
+constexpr int kSmem = 1024 + 2 * kTile + Rings<KVT>::NK * Rings<KVT>::kKey + Rings<KVT>::NV * kTile +
+                      static_cast<int>(sizeof(TileShared));
 
 // ---------------------------------------------------------------- tcgen05
 // The MMAs and commits below are executed by a whole converged warp and issued
@@ -73,6 +90,15 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a_desc, uint64_t b_d
   asm volatile(
       "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Same for e4m3 x e4m3
+__device__ __forceinline__ void mma_ss_e4m3(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -100,6 +126,23 @@ __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int32
       " [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(smem_addr(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
       : "memory");
+}
+// Whether the phase with the given parity is complete, without waiting.
+__device__ __forceinline__ bool mbar_done(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// n arrivals at once
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(n)
+               : "memory");
 }
 // The largest of three.
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -137,10 +180,18 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 // Byte of 16-byte chunk c (8 dims) of row r in a swizzled two-atom tile.
-__device__ __forceinline__ int tile_byte(int r, int c) {
+__device__ __forceinline__ constexpr int tile_byte(int r, int c) {
   return (c >> 3) * kAtom + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
+// The n lowest bits (none for n <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
 __device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
 
 // The key tiles of a CTA: those of the sinks, then those of the window.
@@ -156,9 +207,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   __shared__ int s_pmin, s_pmax, s_neg;
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   uint8_t* sQ = smem_raw + pad;
-  uint8_t* sKV = sQ + 2 * kTileBytes;
-  TileShared& sh = *reinterpret_cast<TileShared*>(sKV + kBufs * kTileBytes);
-  constexpr int kSoftmaxRegs = KVT == 0 ? 192 : 176, kLoadRegs = KVT == 0 ? 80 : 112, kMmaRegs = 48;
+  using RG = Rings<KVT>;
+  uint8_t* sK = sQ + 2 * kTile;
+  uint8_t* sV = sK + RG::NK * RG::kKey;
+  TileShared& sh = *reinterpret_cast<TileShared*>(sV + RG::NV * kTile);
+  constexpr int kSoftmaxRegs = KVT == 0 ? 192 : 184, kLoadRegs = KVT == 0 ? 80 : 96, kMmaRegs = 48;
   static_assert(2 * kSoftmaxRegs + kLoadRegs + kMmaRegs <= 4 * 128, "the launch's registers");
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be uniform)
@@ -219,15 +272,20 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   }
 
   if (tid == 0) {
-    for (int i = 0; i < kBufs; ++i) {
-      mbar_init(&sh.full[i], 128);
-      mbar_init(&sh.empty[i], 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&sh.kfull[i], 4);  // a lane of each loading warp, or the TMA warp's for all
+      mbar_init(&sh.vfull[i], 4);
+      mbar_init(&sh.kempty[i], 1);
+      mbar_init(&sh.vempty[i], 1);
+      mbar_init(&sh.kgo[i], 1);
+      mbar_init(&sh.vgo[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_ready[i], 128);
     }
     for (int i = 0; i < kSlots; ++i) mbar_init(&sh.info[i], 1);
+    mbar_init(&sh.q_ready, two ? 8 : 4);
     mbar_init(&sh.o_full, 1);
     mbar_init(&sh.loads_done, 128);
     fence_barrier_init();
@@ -236,101 +294,73 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
-  // ---- Q, a half-warp per M row
-  for (int m = tid >> 4; m < 256; m += kThreads / 16) {
-    const int lane16 = tid & 15, im = m & 127;
-    const int r = (m >> 7) * R + im / G;
-    const bool act = im < R * G && r < nrows;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (act)
-      v = *reinterpret_cast<const uint4*>(P.q + (static_cast<long long>(row0 + r) * P.hq + kvh * G + im % G) * 128 + 8 * lane16);
-    float qs = 0.08838834764831845f * kLog2e;
-    if constexpr (KVT != 0) {
-      // f16 times a power of two that brings the row's largest |q| into
-      // [2^14, 2^15): exact down to 2^-28 of it
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      float x[8], peak = 0.f;
-      bool odd = false;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] = e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
-        odd |= !(fabsf(x[e]) <= 3.39e38f);
-        peak = fmaxf(peak, fabsf(x[e]));
-      }
-#pragma unroll
-      for (int o = 8; o >= 1; o >>= 1) {
-        peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, o));
-        odd |= __shfl_xor_sync(0xffffffffu, static_cast<int>(odd), o) != 0;
-      }
-      const int e = peak > 0.f ? max(__float_as_int(peak) >> 23, 1) - 127 - 14 : 0;
-      const float f0 = exp2i(-(e / 2)), f1 = exp2i(-(e - e / 2));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = odd ? 0.f : x[i] * f0 * f1;
-      v = make_uint4(pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3]), pack_f16x2(x[4], x[5]), pack_f16x2(x[6], x[7]));
-      qs = fmaxf(exp2i(e / 2) * (qs * (KVT == 1 ? P.k_scale : 1.0f)) * exp2i(e - e / 2), kLeast);
-      if (odd) qs = -1.0f;  // (the row's result is a NaN)
-    }
-    *reinterpret_cast<uint4*>(sQ + (m >> 7) * kTileBytes + tile_byte(im, lane16)) = v;
-    if (lane16 == 0) {
-      sh.qs[m] = qs;
-      sh.pos[m] = act ? max(P.logical[row0 + r], -1) : INT_MIN;
-    }
-  }
-  fence_proxy_async_smem();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = sh.tmem;
 
+  const int32_t* bt_row = P.block_table + static_cast<long long>(req) * P.bt_stride;
+  const uint8_t* kvb = static_cast<const uint8_t*>(P.kv);
+  constexpr int kRow = KVT == 0 ? 512 : 256;  // bytes of a token and KV head
+  const bool page_pow2 = (P.page & (P.page - 1)) == 0;
+  const int page_shift = __ffs(P.page) - 1;
+  auto seen = [&](int key) { return key <= pmax && (key >= wlo || key < P.sinks); };
+  // some row of the CTA does not see all of tile j
+  auto tile_masked = [&](int j) {
+    const int kb = T.first_key(j);
+    return neg || !((kb >= wlo_all || kb + 127 < P.sinks) && kb + 127 <= pmin);
+  };
+  // Page id, then cache row, of the first key of 16-key block (lane & 7) of
+  // tile j; kUnseen where there is nothing to see, kNoPage where the page is
+  // none.
+  constexpr uint32_t kUnseen = 0xFFFFFFFFu, kNoPage = 0xFFFFFFFEu;
+  auto block_key = [&](int j) { return T.first_key(j) + 16 * (lane & 7); };
+  auto fetch_page = [&](int j) -> int {
+    const int k0 = block_key(j);
+    if (!(k0 <= pmax && (k0 + 15 >= wlo || k0 < P.sinks))) return -1;
+    const int blk = page_pow2 ? k0 >> page_shift : k0 / P.page;
+    return blk < P.bt_stride ? bt_row[blk] : -1;
+  };
+  auto to_row = [&](int j, int page) -> uint32_t {
+    const int k0 = block_key(j);
+    if (!(k0 <= pmax && (k0 + 15 >= wlo || k0 < P.sinks))) return kUnseen;
+    if (page < 0 || page >= P.num_blocks) return kNoPage;
+    const int blk = page_pow2 ? k0 >> page_shift : k0 / P.page;
+    return (static_cast<uint32_t>(page) * P.hkv + kvh) * static_cast<uint32_t>(P.page) + (k0 - blk * P.page);
+  };
+  // Tiles that every row sees and whose pages hold whole boxes come by TMA
+  // (both loaders find the same answer).
+  auto by_tma = [&](int j, uint32_t rows) {
+    return P.box != 0 && !tile_masked(j) && all_ok(rows < kNoPage);
+  };
+  auto scale_word = [&](uint32_t rows) -> uint32_t {
+    if (KVT != 2 || rows >= kNoPage) return 0x7F7Fu;
+    return *reinterpret_cast<const uint16_t*>(P.scales + 2ll * (rows / P.scale_block));
+  };
+  // what the softmax needs to know of tile number i, before its K is announced
+  auto publish = [&](int i, uint32_t rows, uint32_t scales) {
+    const int slot = i % kSlots;
+    const unsigned bad = __ballot_sync(0xffffffffu, rows == kNoPage) & 0xFFu;
+    if (bad != 0u && lane < 4) {
+      const unsigned two_blocks = (bad >> (2 * lane)) & 3u;
+      sh.valid[slot][lane] = ~(((two_blocks & 1u) ? 0xFFFFu : 0u) | ((two_blocks & 2u) ? 0xFFFF0000u : 0u));
+    }
+    if (KVT == 2 && lane < 8) {
+      const int ek = scale_exp(scales & 0xFF), ev = scale_exp(scales >> 8);
+      sh.scale[slot][lane] = pack_bf16x2(exp2i(ek), static_cast<float>(ev));
+    }
+    if (lane == 0) {
+      sh.check[slot] = bad != 0u;
+      if (bad) flag_error(P.err);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.info[slot]);
+  };
+
   if (warp >= 8 && warp < 12) {
-    // ------------------------------------------------------------ loads
+    // ------------------------------------------------------------ loads by hand
     regs_down<kLoadRegs>();
     const int lt = tid - 256;  // 0 .. 127
-    const int32_t* bt_row = P.block_table + static_cast<long long>(req) * P.bt_stride;
-    const uint8_t* kvb = static_cast<const uint8_t*>(P.kv);
-    const bool page_pow2 = (P.page & (P.page - 1)) == 0;
-    const int page_shift = __ffs(P.page) - 1;
-    auto seen = [&](int key) { return key <= pmax && (key >= wlo || key < P.sinks); };
-    // cache row of the first key of 16-key block (lane & 7) of tile j, or
-    // kUnseen: nothing to see there, or kNoPage: a page that is none
-    constexpr uint32_t kUnseen = 0xFFFFFFFFu, kNoPage = 0xFFFFFFFEu;
-    auto fetch_rows = [&](int j) -> uint32_t {
-      const int k0 = T.first_key(j) + 16 * (lane & 7);
-      if (!(k0 <= pmax && (k0 + 15 >= wlo || k0 < P.sinks))) return kUnseen;
-      const int blk = page_pow2 ? k0 >> page_shift : k0 / P.page;
-      const int pid = blk < P.bt_stride ? bt_row[blk] : -1;
-      if (pid < 0 || pid >= P.num_blocks) return kNoPage;
-      return (static_cast<uint32_t>(pid) * P.hkv + kvh) * static_cast<uint32_t>(P.page) + (k0 - blk * P.page);
-    };
-    // the masks and scales of tile j, by one warp, before its K is announced
-    auto publish = [&](int j, uint32_t rows) {
-      const int slot = (j - j0) % kSlots;
-      const unsigned bad = __ballot_sync(0xffffffffu, rows == kNoPage) & 0xFFu;
-      if (lane < 4) {
-        const unsigned two_blocks = (bad >> (2 * lane)) & 3u;
-        sh.valid[slot][lane] = ~(((two_blocks & 1u) ? 0xFFFFu : 0u) | ((two_blocks & 2u) ? 0xFFFF0000u : 0u));
-      }
-      if (lane == 0) {
-        sh.check[slot] = bad != 0u;
-        if (bad) flag_error(P.err);
-      }
-      if (KVT == 2 && lane < 8) {
-        int ek = 0, ev = 0;
-        if (rows < kNoPage) {
-          const uint16_t w = *reinterpret_cast<const uint16_t*>(P.scales + 2ll * (rows / P.scale_block));
-          ek = scale_exp(w & 0xFF);
-          ev = scale_exp(w >> 8);
-        }
-        sh.scale[slot][lane] = make_float4(exp2i(ek), static_cast<float>(ev), exp2i(-ev), 0.f);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.info[slot]);
-    };
-    // zeroes odd V elements of a masked tile and remembers their keys
-    auto tile_masked = [&](int j) {
-      const int kb = T.first_key(j);
-      return neg || !((kb >= wlo_all || kb + 127 < P.sinks) && kb + 127 <= pmin);
-    };
     int masked_n = 0;
     auto remember = [&](int slot, int key) {
       if (slot < kPoison) atomicOr(&sh.poison[slot][key >> 5], 1u << (key & 31));
@@ -340,159 +370,183 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       if (lt == 0 && masked_n < kPoison) sh.poison_tile[masked_n] = T.first_key(j);
       return masked_n++;
     };
+    auto announce = [&](uint64_t* bar) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    // the buffer of tile number i, from warp 13 (a buffer is handed over again
+    // only once its tile has been loaded and read)
+    uint32_t k_turn = 0u, v_turn = 0u;
+    auto wait_turn = [&](uint64_t* bars, uint32_t& turns, int b) {
+      const bool ok = all_ok(mbar_wait(&bars[b], (turns >> b) & 1u, P.err));
+      turns ^= 1u << b;
+      return ok;
+    };
+    // 128 keys' K or V by cp.async: CH 16-byte chunks a key
+    auto copy = [&](uint8_t* dst, const uint8_t* src, uint32_t rows, int kb, bool masked, auto chunks) {
+      constexpr int CH = decltype(chunks)::value, PER = 128 / CH;  // keys a pass
+      const int c = lt % CH, k0 = lt / CH;
+      uint32_t base[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) base[i] = __shfl_sync(0xffffffffu, rows, i);
+      uint8_t* d = dst + tile_byte(k0, c);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const uint32_t r = base[i * PER / 16];
+        const int key = i * PER + k0;
+        const bool ok = r < kNoPage && (!masked || seen(kb + key));
+        cp_async16(d + i * PER * 128, src + c * 16 + static_cast<unsigned long long>(ok ? r + (key & 15) : 0u) * kRow,
+                   ok ? 16u : 0u);
+      }
+      cp_async_commit();
+    };
+    int page_n = nt > 1 ? fetch_page(j0 + 1) : -1;
+    uint32_t rows = to_row(j0, fetch_page(j0));
 
     if constexpr (KVT == 0) {
-      // Tiles that every row sees come by TMA where a box holds at least 32
-      // keys of a page (P.box; the SM's TMA unit takes ~90 cycles a box,
-      // whatever its size, and a K and V tile have 2048 cycles between them);
-      // the others by cp.async, which zeroes what is not seen.
-      constexpr int LAG = 2;  // tiles in flight behind the one being issued
-      uint32_t rows = fetch_rows(j0), rows_next = kUnseen;
-      auto finish = [&](int s) {  // tile s has landed
-        const int j = j0 + (s >> 1), b = s % kBufs;
-        if ((s & 1) && tile_masked(j)) {
-          const int slot = open_poison(j);
+      // zeroes odd V elements of masked tile j and remembers their keys
+      auto clean = [&](int j, uint8_t* tile) {
+        const int slot = open_poison(j);
 #pragma unroll 4
-          for (int i = 0; i < 16; ++i) {
-            const int key = 8 * i + (lt >> 4);
-            uint4* p = reinterpret_cast<uint4*>(sKV + b * kTileBytes + tile_byte(key, lt & 15));
-            uint4 v = *p;
-            uint32_t w[4] = {v.x, v.y, v.z, v.w}, odd = 0u;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if ((w[e] & 0x7F80u) == 0x7F80u) {
-                w[e] &= 0xFFFF0000u;
-                odd = 1u;
-              }
-              if ((w[e] & 0x7F800000u) == 0x7F800000u) {
-                w[e] &= 0xFFFFu;
-                odd = 1u;
-              }
-            }
-            if (odd) {
-              *p = make_uint4(w[0], w[1], w[2], w[3]);
-              remember(slot, key);
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&sh.full[b]);
-      };
-      int done = 0;  // tiles announced
-      const int dst0 = tile_byte(lt >> 4, lt & 15);
-      for (int s = 0; s < 2 * nt; ++s) {
-        const int j = j0 + (s >> 1), b = s % kBufs, is_v = s & 1;
-        if (!is_v) {
-          if (s > 0) rows = rows_next;
-          rows_next = (s >> 1) + 1 < nt ? fetch_rows(j + 1) : kUnseen;
-        }
-        const int kb = T.first_key(j);
-        const bool masked = tile_masked(j);
-        const bool tma = P.box != 0 && !masked && __all_sync(0xffffffffu, rows < kNoPage);
-        if (tma && done < s) {
-          cp_async_wait<0>();
-          for (; done < s; ++done) finish(done);
-        }
-        if (!all_ok(mbar_wait(&sh.empty[b], ((s / kBufs) & 1) ^ 1, P.err))) break;
-        if (!is_v && warp == 8) publish(j, rows);
-        uint8_t* dst = sKV + b * kTileBytes;
-        if (tma) {
-          if (lt == 0)
-            mbar_arrive_expect_tx(&sh.full[b], kTileBytes);
-          else
-            mbar_arrive(&sh.full[b]);
-          __syncwarp();
-          if (warp == 8) {
-            // boxes of 64 dims of P.box keys
-            for (int k = 0; k < 128; k += P.box) {
-              const int r = static_cast<int>(__shfl_sync(0xffffffffu, rows, k >> 4));
-              tma_box(dst + k * 128, &tmap, is_v * 128, r, &sh.full[b]);
-              tma_box(dst + kAtom + k * 128, &tmap, is_v * 128 + 64, r, &sh.full[b]);
-            }
-          }
-          done = s + 1;
-          continue;
-        }
-        const uint8_t* src = kvb + is_v * 256 + (lt & 15) * 16;
-        uint32_t base[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) base[i] = __shfl_sync(0xffffffffu, rows, i);
-#pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int key = 8 * i + (lt >> 4);
-          const uint32_t r = base[i >> 1];
-          const bool ok = r < kNoPage && (!masked || seen(kb + key));
-          cp_async16(dst + dst0 + i * 1024, src + static_cast<unsigned long long>(ok ? r + (key & 15) : 0u) * 512,
-                     ok ? 16u : 0u);
+          uint4* p = reinterpret_cast<uint4*>(tile + tile_byte(key, lt & 15));
+          uint4 v = *p;
+          uint32_t w[4] = {v.x, v.y, v.z, v.w}, odd = 0u;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if ((w[e] & 0x7F80u) == 0x7F80u) {
+              w[e] &= 0xFFFF0000u;
+              odd = 1u;
+            }
+            if ((w[e] & 0x7F800000u) == 0x7F800000u) {
+              w[e] &= 0xFFFFu;
+              odd = 1u;
+            }
+          }
+          if (odd) {
+            *p = make_uint4(w[0], w[1], w[2], w[3]);
+            remember(slot, key);
+          }
         }
-        cp_async_commit();
-        if (s - done >= LAG) {
-          cp_async_wait<LAG>();
-          finish(done++);
+      };
+      // a tile's K is announced once its V is on the way, its V once the next
+      // tile's K is (or when the next tile comes by TMA)
+      int v_open = -1;  // tile number whose V is on the way
+      auto finish_v = [&]() {
+        const int i = v_open;
+        v_open = -1;
+        if (tile_masked(j0 + i)) clean(j0 + i, sV + (i % RG::NV) * kTile);
+        announce(&sh.vfull[i % RG::NV]);
+      };
+      for (int i = 0; i < nt; ++i) {
+        const int j = j0 + i, kb = T.first_key(j);
+        const uint32_t here = rows;
+        if (i + 1 < nt) rows = to_row(j + 1, page_n);
+        page_n = i + 2 < nt ? fetch_page(j + 2) : -1;
+        if (by_tma(j, here)) {
+          if (v_open >= 0) {
+            cp_async_wait<0>();
+            finish_v();
+          }
+          continue;
         }
+        const bool masked = tile_masked(j);
+        if (v_open >= 0 && !all_ok(mbar_done(&sh.kgo[i % RG::NK], (k_turn >> (i % RG::NK)) & 1u))) {
+          cp_async_wait<0>();  // (nothing to start meanwhile)
+          finish_v();
+        }
+        if (!wait_turn(sh.kgo, k_turn, i % RG::NK)) break;
+        if (warp == 8) publish(i, here, 0u);
+        copy(sK + (i % RG::NK) * kTile, kvb, here, kb, masked, Int<16>());
+        if (v_open >= 0) {
+          cp_async_wait<1>();
+          finish_v();
+        }
+        if (!wait_turn(sh.vgo, v_turn, i % RG::NV)) break;
+        copy(sV + (i % RG::NV) * kTile, kvb + 256, here, kb, masked, Int<16>());
+        v_open = i;
+        cp_async_wait<1>();
+        announce(&sh.kfull[i % RG::NK]);
       }
       cp_async_wait<0>();
-      for (; done < 2 * nt; ++done) finish(done);
+      if (v_open >= 0) finish_v();
     } else {
-      // 16 codes a lane and load; the next tile's codes are in flight while
+      // V: 16 codes a lane and load; the next tile's codes are in flight while
       // this one's are converted
-      auto load = [&](int s, uint32_t rows, uint4 (&v)[8]) {
-        const int j = j0 + (s >> 1), kb = T.first_key(j);
+      auto load = [&](int j, uint32_t r, uint4 (&v)[8]) {
+        const int kb = T.first_key(j);
         const bool masked = tile_masked(j);
-        const uint8_t* src = kvb + (s & 1) * 128 + (lt & 7) * 16;
+        const uint8_t* src = kvb + 128 + (lt & 7) * 16;
         uint32_t base[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) base[i] = __shfl_sync(0xffffffffu, rows, i);
+        for (int i = 0; i < 8; ++i) base[i] = __shfl_sync(0xffffffffu, r, i);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const bool ok = base[i] < kNoPage && (!masked || seen(kb + 16 * i + (lt >> 3)));
           v[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (ok) v[i] = *reinterpret_cast<const uint4*>(src + static_cast<unsigned long long>(base[i] + (lt >> 3)) * 256);
+          if (ok) v[i] = *reinterpret_cast<const uint4*>(src + static_cast<unsigned long long>(base[i] + (lt >> 3)) * kRow);
         }
       };
-      uint32_t rows = fetch_rows(j0), rows_next = nt > 1 ? fetch_rows(j0 + 1) : kUnseen;
+      auto start_k = [&](int i, uint32_t r) {  // false: a wait gave up
+        if (by_tma(j0 + i, r)) return true;
+        if (!wait_turn(sh.kgo, k_turn, i % RG::NK)) return false;
+        if (warp == 8) publish(i, r, scale_word(r));
+        copy(sK + (i % RG::NK) * RG::kKey, kvb, r, T.first_key(j0 + i), tile_masked(j0 + i), Int<8>());
+        return true;
+      };
+      auto end_k = [&](int i, uint32_t r) {
+        if (by_tma(j0 + i, r)) return;
+        cp_async_wait<0>();
+        announce(&sh.kfull[i % RG::NK]);
+      };
       uint4 cur[8], nxt[8];
-      load(0, rows, cur);
+      load(j0, rows, cur);
+      bool ok = start_k(0, rows);
+      if (ok) end_k(0, rows);
       const int dst0 = tile_byte(lt >> 3, 2 * (lt & 7)), dst1 = tile_byte(lt >> 3, 2 * (lt & 7) + 1);
-      for (int s = 0; s < 2 * nt; ++s) {
-        const int j = j0 + (s >> 1), b = s % kBufs, is_v = s & 1;
-        const uint32_t rows_here = rows;
-        if (is_v) {  // the next load is the next tile's K
-          rows = rows_next;
-          rows_next = (s >> 1) + 2 < nt ? fetch_rows(j + 2) : kUnseen;
+      for (int i = 0; i < nt && ok; ++i) {
+        const int j = j0 + i;
+        const bool more = i + 1 < nt;
+        if (more) {
+          rows = to_row(j + 1, page_n);
+          page_n = i + 2 < nt ? fetch_page(j + 2) : -1;
+          load(j + 1, rows, nxt);
+          ok = start_k(i + 1, rows);
+          if (!ok) break;
         }
-        if (s + 1 < 2 * nt) load(s + 1, rows, nxt);
-        if (!all_ok(mbar_wait(&sh.empty[b], ((s / kBufs) & 1) ^ 1, P.err))) break;
-        if (!is_v && warp == 8) publish(j, rows_here);
-        int slot = -1;
-        if (is_v && tile_masked(j)) slot = open_poison(j);
-        uint8_t* dst = sKV + b * kTileBytes;
+        ok = all_ok(mbar_wait(&sh.vempty[i % RG::NV], ((i / RG::NV) & 1) ^ 1, P.err));
+        if (!ok) break;
+        const int slot = tile_masked(j) ? open_poison(j) : -1;
+        uint8_t* dst = sV + (i % RG::NV) * kTile;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int key = 16 * i + (lt >> 3);
-          uint32_t w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w}, h[8];
+        for (int q = 0; q < 8; ++q) {
+          const int key = 16 * q + (lt >> 3);
+          uint32_t w[4] = {cur[q].x, cur[q].y, cur[q].z, cur[q].w}, h[8];
           if (slot >= 0) {
             bool odd = false;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll
-              for (int q = 0; q < 32; q += 8)
-                if (((w[e] >> q) & 0x7Fu) == 0x7Fu) {
-                  w[e] &= ~(0xFFu << q);
+              for (int c = 0; c < 32; c += 8)
+                if (((w[e] >> c) & 0x7Fu) == 0x7Fu) {
+                  w[e] &= ~(0xFFu << c);
                   odd = true;
                 }
             if (odd) remember(slot, key);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) e4m3x4_to_f16x2x2(w[e], h[2 * e], h[2 * e + 1]);
-          *reinterpret_cast<uint4*>(dst + dst0 + 2048 * i) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(dst + dst1 + 2048 * i) = make_uint4(h[4], h[5], h[6], h[7]);
+          *reinterpret_cast<uint4*>(dst + dst0 + 2048 * q) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst + dst1 + 2048 * q) = make_uint4(h[4], h[5], h[6], h[7]);
         }
-        fence_proxy_async_smem();
-        mbar_arrive(&sh.full[b]);
+        announce(&sh.vfull[i % RG::NV]);
+        if (more) end_k(i + 1, rows);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) cur[i] = nxt[i];
+        for (int q = 0; q < 8; ++q) cur[q] = nxt[q];
       }
+      cp_async_wait<0>();
     }
     if (lt == 0) sh.poison_n = min(masked_n, kPoison);
     mbar_arrive(&sh.loads_done);
@@ -501,33 +555,42 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     regs_down<kMmaRegs>();
     if (warp == 12) {
       constexpr uint32_t fmt = KVT == 0 ? 1u : 0u;  // bf16 or f16
-      const uint32_t id_s = umma_idesc(fmt, 128, 128);
-      const uint32_t id_o = id_s | (1u << 16);      // B is N-major
+      const uint32_t id_s = umma_idesc(fmt, 128, 128);  // (format 0 is e4m3 among 8-bit operands)
+      const uint32_t id_o = id_s | (1u << 16);          // B is N-major
       const uint64_t q0 = umma_sdesc_sw128(smem_addr(sQ));
-      const uint64_t k0 = umma_sdesc_sw128(smem_addr(sKV));
+      const uint64_t k0 = umma_sdesc_sw128(smem_addr(sK));
       // N-major: the second 64 dims one atom on, 8-key groups 1024 bytes apart
-      const uint64_t v0 = (k0 & ~(0x3FFFull << 16)) | (static_cast<uint64_t>(kAtom >> 4) << 16);
-      auto scores = [&](int x, int s) {
-        const uint64_t a = q0 + ((x * kTileBytes) >> 4), b = k0 + (((s % kBufs) * kTileBytes) >> 4);
+      const uint64_t v0 = (umma_sdesc_sw128(smem_addr(sV)) & ~(0x3FFFull << 16)) |
+                          (static_cast<uint64_t>(kAtom >> 4) << 16);
+      auto scores = [&](int x, int i) {
+        const uint64_t a = q0 + ((x * kTile) >> 4), b = k0 + (((i % RG::NK) * RG::kKey) >> 4);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
-          const int off = ((kk >> 2) * kAtom + (kk & 3) * 32) >> 4;
-          mma_ss(tmem + 128 * x, a + off, b + off, id_s, kk != 0 ? 1u : 0u);
+          const int off = (kk & 3) * 32, atom = (kk >> 2) * kAtom;
+          if constexpr (KVT == 0)
+            mma_ss(tmem + 128 * x, a + ((atom + off) >> 4), b + ((atom + off) >> 4), id_s, kk != 0 ? 1u : 0u);
+          else  // the hi terms, then the lo terms, over the same codes
+            mma_ss_e4m3(tmem + 128 * x, a + ((atom + off) >> 4), b + (off >> 4), id_s, kk != 0 ? 1u : 0u);
         }
       };
-      auto values = [&](int x, int s, bool first) {
-        const uint64_t b = v0 + (((s % kBufs) * kTileBytes) >> 4);
+      auto values = [&](int x, int i, bool first) {
+        const uint64_t b = v0 + (((i % RG::NV) * kTile) >> 4);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * kk, b + ((kk * 2048) >> 4), id_o,
-                      first && kk == 0 ? 0u : 1u);
+                 first && kk == 0 ? 0u : 1u);
       };
-      auto wait_full = [&](int s) {
-        const bool ok = all_ok(mbar_wait(&sh.full[s % kBufs], (s / kBufs) & 1, P.err));
+      auto wait_k = [&](int i) {
+        const bool ok = all_ok(mbar_wait(&sh.kfull[i % RG::NK], (i / RG::NK) & 1, P.err));
         tc_fence_after_sync();
         return ok;
       };
-      bool ok = wait_full(0);
+      auto wait_p = [&](int x, int i) {
+        const bool ok = all_ok(mbar_wait(&sh.p_ready[x], i & 1, P.err));
+        tc_fence_after_sync();
+        return ok;
+      };
+      bool ok = all_ok(mbar_wait(&sh.q_ready, 0, P.err)) && wait_k(0);
       if (ok) {
         scores(0, 0);
         mma_commit(&sh.s_full[0]);
@@ -535,41 +598,146 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           scores(1, 0);
           mma_commit(&sh.s_full[1]);
         }
-        mma_commit(&sh.empty[0]);
+        mma_commit(&sh.kempty[0]);
       }
-      for (int j = 0; j < nt && ok; ++j) {
-        const int sv = 2 * j + 1, sk = 2 * j + 2;
-        const bool more = j + 1 < nt;
-        ok = wait_full(sv) && all_ok(mbar_wait(&sh.p_ready[0], j & 1, P.err));
+      for (int i = 0; i < nt && ok; ++i) {
+        const bool more = i + 1 < nt;
+        ok = all_ok(mbar_wait(&sh.vfull[i % RG::NV], (i / RG::NV) & 1, P.err)) && wait_p(0, i);
         if (!ok) break;
-        tc_fence_after_sync();
-        values(0, sv, j == 0);
+        values(0, i, i == 0);
         if (more) {
-          ok = wait_full(sk);
+          ok = wait_k(i + 1);
           if (!ok) break;
-          scores(0, sk);
+          scores(0, i + 1);
           mma_commit(&sh.s_full[0]);
         }
         if (two) {
-          ok = all_ok(mbar_wait(&sh.p_ready[1], j & 1, P.err));
+          ok = wait_p(1, i);
           if (!ok) break;
-          tc_fence_after_sync();
-          values(1, sv, j == 0);
+          values(1, i, i == 0);
         }
-        mma_commit(&sh.empty[sv % kBufs]);
+        mma_commit(&sh.vempty[i % RG::NV]);
         if (more) {
           if (two) {
-            scores(1, sk);
+            scores(1, i + 1);
             mma_commit(&sh.s_full[1]);
           }
-          mma_commit(&sh.empty[sk % kBufs]);
+          mma_commit(&sh.kempty[(i + 1) % RG::NK]);
         }
       }
       mma_commit(&sh.o_full);
+    } else if (warp == 13) {
+      // ---------------------------------------------------------- loads by TMA
+      int page_n = nt > 1 ? fetch_page(j0 + 1) : -1;
+      uint32_t rows = to_row(j0, fetch_page(j0)), word = scale_word(rows);
+      // one tile of `bytes` bytes: boxes of P.box keys
+      auto tile = [&](uint64_t* full, uint8_t* dst, uint32_t r, int x, int atoms) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(full, atoms * kAtom);
+          mbar_arrive_n(full, 3);
+        }
+        __syncwarp();
+        for (int k = 0; k < 128; k += P.box) {
+          const int y = static_cast<int>(__shfl_sync(0xffffffffu, r, k >> 4));
+          tma_box(dst + k * 128, &tmap, x, y, full);
+          if (atoms == 2) tma_box(dst + kAtom + k * 128, &tmap, x + 64, y, full);
+        }
+      };
+      for (int i = 0; i < nt; ++i) {
+        const int j = j0 + i;
+        const uint32_t here = rows, word_here = word;
+        if (i + 1 < nt) {
+          rows = to_row(j + 1, page_n);
+          word = scale_word(rows);
+        }
+        page_n = i + 2 < nt ? fetch_page(j + 2) : -1;
+        const bool own = by_tma(j, here);
+        if (!all_ok(mbar_wait(&sh.kempty[i % RG::NK], ((i / RG::NK) & 1) ^ 1, P.err))) break;
+        if (own) {
+          publish(i, here, word_here);
+          tile(&sh.kfull[i % RG::NK], sK + (i % RG::NK) * RG::kKey, here, 0, KVT == 0 ? 2 : 1);
+        } else if (lane == 0) {
+          mbar_arrive(&sh.kgo[i % RG::NK]);
+        }
+        if constexpr (KVT == 0) {
+          if (!all_ok(mbar_wait(&sh.vempty[i % RG::NV], ((i / RG::NV) & 1) ^ 1, P.err))) break;
+          if (own)
+            tile(&sh.vfull[i % RG::NV], sV + (i % RG::NV) * kTile, here, 128, 2);
+          else if (lane == 0)
+            mbar_arrive(&sh.vgo[i % RG::NV]);
+        }
+      }
     }
   } else if (warp < 4 || two) {
     // ------------------------------------------------------------ softmax
     regs_up<kSoftmaxRegs>();
+    // ---- Q of the warp's own 32 M rows, a half-warp per row, eight in flight
+    {
+      const int r = (warp >> 2) * R + (tid & 127) / G;
+      sh.pos[tid] = (tid & 127) < R * G && r < nrows ? max(P.logical[row0 + r], -1) : INT_MIN;
+    }
+#pragma unroll 1
+    for (int b = 0; b < 32; b += 16) {
+      const int lane16 = lane & 15;
+      uint4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int m = 32 * warp + b + 2 * u + (lane >> 4), im = m & 127, r = (warp >> 2) * R + im / G;
+        v[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (im < R * G && r < nrows)
+          v[u] = *reinterpret_cast<const uint4*>(P.q + (static_cast<long long>(row0 + r) * P.hq + kvh * G + im % G) * 128 + 8 * lane16);
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int m = 32 * warp + b + 2 * u + (lane >> 4), im = m & 127;
+        uint8_t* tile = sQ + (warp >> 2) * kTile;
+        float qs = 0.08838834764831845f * kLog2e;
+        if constexpr (KVT == 0) {
+          *reinterpret_cast<uint4*>(tile + tile_byte(im, lane16)) = v[u];
+        } else {
+          const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+          float f[8], peak = 0.f;
+          bool odd = false;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            f[e] = e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
+            odd |= !(fabsf(f[e]) <= 3.39e38f);
+            peak = fmaxf(peak, fabsf(f[e]));
+          }
+#pragma unroll
+          for (int o = 8; o >= 1; o >>= 1) {
+            peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, o));
+            odd |= __shfl_xor_sync(0xffffffffu, static_cast<int>(odd), o) != 0;
+          }
+          const int e = peak > 0.f ? max(__float_as_int(peak) >> 23, 1) - 127 - 7 : 0;
+          const float f0 = exp2i(-(e / 2)), f1 = exp2i(-(e - e / 2));
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = odd ? 0.f : f[i] * f0 * f1;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t h0 = f32x2_to_e4m3x2(f[4 * i], f[4 * i + 1]), h1 = f32x2_to_e4m3x2(f[4 * i + 2], f[4 * i + 3]);
+            hi[i] = h0 | (h1 << 16);
+            uint32_t b0, b1;
+            e4m3x4_to_f16x2x2(hi[i], b0, b1);
+            const float2 y0 = __half22float2(*reinterpret_cast<const __half2*>(&b0));
+            const float2 y1 = __half22float2(*reinterpret_cast<const __half2*>(&b1));
+            lo[i] = static_cast<uint32_t>(f32x2_to_e4m3x2(f[4 * i] - y0.x, f[4 * i + 1] - y0.y)) |
+                    (static_cast<uint32_t>(f32x2_to_e4m3x2(f[4 * i + 2] - y1.x, f[4 * i + 3] - y1.y)) << 16);
+          }
+          qs = fmaxf(exp2i(e / 2) * (qs * (KVT == 1 ? P.k_scale : 1.0f)) * exp2i(e - e / 2), kLeast);
+          if (odd) qs = -1.0f;
+          // the hi terms' atom, then the lo terms'
+          uint8_t* dst = tile + im * 128 + (((lane16 >> 1) ^ (im & 7)) << 4) + (lane16 & 1) * 8;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(dst + kAtom) = make_uint2(lo[0], lo[1]);
+        }
+        if (lane16 == 0) sh.qs[m] = qs;
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.q_ready);
     const int x = warp >> 2, m = tid;  // M row m & 127 of tile x
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + 128 * x + lanes, to = tmem + 256 + 128 * x + lanes;
@@ -589,27 +757,33 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       if (!ok) break;
       tc_fence_after_sync();
       uint32_t r[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32_issue(ts + 32 * c, r[c]);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_wait_ld32(r[c]);
       const bool plain = kb + 127 <= hi_all && (kb >= lo_all || kb + 127 < P.sinks) && sh.check[slot] == 0;
-      if (!plain) {
-        const int hi = p - kb, lo = p - P.window + 1 - kb, sk = P.sinks - kb;
+      auto mask = [&]() {
+        const int hi = p - kb + 1, lo = p - P.window + 1 - kb, sk = P.sinks - kb;
+        const bool pages = sh.check[slot] != 0;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const uint32_t val = sh.valid[slot][c];
+          uint32_t vis = low_bits(hi - 32 * c) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c));
+          if (pages) vis &= sh.valid[slot][c];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int k = 32 * c + i;
-            const bool vis = k <= hi && (k >= lo || k < sk) && ((val >> i) & 1u);
-            if (!vis) r[c][i] = 0xFF800000u;
-          }
+          for (int i = 0; i < 32; ++i) r[c][i] = (vis & (1u << i)) != 0u ? r[c][i] : 0xFF800000u;
         }
-      }
-      float mx = -INFINITY;
+      };
+      auto load_s = [&]() {
 #pragma unroll
-      for (int b = 0; b < 8; ++b) {
+        for (int c = 0; c < 4; ++c) tmem_ld32_issue(ts + 32 * c, r[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_wait_ld32(r[c]);
+        if (!plain) mask();
+      };
+      uint32_t sc[8];  // (block scales)
+      if constexpr (KVT == 2) {
+        const uint4 a = *reinterpret_cast<const uint4*>(&sh.scale[slot][0]);
+        const uint4 b = *reinterpret_cast<const uint4*>(&sh.scale[slot][4]);
+        sc[0] = a.x; sc[1] = a.y; sc[2] = a.z; sc[3] = a.w;
+        sc[4] = b.x; sc[5] = b.y; sc[6] = b.z; sc[7] = b.w;
+      }
+      auto block_max_raw = [&](int b) {  // the largest of 16 scores
         const uint32_t* rr = &r[b >> 1][(b & 1) * 16];
         float bm = max3(__uint_as_float(rr[0]), __uint_as_float(rr[1]), __uint_as_float(rr[2]));
         float b2 = max3(__uint_as_float(rr[3]), __uint_as_float(rr[4]), __uint_as_float(rr[5]));
@@ -618,15 +792,19 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           bm = max3(bm, __uint_as_float(rr[i]), __uint_as_float(rr[i + 1]));
           b2 = max3(b2, __uint_as_float(rr[i + 2]), __uint_as_float(rr[i + 3]));
         }
-        bm = fmaxf(max3(bm, __uint_as_float(rr[14]), __uint_as_float(rr[15])), b2);
+        bm = max3(bm, __uint_as_float(rr[14]), __uint_as_float(rr[15]));
+        return fmaxf(bm, b2);
+      };
+      // its exponent (log2), without the reference
+      auto block_max = [&](int b) {
+        const float bm = block_max_raw(b);
         if constexpr (KVT == 2) {
-          const float4 sc = sh.scale[slot][b];
-          bm = fmaf(bm, fmaxf(qs * sc.x, kLeast), sc.y);
+          return fmaf(bm, fmaxf(qs * bf16_lo(sc[b]), kLeast), bf16_hi(sc[b]));
         }
-        mx = fmaxf(mx, bm);
-      }
-      if constexpr (KVT != 2) mx *= qs;
-      if (__any_sync(0xffffffffu, mx > ref + kUp)) {
+        return bm * qs;
+      };
+      // moves the reference to mx where that is larger, the sums with it
+      auto move_ref = [&](float mx) {
         const float mn = fmaxf(ref, mx);
         const float al = ex2_ftz(ref - (mn == -INFINITY ? 0.f : mn));
         l *= al;
@@ -642,42 +820,63 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           }
         }
         ref = mn;
+      };
+      load_s();
+      // The weights are taken against the reference as it stands, and their
+      // maximum beside them; only where a score passes the reference by kUp
+      // (or a row has none yet) is it moved and the tile done again.
+      bool moved = __any_sync(0xffffffffu, ref == -INFINITY);
+      float mx = -INFINITY;
+      if (moved) {
+#pragma unroll
+        for (int b = 0; b < 8; ++b) mx = fmaxf(mx, block_max(b));
+        move_ref(mx);
       }
-      const float neg = ref == -INFINITY ? 0.f : -ref;
-      unsigned long long sum2 = 0ull;  // (two sums, of even and odd keys)
-      float sum = 0.f;
+      uint32_t pk[2][32];
+      float sum;
+      while (true) {
+        const float neg = ref == -INFINITY ? 0.f : -ref;
+        unsigned long long sum2 = 0ull;  // (two sums, of even and odd keys)
+        sum = 0.f;
+        mx = -INFINITY;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 0; b < 8; ++b) {
           float c = qs, base = neg, inv_vs = 1.0f;
           if constexpr (KVT == 2) {
-            const float4 sc = sh.scale[slot][4 * h + b];
-            c = fmaxf(c * sc.x, kLeast);
-            base += sc.y;
-            inv_vs = sc.z;
+            c = fmaxf(c * bf16_lo(sc[b]), kLeast);
+            base += bf16_hi(sc[b]);
+            inv_vs = ex2_ftz(-bf16_hi(sc[b]));
+          }
+          {
+            const float bm = block_max_raw(b);
+            mx = fmaxf(mx, KVT == 2 ? fmaf(bm, c, base - neg) : bm * qs);
           }
           const unsigned long long c2 = f32x2_pack(c, c), base2 = f32x2_pack(base, base);
           unsigned long long bs2 = KVT == 2 ? 0ull : sum2;
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const uint32_t* rr = &r[2 * h + (b >> 1)][(b & 1) * 16 + i];
+            const uint32_t* rr = &r[b >> 1][(b & 1) * 16 + i];
             float p0, p1;
             f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(rr[0]), __uint_as_float(rr[1])), c2, base2), p0, p1);
             p0 = ex2_ftz(p0);
             p1 = ex2_ftz(p1);
             bs2 = f32x2_add(bs2, f32x2_pack(p0, p1));
-            pk[8 * b + (i >> 1)] = KVT == 0 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+            pk[b >> 2][8 * (b & 3) + (i >> 1)] = KVT == 0 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
           }
           if constexpr (KVT == 2)
             sum = fmaf(f32x2_hsum(bs2), inv_vs, sum);
           else
             sum2 = bs2;
         }
-        tmem_st32(ts + 32 * h, pk);
+        if constexpr (KVT != 2) sum = f32x2_hsum(sum2);
+        if (moved || !__any_sync(0xffffffffu, mx > ref + kUp)) break;
+        moved = true;
+        load_s();
+        move_ref(mx);
       }
-      l += KVT == 2 ? sum : f32x2_hsum(sum2);
+      l += sum;
+      tmem_st32(ts, pk[0]);
+      tmem_st32(ts + 32, pk[1]);
       tmem_wait_st();
       tc_fence_before_sync();
       mbar_arrive(&sh.p_ready[x]);
@@ -694,6 +893,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     for (int b = 0; b < sh.poison_n; ++b)
       poisoned |= (sh.poison[b][0] | sh.poison[b][1] | sh.poison[b][2] | sh.poison[b][3]) != 0u;
     const long long ph = static_cast<long long>(split) * P.rows * P.hq + head;
+    // the warp's 32 rows cross to whole-row stores through its own rows of
+    // the Q tile, which no MMA reads any more
+    uint8_t* tile = sQ + x * kTile;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       uint32_t o[32];
@@ -702,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       float f[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * inv;
-      if (!act) continue;
+      if (act)
       if (poisoned) {  // what the row sees of the remembered elements
 #pragma unroll 1
         for (int b = 0; b < sh.poison_n * 128; ++b) {
@@ -720,20 +922,44 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           }
         }
       }
+      if (P.splits > 1) {
+        if (!act) continue;
+        float4* po = reinterpret_cast<float4*>(P.part_o + ph * 128 + 32 * c);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float y[8] = {f[8 * q], f[8 * q + 1], f[8 * q + 2], f[8 * q + 3], f[8 * q + 4], f[8 * q + 5], f[8 * q + 6], f[8 * q + 7]};
-        const int d0 = 32 * c + 8 * q;
-        if (P.splits > 1) {
-          float4* po = reinterpret_cast<float4*>(P.part_o + ph * 128 + d0);
-          po[0] = make_float4(y[0], y[1], y[2], y[3]);
-          po[1] = make_float4(y[4], y[5], y[6], y[7]);
-        } else {
-          store_gated8(P, head * 128 + d0, y, load_gate(P, head * 128 + d0));
+        for (int q = 0; q < 8; ++q) po[q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(tile + tile_byte(im, 4 * c + q)) =
+              make_uint4(pack_bf16x2(f[8 * q], f[8 * q + 1]), pack_bf16x2(f[8 * q + 2], f[8 * q + 3]),
+                         pack_bf16x2(f[8 * q + 4], f[8 * q + 5]), pack_bf16x2(f[8 * q + 6], f[8 * q + 7]));
+      }
+    }
+    if (P.splits > 1) {
+      if (act) P.part_lse[ph] = l == 0.f ? -INFINITY : ref + log2f(l);
+    } else if (ok) {
+      __syncwarp();
+#pragma unroll 1
+      for (int b = 0; b < 32; b += 16) {
+        const int c16 = lane & 15;
+        uint4 gate[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int i2 = (32 * warp + b + 2 * u + (lane >> 4)) & 127, r2 = x * R + i2 / G;
+          const long long at = (static_cast<long long>(row0 + r2) * P.hq + kvh * G + i2 % G) * 128 + 8 * c16;
+          gate[u] = i2 < R * G && r2 < nrows ? load_gate(P, at) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int i2 = (32 * warp + b + 2 * u + (lane >> 4)) & 127, r2 = x * R + i2 / G;
+          if (i2 >= R * G || r2 >= nrows) continue;
+          const uint4 y = *reinterpret_cast<const uint4*>(tile + tile_byte(i2, c16));
+          const float f[8] = {bf16_lo(y.x), bf16_hi(y.x), bf16_lo(y.y), bf16_hi(y.y),
+                              bf16_lo(y.z), bf16_hi(y.z), bf16_lo(y.w), bf16_hi(y.w)};
+          store_gated8(P, (static_cast<long long>(row0 + r2) * P.hq + kvh * G + i2 % G) * 128 + 8 * c16, f, gate[u]);
         }
       }
     }
-    if (act && P.splits > 1) P.part_lse[ph] = l == 0.f ? -INFINITY : ref + log2f(l);
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -750,11 +976,11 @@ cudaError_t launch_kind(const RowGqaParams& p, const CUtensorMap& tmap, const di
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
     const cudaError_t e = cudaFuncSetAttribute(window_tile_kernel<KVT>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<KVT>);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  return launch_kernel(window_tile_kernel<KVT>, grid, dim3(kThreads), kSmem, stream, false, tmap, p);
+  return launch_kernel(window_tile_kernel<KVT>, grid, dim3(kThreads), kSmem<KVT>, stream, false, tmap, p);
 }
 
 }  // namespace
