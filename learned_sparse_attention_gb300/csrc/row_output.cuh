@@ -21,8 +21,12 @@ __device__ __forceinline__ bool row_live(const RowGqaParams& P, int row, int req
   return req >= 0 && req < P.reqs && row >= P.qsl[req] && row < P.qsl[req + 1];
 }
 
+// 1 / (1 + 2^(-x log2 e)) by the PTX approximate reciprocal (1 ulp): 0 for a
+// gate far below 0, where the exponential is an infinity.
 __device__ __forceinline__ float sigmoid_of(uint32_t bf16_bits) {
-  return 1.0f / (1.0f + __expf(-__uint_as_float(bf16_bits << 16)));
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + ex2_ftz(__uint_as_float(bf16_bits << 16) * -kLog2e)));
+  return y;
 }
 
 // The gate of 8 dims (bf16x8), or zeros when there is none.

@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   uint8_t* sK = sQ + 2 * kTile;
   uint8_t* sV = sK + RG::NK * RG::kKey;
   TileShared& sh = *reinterpret_cast<TileShared*>(sV + RG::NV * kTile);
-  constexpr int kSoftmaxRegs = KVT == 0 ? 192 : 184, kLoadRegs = KVT == 0 ? 80 : 96, kMmaRegs = 48;
+  constexpr int kSoftmaxRegs = 176, kLoadRegs = 96, kMmaRegs = 64;
   static_assert(2 * kSoftmaxRegs + kLoadRegs + kMmaRegs <= 4 * 128, "the launch's registers");
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be uniform)
@@ -756,26 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       ok = all_ok(mbar_wait(&sh.info[slot], (j / kSlots) & 1, P.err) && mbar_wait(&sh.s_full[x], j & 1, P.err));
       if (!ok) break;
       tc_fence_after_sync();
-      uint32_t r[4][32];
       const bool plain = kb + 127 <= hi_all && (kb >= lo_all || kb + 127 < P.sinks) && sh.check[slot] == 0;
-      auto mask = [&]() {
-        const int hi = p - kb + 1, lo = p - P.window + 1 - kb, sk = P.sinks - kb;
-        const bool pages = sh.check[slot] != 0;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t vis = low_bits(hi - 32 * c) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c));
-          if (pages) vis &= sh.valid[slot][c];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) r[c][i] = (vis & (1u << i)) != 0u ? r[c][i] : 0xFF800000u;
-        }
-      };
-      auto load_s = [&]() {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_issue(ts + 32 * c, r[c]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_wait_ld32(r[c]);
-        if (!plain) mask();
-      };
       uint32_t sc[8];  // (block scales)
       if constexpr (KVT == 2) {
         const uint4 a = *reinterpret_cast<const uint4*>(&sh.scale[slot][0]);
@@ -783,8 +764,28 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         sc[0] = a.x; sc[1] = a.y; sc[2] = a.z; sc[3] = a.w;
         sc[4] = b.x; sc[5] = b.y; sc[6] = b.z; sc[7] = b.w;
       }
-      auto block_max_raw = [&](int b) {  // the largest of 16 scores
-        const uint32_t* rr = &r[b >> 1][(b & 1) * 16];
+      // Calls f(c, scores of columns 32 c .. 32 c + 31) for the four chunks of
+      // the row, each loaded while the one before it is worked on.
+      auto each_chunk = [&](auto&& f) {
+        uint32_t ra[32], rb[32];
+        tmem_ld32_issue(ts, ra);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t(&r)[32] = c & 1 ? rb : ra;
+          tmem_wait_ld32(r);
+          if (c < 3) tmem_ld32_issue(ts + 32 * (c + 1), c & 1 ? ra : rb);
+          if (!plain) {
+            const int hi = p - kb + 1 - 32 * c, lo = p - P.window + 1 - kb - 32 * c, sk = P.sinks - kb - 32 * c;
+            uint32_t vis = low_bits(hi) & (~low_bits(lo) | low_bits(sk));
+            if (sh.check[slot] != 0) vis &= sh.valid[slot][c];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = (vis & (1u << i)) != 0u ? r[i] : 0xFF800000u;
+          }
+          f(c, r);
+        }
+      };
+      // the largest of 16 scores
+      auto max16 = [&](const uint32_t* rr) {
         float bm = max3(__uint_as_float(rr[0]), __uint_as_float(rr[1]), __uint_as_float(rr[2]));
         float b2 = max3(__uint_as_float(rr[3]), __uint_as_float(rr[4]), __uint_as_float(rr[5]));
 #pragma unroll
@@ -796,83 +797,77 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         return fmaxf(bm, b2);
       };
       // its exponent (log2), without the reference
-      auto block_max = [&](int b) {
-        const float bm = block_max_raw(b);
-        if constexpr (KVT == 2) {
-          return fmaf(bm, fmaxf(qs * bf16_lo(sc[b]), kLeast), bf16_hi(sc[b]));
-        }
+      auto exponent = [&](float bm, int b) {
+        if constexpr (KVT == 2) return fmaf(bm, fmaxf(qs * bf16_lo(sc[b]), kLeast), bf16_hi(sc[b]));
         return bm * qs;
       };
-      // moves the reference to mx where that is larger, the sums with it
-      auto move_ref = [&](float mx) {
-        const float mn = fmaxf(ref, mx);
-        const float al = ex2_ftz(ref - (mn == -INFINITY ? 0.f : mn));
-        l *= al;
-        if (j > 0) {  // (S of this tile is complete, so O of the last one is)
-          uint32_t o[32];
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld32_issue(to + 32 * c, o);
-            tmem_wait_ld32(o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-            tmem_st32(to + 32 * c, o);
-          }
-        }
-        ref = mn;
-      };
-      load_s();
       // The weights are taken against the reference as it stands, and their
       // maximum beside them; only where a score passes the reference by kUp
-      // (or a row has none yet) is it moved and the tile done again.
+      // (or a row has none yet) is it moved and the tile done again (S is in
+      // place until P is stored).
       bool moved = __any_sync(0xffffffffu, ref == -INFINITY);
-      float mx = -INFINITY;
-      if (moved) {
-#pragma unroll
-        for (int b = 0; b < 8; ++b) mx = fmaxf(mx, block_max(b));
-        move_ref(mx);
-      }
       uint32_t pk[2][32];
       float sum;
+#pragma unroll 1
       while (true) {
+        if (moved) {
+          float mx = -INFINITY;
+          each_chunk([&](int c, const uint32_t* r) {
+            mx = fmaxf(mx, fmaxf(exponent(max16(r), 2 * c), exponent(max16(r + 16), 2 * c + 1)));
+          });
+          // moves the reference to mx where that is larger, the sums with it
+          const float mn = fmaxf(ref, mx);
+          const float al = ex2_ftz(ref - (mn == -INFINITY ? 0.f : mn));
+          l *= al;
+          if (j > 0) {  // (S of this tile is complete, so O of the last one is)
+            uint32_t o[32];
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld32_issue(to + 32 * c, o);
+              tmem_wait_ld32(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+              tmem_st32(to + 32 * c, o);
+            }
+          }
+          ref = mn;
+        }
         const float neg = ref == -INFINITY ? 0.f : -ref;
         unsigned long long sum2 = 0ull;  // (two sums, of even and odd keys)
+        float mx = -INFINITY;
         sum = 0.f;
-        mx = -INFINITY;
+        each_chunk([&](int c, const uint32_t* r) {
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-          float c = qs, base = neg, inv_vs = 1.0f;
-          if constexpr (KVT == 2) {
-            c = fmaxf(c * bf16_lo(sc[b]), kLeast);
-            base += bf16_hi(sc[b]);
-            inv_vs = ex2_ftz(-bf16_hi(sc[b]));
-          }
-          {
-            const float bm = block_max_raw(b);
-            mx = fmaxf(mx, KVT == 2 ? fmaf(bm, c, base - neg) : bm * qs);
-          }
-          const unsigned long long c2 = f32x2_pack(c, c), base2 = f32x2_pack(base, base);
-          unsigned long long bs2 = KVT == 2 ? 0ull : sum2;
+          for (int h = 0; h < 2; ++h) {
+            const int b = 2 * c + h;
+            const uint32_t* rr = r + 16 * h;
+            float f = qs, base = neg, inv_vs = 1.0f;
+            if constexpr (KVT == 2) {
+              f = fmaxf(f * bf16_lo(sc[b]), kLeast);
+              base += bf16_hi(sc[b]);
+              inv_vs = ex2_ftz(-bf16_hi(sc[b]));
+            }
+            mx = fmaxf(mx, exponent(max16(rr), b));
+            const unsigned long long f2 = f32x2_pack(f, f), base2 = f32x2_pack(base, base);
+            unsigned long long bs2 = KVT == 2 ? 0ull : sum2;
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const uint32_t* rr = &r[b >> 1][(b & 1) * 16 + i];
-            float p0, p1;
-            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(rr[0]), __uint_as_float(rr[1])), c2, base2), p0, p1);
-            p0 = ex2_ftz(p0);
-            p1 = ex2_ftz(p1);
-            bs2 = f32x2_add(bs2, f32x2_pack(p0, p1));
-            pk[b >> 2][8 * (b & 3) + (i >> 1)] = KVT == 0 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+            for (int i = 0; i < 16; i += 2) {
+              float p0, p1;
+              f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(rr[i]), __uint_as_float(rr[i + 1])), f2, base2), p0, p1);
+              p0 = ex2_ftz(p0);
+              p1 = ex2_ftz(p1);
+              bs2 = f32x2_add(bs2, f32x2_pack(p0, p1));
+              pk[c >> 1][16 * (c & 1) + 8 * h + (i >> 1)] = KVT == 0 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+            }
+            if constexpr (KVT == 2)
+              sum = fmaf(f32x2_hsum(bs2), inv_vs, sum);
+            else
+              sum2 = bs2;
           }
-          if constexpr (KVT == 2)
-            sum = fmaf(f32x2_hsum(bs2), inv_vs, sum);
-          else
-            sum2 = bs2;
-        }
+        });
         if constexpr (KVT != 2) sum = f32x2_hsum(sum2);
         if (moved || !__any_sync(0xffffffffu, mx > ref + kUp)) break;
         moved = true;
-        load_s();
-        move_ref(mx);
       }
       l += sum;
       tmem_st32(ts, pk[0]);
