@@ -23,9 +23,9 @@ __device__ __forceinline__ bool row_live(const RowGqaParams& P, int row, int req
 
 // 1 / (1 + 2^(-x log2 e)) by the PTX approximate reciprocal (1 ulp): 0 for a
 // gate far below 0, where the exponential is an infinity.
-__device__ __forceinline__ float sigmoid_of(uint32_t bf16_bits) {
+__device__ __forceinline__ float sigmoid_of(float x) {
   float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + ex2_ftz(__uint_as_float(bf16_bits << 16) * -kLog2e)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + ex2_ftz(x * -kLog2e)));
   return y;
 }
 
@@ -34,21 +34,23 @@ __device__ __forceinline__ uint4 load_gate(const RowGqaParams& P, long long at) 
   return P.gate != nullptr ? *reinterpret_cast<const uint4*>(P.gate + at) : make_uint4(0u, 0u, 0u, 0u);
 }
 
-// out[8 dims] = bf16(bf16(x) * sigmoid(gate)), or bf16(x) without a gate (the
-// rounding before the gate is the sparse GQA stage's).
-__device__ __forceinline__ void store_gated8(const RowGqaParams& P, long long at, const float (&x)[8], uint4 g) {
-  const uint32_t gv[4] = {g.x, g.y, g.z, g.w};
-  uint32_t o[4];
+// out[8 dims] = bf16(x * sigmoid(gate)) of bf16 values x, or x without a gate.
+__device__ __forceinline__ void store_gated(const RowGqaParams& P, long long at, uint4 x, uint4 g) {
+  if (P.gate != nullptr) {
+    uint32_t xv[4] = {x.x, x.y, x.z, x.w};
+    const uint32_t gv[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    float a = bf16_round(x[2 * e]), b = bf16_round(x[2 * e + 1]);
-    if (P.gate != nullptr) {
-      a *= sigmoid_of(gv[e] & 0xFFFFu);
-      b *= sigmoid_of(gv[e] >> 16);
-    }
-    o[e] = pack_bf16x2(a, b);
+    for (int e = 0; e < 4; ++e)
+      xv[e] = pack_bf16x2(bf16_lo(xv[e]) * sigmoid_of(bf16_lo(gv[e])), bf16_hi(xv[e]) * sigmoid_of(bf16_hi(gv[e])));
+    x = make_uint4(xv[0], xv[1], xv[2], xv[3]);
   }
-  *reinterpret_cast<uint4*>(P.out + at) = make_uint4(o[0], o[1], o[2], o[3]);
+  *reinterpret_cast<uint4*>(P.out + at) = x;
+}
+// The same of fp32 values, rounded to bf16 first (the sparse GQA stage's
+// rounding before its gate).
+__device__ __forceinline__ void store_gated8(const RowGqaParams& P, long long at, const float (&x)[8], uint4 g) {
+  store_gated(P, at, make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                pack_bf16x2(x[6], x[7])), g);
 }
 
 }  // namespace qsa

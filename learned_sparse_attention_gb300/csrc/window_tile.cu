@@ -12,15 +12,15 @@
 // Roles, 16 warps:
 //   0-3, 4-7  softmax of tile A, B: S from TMEM, masks on the tiles that need
 //             them, P back over S's columns, at the end the gated output;
-//   8-11      load what needs a thread's hand: key tiles that some row does
-//             not see, or that lie on small pages (keys that no row of the
-//             CTA sees become zeros, whatever the cache holds there), and the
-//             V tiles of e4m3 caches, as f16 (exact);
+//   8-11      what needs a thread's hand: V of tiles that some row does not
+//             see (keys that no row of the CTA sees become zeros, whatever the
+//             cache holds there), V of e4m3 caches, as f16 (exact), and tiles
+//             on pages of less than a TMA box, by cp.async;
 //   12        issues the MMAs: S_A(j+1) right after O_A(j), so the softmax of
 //             one tile runs under the products of the other;
-//   13        loads the other tiles by TMA.  It alone waits for K's ring buffers
-//             (bf16: V's too) to be free, in order, and hands the buffer of a
-//             tile that is not its own to warps 8-11.
+//   13        loads by TMA.  It alone waits for K's ring buffers (bf16: V's
+//             too) to be free, in order, and hands those that are not its own
+//             to warps 8-11.
 // TMEM: S_A, S_B, O_A, O_B of 128 columns each.  P is the A operand from
 // TMEM; V is the N-major B operand of the ring tile as it is stored.
 // e4m3 caches: K's codes are multiplied as they are, by q split into two e4m3
@@ -84,31 +84,40 @@ constexpr int kSmem = 1024 + 2 * kTile + Rings<KVT>::NK * Rings<KVT>::kKey + Rin
 // by the lane that elect.sync names (always the same one): their operands
 // then stay in uniform registers, and an issue costs a few cycles instead of
 // the ~120 that a lone lane's took (measured: as long as the MMA itself).
+// Matrix descriptors by their low words (address, leading offset): the high
+// word (8-row groups 1024 bytes apart, 128-byte swizzle) is the same for all.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t leading) {
+  return ((saddr >> 4) & 0x3FFFu) | ((leading >> 4) << 16);
+}
 // D[tmem] (+)= A[smem] * B[smem]^T, 16-bit inputs, fp32 accumulate
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // Same for e4m3 x e4m3
-__device__ __forceinline__ void mma_ss_e4m3(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+__device__ __forceinline__ void mma_ss_e4m3(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
                                             uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc,
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
@@ -328,11 +337,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     const int blk = page_pow2 ? k0 >> page_shift : k0 / P.page;
     return (static_cast<uint32_t>(page) * P.hkv + kvh) * static_cast<uint32_t>(P.page) + (k0 - blk * P.page);
   };
-  // Tiles that every row sees and whose pages hold whole boxes come by TMA
-  // (both loaders find the same answer).
-  auto by_tma = [&](int j, uint32_t rows) {
-    return P.box != 0 && !tile_masked(j) && all_ok(rows < kNoPage);
-  };
+  // V of a tile that some row does not see, or that lies on a page that is
+  // none, has to be looked through (both loaders find the same answer)
+  auto by_hand = [&](int j, uint32_t rows) { return tile_masked(j) || !all_ok(rows != kNoPage); };
   auto scale_word = [&](uint32_t rows) -> uint32_t {
     if (KVT != 2 || rows >= kNoPage) return 0x7F7Fu;
     return *reinterpret_cast<const uint16_t*>(P.scales + 2ll * (rows / P.scale_block));
@@ -405,73 +412,87 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     uint32_t rows = to_row(j0, fetch_page(j0));
 
     if constexpr (KVT == 0) {
-      // zeroes odd V elements of masked tile j and remembers their keys
-      auto clean = [&](int j, uint8_t* tile) {
-        const int slot = open_poison(j);
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-          const int key = 8 * i + (lt >> 4);
-          uint4* p = reinterpret_cast<uint4*>(tile + tile_byte(key, lt & 15));
-          uint4 v = *p;
-          uint32_t w[4] = {v.x, v.y, v.z, v.w}, odd = 0u;
+      // V of tile j as it has landed: zeroes where no row sees the key or its
+      // page is none (rows: the tile's), and for elements that are not
+      // finite, whose keys are remembered
+      auto clean = [&](int j, uint32_t rows, uint8_t* tile) {
+        const int slot = open_poison(j), kb = T.first_key(j);
+        const unsigned there = __ballot_sync(0xffffffffu, rows < kNoPage);
+        uint8_t* d = tile + tile_byte(lt >> 4, lt & 15);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if ((w[e] & 0x7F80u) == 0x7F80u) {
-              w[e] &= 0xFFFF0000u;
-              odd = 1u;
+        for (int h = 0; h < 2; ++h) {
+          uint4 v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4*>(d + (8 * h + i) * 1024);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int key = 8 * (8 * h + i) + (lt >> 4);
+            uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, odd = 0u;
+            // an exponent of all ones carries into the sign's place
+#pragma unroll
+            for (int e = 0; e < 4; ++e) odd |= ((w[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+            const bool none = !((there >> (4 * h + (i >> 1))) & 1u) || !seen(kb + key);
+            if (odd == 0u && !none) continue;
+            if (none) {
+              w[0] = w[1] = w[2] = w[3] = 0u;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
+                if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
+              }
+              remember(slot, key);
             }
-            if ((w[e] & 0x7F800000u) == 0x7F800000u) {
-              w[e] &= 0xFFFFu;
-              odd = 1u;
-            }
-          }
-          if (odd) {
-            *p = make_uint4(w[0], w[1], w[2], w[3]);
-            remember(slot, key);
+            *reinterpret_cast<uint4*>(d + (8 * h + i) * 1024) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
       };
-      // a tile's K is announced once its V is on the way, its V once the next
-      // tile's K is (or when the next tile comes by TMA)
+      // Small pages: K and V by cp.async.  A tile's K is announced once its V
+      // is on the way, its V once the next tile's K is, or with its own data
+      // where there is nothing to start meanwhile or it is cleaned.
       int v_open = -1;  // tile number whose V is on the way
-      auto finish_v = [&]() {
-        const int i = v_open;
-        v_open = -1;
-        if (tile_masked(j0 + i)) clean(j0 + i, sV + (i % RG::NV) * kTile);
-        announce(&sh.vfull[i % RG::NV]);
-      };
       for (int i = 0; i < nt; ++i) {
         const int j = j0 + i, kb = T.first_key(j);
         const uint32_t here = rows;
         if (i + 1 < nt) rows = to_row(j + 1, page_n);
         page_n = i + 2 < nt ? fetch_page(j + 2) : -1;
-        if (by_tma(j, here)) {
-          if (v_open >= 0) {
-            cp_async_wait<0>();
-            finish_v();
-          }
+        const bool hand = by_hand(j, here);
+        const int kbuf = i % RG::NK, vbuf = i % RG::NV;
+        if (P.box != 0) {
+          if (!hand) continue;
+          if (!wait_turn(sh.vgo, v_turn, vbuf)) break;
+          clean(j, here, sV + vbuf * kTile);
+          announce(&sh.vfull[vbuf]);
           continue;
         }
-        const bool masked = tile_masked(j);
-        if (v_open >= 0 && !all_ok(mbar_done(&sh.kgo[i % RG::NK], (k_turn >> (i % RG::NK)) & 1u))) {
+        if (v_open >= 0 && !all_ok(mbar_done(&sh.kgo[kbuf], (k_turn >> kbuf) & 1u))) {
           cp_async_wait<0>();  // (nothing to start meanwhile)
-          finish_v();
+          announce(&sh.vfull[v_open]);
+          v_open = -1;
         }
-        if (!wait_turn(sh.kgo, k_turn, i % RG::NK)) break;
+        if (!wait_turn(sh.kgo, k_turn, kbuf)) break;
         if (warp == 8) publish(i, here, 0u);
-        copy(sK + (i % RG::NK) * kTile, kvb, here, kb, masked, Int<16>());
+        copy(sK + kbuf * kTile, kvb, here, kb, hand, Int<16>());
         if (v_open >= 0) {
           cp_async_wait<1>();
-          finish_v();
+          announce(&sh.vfull[v_open]);
+          v_open = -1;
         }
-        if (!wait_turn(sh.vgo, v_turn, i % RG::NV)) break;
-        copy(sV + (i % RG::NV) * kTile, kvb + 256, here, kb, masked, Int<16>());
-        v_open = i;
+        if (!wait_turn(sh.vgo, v_turn, vbuf)) break;
+        copy(sV + vbuf * kTile, kvb + 256, here, kb, hand, Int<16>());
         cp_async_wait<1>();
-        announce(&sh.kfull[i % RG::NK]);
+        announce(&sh.kfull[kbuf]);
+        if (hand) {
+          cp_async_wait<0>();
+          __syncwarp();
+          clean(j, here, sV + vbuf * kTile);
+          announce(&sh.vfull[vbuf]);
+        } else {
+          v_open = vbuf;
+        }
       }
       cp_async_wait<0>();
-      if (v_open >= 0) finish_v();
+      if (v_open >= 0) announce(&sh.vfull[v_open]);
     } else {
       // V: 16 codes a lane and load; the next tile's codes are in flight while
       // this one's are converted
@@ -490,21 +511,21 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         }
       };
       auto start_k = [&](int i, uint32_t r) {  // false: a wait gave up
-        if (by_tma(j0 + i, r)) return true;
+        if (P.box != 0) return true;
         if (!wait_turn(sh.kgo, k_turn, i % RG::NK)) return false;
         if (warp == 8) publish(i, r, scale_word(r));
         copy(sK + (i % RG::NK) * RG::kKey, kvb, r, T.first_key(j0 + i), tile_masked(j0 + i), Int<8>());
         return true;
       };
-      auto end_k = [&](int i, uint32_t r) {
-        if (by_tma(j0 + i, r)) return;
+      auto end_k = [&](int i) {
+        if (P.box != 0) return;
         cp_async_wait<0>();
         announce(&sh.kfull[i % RG::NK]);
       };
       uint4 cur[8], nxt[8];
       load(j0, rows, cur);
       bool ok = start_k(0, rows);
-      if (ok) end_k(0, rows);
+      if (ok) end_k(0);
       const int dst0 = tile_byte(lt >> 3, 2 * (lt & 7)), dst1 = tile_byte(lt >> 3, 2 * (lt & 7) + 1);
       for (int i = 0; i < nt && ok; ++i) {
         const int j = j0 + i;
@@ -542,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           *reinterpret_cast<uint4*>(dst + dst1 + 2048 * q) = make_uint4(h[4], h[5], h[6], h[7]);
         }
         announce(&sh.vfull[i % RG::NV]);
-        if (more) end_k(i + 1, rows);
+        if (more) end_k(i + 1);
 #pragma unroll
         for (int q = 0; q < 8; ++q) cur[q] = nxt[q];
       }
@@ -557,13 +578,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       constexpr uint32_t fmt = KVT == 0 ? 1u : 0u;  // bf16 or f16
       const uint32_t id_s = umma_idesc(fmt, 128, 128);  // (format 0 is e4m3 among 8-bit operands)
       const uint32_t id_o = id_s | (1u << 16);          // B is N-major
-      const uint64_t q0 = umma_sdesc_sw128(smem_addr(sQ));
-      const uint64_t k0 = umma_sdesc_sw128(smem_addr(sK));
-      // N-major: the second 64 dims one atom on, 8-key groups 1024 bytes apart
-      const uint64_t v0 = (umma_sdesc_sw128(smem_addr(sV)) & ~(0x3FFFull << 16)) |
-                          (static_cast<uint64_t>(kAtom >> 4) << 16);
+      const uint32_t q0 = desc_lo(smem_addr(sQ), 16), k0 = desc_lo(smem_addr(sK), 16);
+      // N-major: the second 64 dims one atom on
+      const uint32_t v0 = desc_lo(smem_addr(sV), kAtom);
       auto scores = [&](int x, int i) {
-        const uint64_t a = q0 + ((x * kTile) >> 4), b = k0 + (((i % RG::NK) * RG::kKey) >> 4);
+        const uint32_t a = q0 + ((x * kTile) >> 4), b = k0 + (((i % RG::NK) * RG::kKey) >> 4);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
           const int off = (kk & 3) * 32, atom = (kk >> 2) * kAtom;
@@ -574,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         }
       };
       auto values = [&](int x, int i, bool first) {
-        const uint64_t b = v0 + (((i % RG::NV) * kTile) >> 4);
+        const uint32_t b = v0 + (((i % RG::NV) * kTile) >> 4);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * kk, b + ((kk * 2048) >> 4), id_o,
@@ -630,41 +649,52 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       // ---------------------------------------------------------- loads by TMA
       int page_n = nt > 1 ? fetch_page(j0 + 1) : -1;
       uint32_t rows = to_row(j0, fetch_page(j0)), word = scale_word(rows);
-      // one tile of `bytes` bytes: boxes of P.box keys
-      auto tile = [&](uint64_t* full, uint8_t* dst, uint32_t r, int x, int atoms) {
+      // the boxes of one tile that hold keys of the cache, on `full` with
+      // `arrivals` arrivals
+      auto tile = [&](uint64_t* full, uint32_t arrivals, uint8_t* dst, uint32_t r, int x, int atoms) {
+        const unsigned there = __ballot_sync(0xffffffffu, r < kNoPage) & 0xFFu;  // of 16-key blocks
+        const unsigned blocks = (1u << (P.box >> 4)) - 1u;                       // of a box
+        int n = 0;
+        for (int k = 0; k < 128; k += P.box) n += ((there >> (k >> 4)) & blocks) != 0u;
         if (lane == 0) {
-          mbar_arrive_expect_tx(full, atoms * kAtom);
-          mbar_arrive_n(full, 3);
+          mbar_arrive_expect_tx(full, n * atoms * P.box * 128);
+          if (arrivals > 1) mbar_arrive_n(full, arrivals - 1);
         }
         __syncwarp();
         for (int k = 0; k < 128; k += P.box) {
-          const int y = static_cast<int>(__shfl_sync(0xffffffffu, r, k >> 4));
+          const unsigned in = (there >> (k >> 4)) & blocks;
+          if (in == 0u) continue;
+          // (the box's first block may be one that nothing sees: count back)
+          const int first = __ffs(in) - 1;
+          const int y = static_cast<int>(__shfl_sync(0xffffffffu, r, (k >> 4) + first)) - 16 * first;
           tma_box(dst + k * 128, &tmap, x, y, full);
           if (atoms == 2) tma_box(dst + kAtom + k * 128, &tmap, x + 64, y, full);
         }
       };
       for (int i = 0; i < nt; ++i) {
-        const int j = j0 + i;
+        const int j = j0 + i, kbuf = i % RG::NK, vbuf = i % RG::NV;
         const uint32_t here = rows, word_here = word;
         if (i + 1 < nt) {
           rows = to_row(j + 1, page_n);
           word = scale_word(rows);
         }
         page_n = i + 2 < nt ? fetch_page(j + 2) : -1;
-        const bool own = by_tma(j, here);
-        if (!all_ok(mbar_wait(&sh.kempty[i % RG::NK], ((i / RG::NK) & 1) ^ 1, P.err))) break;
-        if (own) {
+        if (!all_ok(mbar_wait(&sh.kempty[kbuf], ((i / RG::NK) & 1) ^ 1, P.err))) break;
+        if (P.box != 0) {
           publish(i, here, word_here);
-          tile(&sh.kfull[i % RG::NK], sK + (i % RG::NK) * RG::kKey, here, 0, KVT == 0 ? 2 : 1);
+          tile(&sh.kfull[kbuf], 4, sK + kbuf * RG::kKey, here, 0, KVT == 0 ? 2 : 1);
         } else if (lane == 0) {
-          mbar_arrive(&sh.kgo[i % RG::NK]);
+          mbar_arrive(&sh.kgo[kbuf]);
         }
         if constexpr (KVT == 0) {
-          if (!all_ok(mbar_wait(&sh.vempty[i % RG::NV], ((i / RG::NV) & 1) ^ 1, P.err))) break;
-          if (own)
-            tile(&sh.vfull[i % RG::NV], sV + (i % RG::NV) * kTile, here, 128, 2);
-          else if (lane == 0)
-            mbar_arrive(&sh.vgo[i % RG::NV]);
+          if (!all_ok(mbar_wait(&sh.vempty[vbuf], ((i / RG::NV) & 1) ^ 1, P.err))) break;
+          if (P.box == 0) {
+            if (lane == 0) mbar_arrive(&sh.vgo[vbuf]);
+          } else if (by_hand(j, here)) {
+            tile(&sh.vgo[vbuf], 1, sV + vbuf * kTile, here, 128, 2);
+          } else {
+            tile(&sh.vfull[vbuf], 4, sV + vbuf * kTile, here, 128, 2);
+          }
         }
       }
     }
@@ -764,24 +794,21 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         sc[0] = a.x; sc[1] = a.y; sc[2] = a.z; sc[3] = a.w;
         sc[4] = b.x; sc[5] = b.y; sc[6] = b.z; sc[7] = b.w;
       }
-      // Calls f(c, scores of columns 32 c .. 32 c + 31) for the four chunks of
-      // the row, each loaded while the one before it is worked on.
-      auto each_chunk = [&](auto&& f) {
-        uint32_t ra[32], rb[32];
-        tmem_ld32_issue(ts, ra);
+      uint32_t r[4][32];
+      auto load_s = [&]() {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t(&r)[32] = c & 1 ? rb : ra;
-          tmem_wait_ld32(r);
-          if (c < 3) tmem_ld32_issue(ts + 32 * (c + 1), c & 1 ? ra : rb);
-          if (!plain) {
+        for (int c = 0; c < 4; ++c) tmem_ld32_issue(ts + 32 * c, r[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_wait_ld32(r[c]);
+        if (!plain) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
             const int hi = p - kb + 1 - 32 * c, lo = p - P.window + 1 - kb - 32 * c, sk = P.sinks - kb - 32 * c;
             uint32_t vis = low_bits(hi) & (~low_bits(lo) | low_bits(sk));
             if (sh.check[slot] != 0) vis &= sh.valid[slot][c];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = (vis & (1u << i)) != 0u ? r[i] : 0xFF800000u;
+            for (int i = 0; i < 32; ++i) r[c][i] = (vis & (1u << i)) != 0u ? r[c][i] : 0xFF800000u;
           }
-          f(c, r);
         }
       };
       // the largest of 16 scores
@@ -808,13 +835,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       bool moved = __any_sync(0xffffffffu, ref == -INFINITY);
       uint32_t pk[2][32];
       float sum;
+      load_s();
 #pragma unroll 1
       while (true) {
         if (moved) {
           float mx = -INFINITY;
-          each_chunk([&](int c, const uint32_t* r) {
-            mx = fmaxf(mx, fmaxf(exponent(max16(r), 2 * c), exponent(max16(r + 16), 2 * c + 1)));
-          });
+#pragma unroll
+          for (int b = 0; b < 8; ++b) mx = fmaxf(mx, exponent(max16(&r[b >> 1][16 * (b & 1)]), b));
           // moves the reference to mx where that is larger, the sums with it
           const float mn = fmaxf(ref, mx);
           const float al = ex2_ftz(ref - (mn == -INFINITY ? 0.f : mn));
@@ -836,11 +863,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         unsigned long long sum2 = 0ull;  // (two sums, of even and odd keys)
         float mx = -INFINITY;
         sum = 0.f;
-        each_chunk([&](int c, const uint32_t* r) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int b = 2 * c + h;
-            const uint32_t* rr = r + 16 * h;
+        for (int b = 0; b < 8; ++b) {
+            const uint32_t* rr = &r[b >> 1][16 * (b & 1)];
             float f = qs, base = neg, inv_vs = 1.0f;
             if constexpr (KVT == 2) {
               f = fmaxf(f * bf16_lo(sc[b]), kLeast);
@@ -857,17 +882,17 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
               p0 = ex2_ftz(p0);
               p1 = ex2_ftz(p1);
               bs2 = f32x2_add(bs2, f32x2_pack(p0, p1));
-              pk[c >> 1][16 * (c & 1) + 8 * h + (i >> 1)] = KVT == 0 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+              pk[b >> 2][8 * (b & 3) + (i >> 1)] = KVT == 0 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
             }
             if constexpr (KVT == 2)
               sum = fmaf(f32x2_hsum(bs2), inv_vs, sum);
             else
               sum2 = bs2;
-          }
-        });
+        }
         if constexpr (KVT != 2) sum = f32x2_hsum(sum2);
         if (moved || !__any_sync(0xffffffffu, mx > ref + kUp)) break;
         moved = true;
+        load_s();
       }
       l += sum;
       tmem_st32(ts, pk[0]);
@@ -948,10 +973,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         for (int u = 0; u < 8; ++u) {
           const int i2 = (32 * warp + b + 2 * u + (lane >> 4)) & 127, r2 = x * R + i2 / G;
           if (i2 >= R * G || r2 >= nrows) continue;
-          const uint4 y = *reinterpret_cast<const uint4*>(tile + tile_byte(i2, c16));
-          const float f[8] = {bf16_lo(y.x), bf16_hi(y.x), bf16_lo(y.y), bf16_hi(y.y),
-                              bf16_lo(y.z), bf16_hi(y.z), bf16_lo(y.w), bf16_hi(y.w)};
-          store_gated8(P, (static_cast<long long>(row0 + r2) * P.hq + kvh * G + i2 % G) * 128 + 8 * c16, f, gate[u]);
+          store_gated(P, (static_cast<long long>(row0 + r2) * P.hq + kvh * G + i2 % G) * 128 + 8 * c16,
+                      *reinterpret_cast<const uint4*>(tile + tile_byte(i2, c16)), gate[u]);
         }
       }
     }
