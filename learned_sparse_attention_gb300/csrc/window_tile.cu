@@ -52,7 +52,14 @@ constexpr int kTile = 128 * 256;  // bytes of 128 rows of 128 16-bit values, two
 constexpr int kAtom = 128 * 128;
 constexpr int kSlots = 4;        // tiles whose scales and page masks are kept
 constexpr int kPoison = 32;      // masked tiles that can remember odd V elements
-constexpr float kUp = 8.0f;
+// A row's reference is set so that its largest weight is 2^-kRoom, and moved
+// when a weight reaches 2: rooms of 2^8 and (f16 weights, whose subnormals
+// begin at 2^-14) 2^5.  That a weight has reached 2 shows in the top bit of
+// its exponent, so a tile is checked by or-ing its packed weights: half the
+// instructions of a maximum.
+template <int KVT>
+constexpr float kRoom = KVT == 0 ? 7.0f : 4.0f;
+constexpr uint32_t kTwo = 0x40004000u;  // (bf16 and f16 alike)
 constexpr float kLeast = 1.2e-38f;  // a score's factor is never 0: masked scores are -inf
 
 // The rings.  K tiles of e4m3 caches stay codes: half the size.
@@ -64,7 +71,7 @@ struct Rings {
 };
 
 struct TileShared {
-  uint64_t kfull[3], kempty[3], kgo[3], vfull[3], vempty[3], vgo[3], info[kSlots], s_full[2], p_ready[2], q_ready, o_full, loads_done;
+  uint64_t kfull[3], kempty[3], kgo[3], vfull[3], vempty[3], vgo[3], info[kSlots], s_full[2], p_ready[2][2], half_done[2], q_ready, o_full, loads_done;
   uint32_t tmem;
   int poison_n;
   int poison_tile[kPoison];        // first key
@@ -220,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   uint8_t* sK = sQ + 2 * kTile;
   uint8_t* sV = sK + RG::NK * RG::kKey;
   TileShared& sh = *reinterpret_cast<TileShared*>(sV + RG::NV * kTile);
-  constexpr int kSoftmaxRegs = 176, kLoadRegs = 96, kMmaRegs = 64;
+  constexpr int kSoftmaxRegs = KVT == 2 ? 184 : 176, kLoadRegs = KVT == 2 ? 88 : 96, kMmaRegs = KVT == 2 ? 56 : 64;
   static_assert(2 * kSoftmaxRegs + kLoadRegs + kMmaRegs <= 4 * 128, "the launch's registers");
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be uniform)
@@ -291,7 +298,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_ready[i], 128);
+      mbar_init(&sh.p_ready[i][0], 128);
+      mbar_init(&sh.p_ready[i][1], 128);
+      mbar_init(&sh.half_done[i], 1);
     }
     for (int i = 0; i < kSlots; ++i) mbar_init(&sh.info[i], 1);
     mbar_init(&sh.q_ready, two ? 8 : 4);
@@ -592,20 +601,23 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
             mma_ss_e4m3(tmem + 128 * x, a + ((atom + off) >> 4), b + (off >> 4), id_s, kk != 0 ? 1u : 0u);
         }
       };
-      auto values = [&](int x, int i, bool first) {
+      // O += P V of tile number i, a half of its keys at a time
+      auto values = [&](int x, int i) {
         const uint32_t b = v0 + (((i % RG::NV) * kTile) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * kk, b + ((kk * 2048) >> 4), id_o,
-                 first && kk == 0 ? 0u : 1u);
+        for (int h = 0; h < 2; ++h) {
+          if (!all_ok(mbar_wait(&sh.p_ready[x][h], i & 1, P.err))) return false;
+          tc_fence_after_sync();
+#pragma unroll
+          for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+            mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * kk, b + ((kk * 2048) >> 4), id_o,
+                   i == 0 && kk == 0 ? 0u : 1u);
+          if (h == 0) mma_commit(&sh.half_done[x]);
+        }
+        return true;
       };
       auto wait_k = [&](int i) {
         const bool ok = all_ok(mbar_wait(&sh.kfull[i % RG::NK], (i / RG::NK) & 1, P.err));
-        tc_fence_after_sync();
-        return ok;
-      };
-      auto wait_p = [&](int x, int i) {
-        const bool ok = all_ok(mbar_wait(&sh.p_ready[x], i & 1, P.err));
         tc_fence_after_sync();
         return ok;
       };
@@ -621,9 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       }
       for (int i = 0; i < nt && ok; ++i) {
         const bool more = i + 1 < nt;
-        ok = all_ok(mbar_wait(&sh.vfull[i % RG::NV], (i / RG::NV) & 1, P.err)) && wait_p(0, i);
+        ok = all_ok(mbar_wait(&sh.vfull[i % RG::NV], (i / RG::NV) & 1, P.err)) && values(0, i);
         if (!ok) break;
-        values(0, i, i == 0);
         if (more) {
           ok = wait_k(i + 1);
           if (!ok) break;
@@ -631,9 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           mma_commit(&sh.s_full[0]);
         }
         if (two) {
-          ok = wait_p(1, i);
+          ok = values(1, i);
           if (!ok) break;
-          values(1, i, i == 0);
         }
         mma_commit(&sh.vempty[i % RG::NV]);
         if (more) {
@@ -794,21 +804,21 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         sc[0] = a.x; sc[1] = a.y; sc[2] = a.z; sc[3] = a.w;
         sc[4] = b.x; sc[5] = b.y; sc[6] = b.z; sc[7] = b.w;
       }
-      uint32_t r[4][32];
-      auto load_s = [&]() {
+      // S of columns 64 h .. 64 h + 63: asked for, and there with its masks
+      auto ask_s = [&](int h, uint32_t (&r)[2][32]) {
+        tmem_ld32_issue(ts + 64 * h, r[0]);
+        tmem_ld32_issue(ts + 64 * h + 32, r[1]);
+      };
+      auto mask_s = [&](int h, uint32_t (&r)[2][32]) {
+        if (plain) return;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_issue(ts + 32 * c, r[c]);
+        for (int c = 0; c < 2; ++c) {
+          const int k0 = 64 * h + 32 * c;
+          const int hi = p - kb + 1 - k0, lo = p - P.window + 1 - kb - k0, sk = P.sinks - kb - k0;
+          uint32_t vis = low_bits(hi) & (~low_bits(lo) | low_bits(sk));
+          if (sh.check[slot] != 0) vis &= sh.valid[slot][2 * h + c];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_wait_ld32(r[c]);
-        if (!plain) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int hi = p - kb + 1 - 32 * c, lo = p - P.window + 1 - kb - 32 * c, sk = P.sinks - kb - 32 * c;
-            uint32_t vis = low_bits(hi) & (~low_bits(lo) | low_bits(sk));
-            if (sh.check[slot] != 0) vis &= sh.valid[slot][c];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) r[c][i] = (vis & (1u << i)) != 0u ? r[c][i] : 0xFF800000u;
-          }
+          for (int i = 0; i < 32; ++i) r[c][i] = (vis & (1u << i)) != 0u ? r[c][i] : 0xFF800000u;
         }
       };
       // the largest of 16 scores
@@ -828,51 +838,55 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         if constexpr (KVT == 2) return fmaf(bm, fmaxf(qs * bf16_lo(sc[b]), kLeast), bf16_hi(sc[b]));
         return bm * qs;
       };
-      // The weights are taken against the reference as it stands, and their
-      // maximum beside them; only where a score passes the reference by kUp
-      // (or a row has none yet) is it moved and the tile done again (S is in
-      // place until P is stored).
-      bool moved = __any_sync(0xffffffffu, ref == -INFINITY);
-      uint32_t pk[2][32];
-      float sum;
-      load_s();
+      // The weights of 64 keys are taken against the reference as it stands;
+      // only where one of them has grown too large (or a row has no reference
+      // yet) is it moved and the 64 done again.  (S is in place until P is
+      // stored.)  The first half's P is handed over while the second's is
+      // taken: its product runs meanwhile.
+      auto half = [&](int h, uint32_t (&r)[2][32]) {
+        bool moved = __any_sync(0xffffffffu, ref == -INFINITY);
+        uint32_t pk[32];
+        float sum;
 #pragma unroll 1
-      while (true) {
-        if (moved) {
-          float mx = -INFINITY;
+        while (true) {
+          if (moved) {
+            float mx = -INFINITY;
 #pragma unroll
-          for (int b = 0; b < 8; ++b) mx = fmaxf(mx, exponent(max16(&r[b >> 1][16 * (b & 1)]), b));
-          // moves the reference to mx where that is larger, the sums with it
-          const float mn = fmaxf(ref, mx);
-          const float al = ex2_ftz(ref - (mn == -INFINITY ? 0.f : mn));
-          l *= al;
-          if (j > 0) {  // (S of this tile is complete, so O of the last one is)
-            uint32_t o[32];
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              tmem_ld32_issue(to + 32 * c, o);
-              tmem_wait_ld32(o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-              tmem_st32(to + 32 * c, o);
+            for (int b = 0; b < 4; ++b) mx = fmaxf(mx, exponent(max16(&r[b >> 1][16 * (b & 1)]), 4 * h + b));
+            // moves the reference up, the sums with it
+            const float mn = fmaxf(ref, mx + kRoom<KVT>);
+            const float al = ex2_ftz(ref - (mn == -INFINITY ? 0.f : mn));
+            l *= al;
+            if (h == 1) {  // (the first half's product is in O, or on its way)
+              ok = all_ok(mbar_wait(&sh.half_done[x], j & 1, P.err)) && ok;
+              tc_fence_after_sync();
             }
-          }
-          ref = mn;
-        }
-        const float neg = ref == -INFINITY ? 0.f : -ref;
-        unsigned long long sum2 = 0ull;  // (two sums, of even and odd keys)
-        float mx = -INFINITY;
-        sum = 0.f;
+            if (j > 0 || h == 1) {  // (S of this tile is complete, so O of the last one is)
+              uint32_t o[32];
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                tmem_ld32_issue(to + 32 * c, o);
+                tmem_wait_ld32(o);
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                tmem_st32(to + 32 * c, o);
+              }
+            }
+            ref = mn;
+          }
+          const float neg = ref == -INFINITY ? 0.f : -ref;
+          unsigned long long sum2 = 0ull;  // (two sums, of even and odd keys)
+          uint32_t any_bits = 0u;
+          sum = 0.f;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
             const uint32_t* rr = &r[b >> 1][16 * (b & 1)];
             float f = qs, base = neg, inv_vs = 1.0f;
             if constexpr (KVT == 2) {
-              f = fmaxf(f * bf16_lo(sc[b]), kLeast);
-              base += bf16_hi(sc[b]);
-              inv_vs = ex2_ftz(-bf16_hi(sc[b]));
+              f = fmaxf(f * bf16_lo(sc[4 * h + b]), kLeast);
+              base += bf16_hi(sc[4 * h + b]);
+              inv_vs = ex2_ftz(-bf16_hi(sc[4 * h + b]));
             }
-            mx = fmaxf(mx, exponent(max16(rr), b));
             const unsigned long long f2 = f32x2_pack(f, f), base2 = f32x2_pack(base, base);
             unsigned long long bs2 = KVT == 2 ? 0ull : sum2;
 #pragma unroll
@@ -882,24 +896,36 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
               p0 = ex2_ftz(p0);
               p1 = ex2_ftz(p1);
               bs2 = f32x2_add(bs2, f32x2_pack(p0, p1));
-              pk[b >> 2][8 * (b & 3) + (i >> 1)] = KVT == 0 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+              pk[8 * b + (i >> 1)] = KVT == 0 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
             }
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) any_bits |= pk[8 * b + i] | pk[8 * b + i + 1];
             if constexpr (KVT == 2)
               sum = fmaf(f32x2_hsum(bs2), inv_vs, sum);
             else
               sum2 = bs2;
+          }
+          if constexpr (KVT != 2) sum = f32x2_hsum(sum2);
+          if (moved || !__any_sync(0xffffffffu, (any_bits & kTwo) != 0u)) break;
+          moved = true;
         }
-        if constexpr (KVT != 2) sum = f32x2_hsum(sum2);
-        if (moved || !__any_sync(0xffffffffu, mx > ref + kUp)) break;
-        moved = true;
-        load_s();
-      }
-      l += sum;
-      tmem_st32(ts, pk[0]);
-      tmem_st32(ts + 32, pk[1]);
-      tmem_wait_st();
-      tc_fence_before_sync();
-      mbar_arrive(&sh.p_ready[x]);
+        l += sum;
+        tmem_st32(ts + 32 * h, pk);
+        tmem_wait_st();
+        tc_fence_before_sync();
+        mbar_arrive(&sh.p_ready[x][h]);
+      };
+      uint32_t r0[2][32], r1[2][32];
+      ask_s(0, r0);
+      tmem_wait_ld32(r0[0]);
+      tmem_wait_ld32(r0[1]);
+      ask_s(1, r1);
+      mask_s(0, r0);
+      half(0, r0);
+      tmem_wait_ld32(r1[0]);
+      tmem_wait_ld32(r1[1]);
+      mask_s(1, r1);
+      half(1, r1);
     }
     // ---- output
     ok = all_ok(ok && mbar_wait(&sh.o_full, 0, P.err) && mbar_wait(&sh.loads_done, 0, P.err));
