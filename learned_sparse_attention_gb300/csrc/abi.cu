@@ -687,8 +687,9 @@ qsa_status do_window(const qsa_gqa_cfg* g, const qsa_window_args* a, void* ws, s
   if (st != QSA_OK) return st;
   p.qsl = a->query_start_loc;
   p.logical = a->logical_positions;
-  p.window = a->window;
-  p.sinks = a->sinks;
+  // (a cache holds fewer tokens than 2^30; sums of positions stay in int32)
+  p.window = a->window < (1 << 30) ? a->window : 1 << 30;
+  p.sinks = a->sinks < (1 << 30) ? a->sinks : 1 << 30;
   const WindowPlan plan = window_plan(g, a);
   st = place_splits(&p, g, plan.splits, ws, ws_bytes);
   if (st != QSA_OK) return st;

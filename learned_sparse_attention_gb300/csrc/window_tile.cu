@@ -4,23 +4,26 @@
 // Mathematics.  As in row_gqa.cu; here 128 (row, head) pairs of one request
 // and KV head are the M rows of S = Q K^T and O += P V, R = 128 / G rows with
 // their G heads, and a CTA runs two such tiles, A and B (rows r0 .. r0 + R - 1
-// and the R after them), over one stream of 128-key tiles.  A thread owns one
-// M row of S, so the softmax needs no exchange: it keeps the row's reference
-// (moved only when a score passes it by 2^8) and sum in registers, and
-// rescales the accumulator itself when the reference moves.
+// and the R after them), over one stream of 128-key tiles.  Two threads share
+// an M row, 64 keys each; both keep the row's reference and a sum of their
+// own weights in registers.
 //
-// Roles, 16 warps:
-//   0-3, 4-7  softmax of tile A, B: S from TMEM, masks on the tiles that need
+// Roles, 20 warps:
+//   0-7, 8-15 softmax of tile A, B: S from TMEM, masks on the tiles that need
 //             them, P back over S's columns, at the end the gated output;
-//   8-11      what needs a thread's hand: V of tiles that some row does not
-//             see (keys that no row of the CTA sees become zeros, whatever the
-//             cache holds there), V of e4m3 caches, as f16 (exact), and tiles
-//             on pages of less than a TMA box, by cp.async;
-//   12        issues the MMAs: S_A(j+1) right after O_A(j), so the softmax of
+//   16        issues the MMAs: S_A(j+1) right after O_A(j), so the softmax of
 //             one tile runs under the products of the other;
-//   13        loads by TMA.  It alone waits for K's ring buffers (bf16: V's
-//             too) to be free, in order, and hands those that are not its own
-//             to warps 8-11.
+//   17        loads by TMA.  It alone waits for the ring buffers that it or
+//             warps 18-19 fill with K (and V of bf16 caches) to be free, in
+//             order, and hands those that are not its own to them;
+//   18, 19    what needs a thread's hand: V of tiles that some row does not
+//             see (keys that no row of the CTA sees become zeros, whatever the
+//             cache holds there), V of e4m3 caches from codes to f16 (exact),
+//             and tiles on pages of less than a TMA box, by cp.async.
+// Two warps to a row and tile because a warp alone on its scheduler issues an
+// instruction every other cycle at best: with one, the ~550 instructions of a
+// row's softmax took 1450 cycles, the two products 1060 a tile, and neither
+// could hide the other.
 // TMEM: S_A, S_B, O_A, O_B of 128 columns each.  P is the A operand from
 // TMEM; V is the N-major B operand of the ring tile as it is stored.
 // e4m3 caches: K's codes are multiplied as they are, by q split into two e4m3
@@ -47,7 +50,8 @@
 namespace qsa {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kSoftWarps = 16;
+constexpr int kThreads = (kSoftWarps + 4) * 32;
 constexpr int kTile = 128 * 256;  // bytes of 128 rows of 128 16-bit values, two 64-dim atoms
 constexpr int kAtom = 128 * 128;
 constexpr int kSlots = 4;        // tiles whose scales and page masks are kept
@@ -62,16 +66,19 @@ constexpr float kRoom = KVT == 0 ? 7.0f : 4.0f;
 constexpr uint32_t kTwo = 0x40004000u;  // (bf16 and f16 alike)
 constexpr float kLeast = 1.2e-38f;  // a score's factor is never 0: masked scores are -inf
 
-// The rings.  K tiles of e4m3 caches stay codes: half the size.
+// The rings.  e4m3 caches: K tiles stay codes, half the size, and V's codes
+// have a ring of their own before they become f16.
 template <int KVT>
 struct Rings {
-  static constexpr int NK = KVT == 0 ? 2 : 3, NV = KVT == 0 ? 2 : 3;
+  static constexpr int NK = KVT == 0 ? 2 : 3, NV = 2, NR = KVT == 0 ? 0 : 2;
   static constexpr int kKey = KVT == 0 ? kTile : kAtom;
+  static constexpr int kBytes = NK * kKey + NV * kTile + NR * kAtom;
   static_assert(kSlots > NK, "a slot is rewritten only after its tile's softmax");
 };
 
 struct TileShared {
-  uint64_t kfull[3], kempty[3], kgo[3], vfull[3], vempty[3], vgo[3], info[kSlots], s_full[2], p_ready[2][2], half_done[2], q_ready, o_full, loads_done;
+  uint64_t kfull[3], kempty[3], kgo[3], vfull[2], vempty[2], vgo[2], rfull[2], rempty[2];
+  uint64_t info[kSlots], s_full[2], p_ready[2], q_ready, o_full, loads_done;
   uint32_t tmem;
   int poison_n;
   int poison_tile[kPoison];        // first key
@@ -80,11 +87,10 @@ struct TileShared {
   int check[kSlots];               // some key is not
   alignas(16) uint32_t scale[kSlots][8];  // of each 16 keys, two bf16: ks, and log2 vs above it
   float qs[256];                   // per M row: what its scores are multiplied by (< 0: the row is a NaN)
-  int pos[256];                    // its position (-1: before the start; INT_MIN: no row)
+  float pair[2][2][256];           // what a row's two threads tell each other
 };
 template <int KVT>
-constexpr int kSmem = 1024 + 2 * kTile + Rings<KVT>::NK * Rings<KVT>::kKey + Rings<KVT>::NV * kTile +
-                      static_cast<int>(sizeof(TileShared));
+constexpr int kSmem = 1024 + 2 * kTile + Rings<KVT>::kBytes + static_cast<int>(sizeof(TileShared));
 
 // ---------------------------------------------------------------- tcgen05
 // The MMAs and commits below are executed by a whole converged warp and issued
@@ -155,11 +161,6 @@ __device__ __forceinline__ bool mbar_done(uint64_t* bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
-// n arrivals at once
-__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(n)
-               : "memory");
-}
 // The largest of three.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -182,10 +183,26 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
           "r"(taddr)
       : "memory");
 }
+// 16 columns, waited for
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::
+          "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+          "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// Registers of a warpgroup's threads, which together keep to the launch's 128
+// Registers of a warpgroup's threads, which together keep to the launch's 96
 // a thread: all four warps of the group execute it.
 template <int N>
 __device__ __forceinline__ void regs_up() {
@@ -198,6 +215,21 @@ __device__ __forceinline__ void regs_down() {
 // Byte of 16-byte chunk c (8 dims) of row r in a swizzled two-atom tile.
 __device__ __forceinline__ constexpr int tile_byte(int r, int c) {
   return (c >> 3) * kAtom + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// The two warps of a row meet (64 threads); with a vote, any's answer.
+__device__ __forceinline__ void pair_sync(int id) {
+  asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ bool pair_any(int id, bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+      "bar.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(static_cast<uint32_t>(mine))
+      : "memory");
+  return any != 0u;
 }
 
 // The n lowest bits (none for n <= 0, all from 32 on).
@@ -226,9 +258,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   using RG = Rings<KVT>;
   uint8_t* sK = sQ + 2 * kTile;
   uint8_t* sV = sK + RG::NK * RG::kKey;
-  TileShared& sh = *reinterpret_cast<TileShared*>(sV + RG::NV * kTile);
-  constexpr int kSoftmaxRegs = KVT == 2 ? 184 : 176, kLoadRegs = KVT == 2 ? 88 : 96, kMmaRegs = KVT == 2 ? 56 : 64;
-  static_assert(2 * kSoftmaxRegs + kLoadRegs + kMmaRegs <= 4 * 128, "the launch's registers");
+  uint8_t* sR = sV + RG::NV * kTile;
+  TileShared& sh = *reinterpret_cast<TileShared*>(sK + RG::kBytes);
+  constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
+  static_assert(4 * kSoftmaxRegs + kOtherRegs <= 5 * 96, "the launch's registers");
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be uniform)
   const int kvh = blockIdx.y, split = blockIdx.z;
@@ -288,27 +321,28 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   }
 
   if (tid == 0) {
+    // (full: a lane of each of warps 18 and 19, or the TMA warp's for both)
     for (int i = 0; i < 3; ++i) {
-      mbar_init(&sh.kfull[i], 4);  // a lane of each loading warp, or the TMA warp's for all
-      mbar_init(&sh.vfull[i], 4);
+      mbar_init(&sh.kfull[i], 2);
       mbar_init(&sh.kempty[i], 1);
-      mbar_init(&sh.vempty[i], 1);
       mbar_init(&sh.kgo[i], 1);
-      mbar_init(&sh.vgo[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.vfull[i], 2);
+      mbar_init(&sh.vempty[i], 1);
+      mbar_init(&sh.vgo[i], 1);
+      mbar_init(&sh.rfull[i], 1);
+      mbar_init(&sh.rempty[i], 2);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_ready[i][0], 128);
-      mbar_init(&sh.p_ready[i][1], 128);
-      mbar_init(&sh.half_done[i], 1);
+      mbar_init(&sh.p_ready[i], 256);
     }
     for (int i = 0; i < kSlots; ++i) mbar_init(&sh.info[i], 1);
-    mbar_init(&sh.q_ready, two ? 8 : 4);
+    mbar_init(&sh.q_ready, two ? 16 : 8);
     mbar_init(&sh.o_full, 1);
-    mbar_init(&sh.loads_done, 128);
+    mbar_init(&sh.loads_done, 64);
     fence_barrier_init();
   }
-  if (warp == 12) {
+  if (warp == kSoftWarps) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
@@ -323,6 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   const bool page_pow2 = (P.page & (P.page - 1)) == 0;
   const int page_shift = __ffs(P.page) - 1;
   auto seen = [&](int key) { return key <= pmax && (key >= wlo || key < P.sinks); };
+  // every row of the CTA sees it
+  auto seen_by_all = [&](int key) { return !neg && key <= pmin && (key >= wlo_all || key < P.sinks); };
   // some row of the CTA does not see all of tile j
   auto tile_masked = [&](int j) {
     const int kb = T.first_key(j);
@@ -373,217 +409,206 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     if (lane == 0) mbar_arrive(&sh.info[slot]);
   };
 
-  if (warp >= 8 && warp < 12) {
-    // ------------------------------------------------------------ loads by hand
-    regs_down<kLoadRegs>();
-    const int lt = tid - 256;  // 0 .. 127
-    int masked_n = 0;
-    auto remember = [&](int slot, int key) {
-      if (slot < kPoison) atomicOr(&sh.poison[slot][key >> 5], 1u << (key & 31));
-      else flag_error(P.err);
-    };
-    auto open_poison = [&](int j) {  // (the same in every thread)
-      if (lt == 0 && masked_n < kPoison) sh.poison_tile[masked_n] = T.first_key(j);
-      return masked_n++;
-    };
-    auto announce = [&](uint64_t* bar) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar);
-    };
-    // the buffer of tile number i, from warp 13 (a buffer is handed over again
-    // only once its tile has been loaded and read)
-    uint32_t k_turn = 0u, v_turn = 0u;
-    auto wait_turn = [&](uint64_t* bars, uint32_t& turns, int b) {
-      const bool ok = all_ok(mbar_wait(&bars[b], (turns >> b) & 1u, P.err));
-      turns ^= 1u << b;
-      return ok;
-    };
-    // 128 keys' K or V by cp.async: CH 16-byte chunks a key
-    auto copy = [&](uint8_t* dst, const uint8_t* src, uint32_t rows, int kb, bool masked, auto chunks) {
-      constexpr int CH = decltype(chunks)::value, PER = 128 / CH;  // keys a pass
-      const int c = lt % CH, k0 = lt / CH;
-      uint32_t base[8];
+  if (warp >= kSoftWarps) {
+    regs_down<kOtherRegs>();
+    if (warp >= kSoftWarps + 2) {
+      // ---------------------------------------------------------- by hand
+      const int lt = tid - (kSoftWarps + 2) * 32;  // 0 .. 63
+      int masked_n = 0;
+      auto remember = [&](int slot, int key) {
+        if (slot < kPoison) atomicOr(&sh.poison[slot][key >> 5], 1u << (key & 31));
+        else flag_error(P.err);
+      };
+      auto open_poison = [&](int j) {  // (the same in every thread)
+        if (lt == 0 && masked_n < kPoison) sh.poison_tile[masked_n] = T.first_key(j);
+        return masked_n++;
+      };
+      auto announce = [&](uint64_t* bar) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+      };
+      // buffer b, from warp 17 (it is handed over again only once its tile
+      // has been loaded and read)
+      uint32_t k_turn = 0u, v_turn = 0u;
+      auto wait_turn = [&](uint64_t* bars, uint32_t& turns, int b) {
+        const bool ok = all_ok(mbar_wait(&bars[b], (turns >> b) & 1u, P.err));
+        turns ^= 1u << b;
+        return ok;
+      };
+      // 128 keys' K or V by cp.async: CH 16-byte chunks a key
+      auto copy = [&](uint8_t* dst, const uint8_t* src, uint32_t rows, int kb, bool masked, auto chunks) {
+        constexpr int CH = decltype(chunks)::value, PER = 64 / CH;  // keys a pass
+        const int c = lt % CH, k0 = lt / CH;
+#pragma unroll 2
+        for (int g = 0; g < 8; ++g) {  // 16 keys
+          const uint32_t r = __shfl_sync(0xffffffffu, rows, g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) base[i] = __shfl_sync(0xffffffffu, rows, i);
-      uint8_t* d = dst + tile_byte(k0, c);
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const uint32_t r = base[i * PER / 16];
-        const int key = i * PER + k0;
-        const bool ok = r < kNoPage && (!masked || seen(kb + key));
-        cp_async16(d + i * PER * 128, src + c * 16 + static_cast<unsigned long long>(ok ? r + (key & 15) : 0u) * kRow,
-                   ok ? 16u : 0u);
-      }
-      cp_async_commit();
-    };
-    int page_n = nt > 1 ? fetch_page(j0 + 1) : -1;
-    uint32_t rows = to_row(j0, fetch_page(j0));
+          for (int i = 0; i < 16 / PER; ++i) {
+            const int key = 16 * g + i * PER + k0;
+            const bool ok = r < kNoPage && (!masked || seen(kb + key));
+            cp_async16(dst + tile_byte(key, c), src + c * 16 + static_cast<unsigned long long>(ok ? r + (key & 15) : 0u) * kRow,
+                       ok ? 16u : 0u);
+          }
+        }
+        cp_async_commit();
+      };
+      int page_n = nt > 1 ? fetch_page(j0 + 1) : -1;
+      uint32_t rows = to_row(j0, fetch_page(j0));
 
-    if constexpr (KVT == 0) {
-      // V of tile j as it has landed: zeroes where no row sees the key or its
-      // page is none (rows: the tile's), and for elements that are not
-      // finite, whose keys are remembered
-      auto clean = [&](int j, uint32_t rows, uint8_t* tile) {
-        const int slot = open_poison(j), kb = T.first_key(j);
-        const unsigned there = __ballot_sync(0xffffffffu, rows < kNoPage);
-        uint8_t* d = tile + tile_byte(lt >> 4, lt & 15);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint4 v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4*>(d + (8 * h + i) * 1024);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int key = 8 * (8 * h + i) + (lt >> 4);
-            uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, odd = 0u;
+      if constexpr (KVT == 0) {
+        // V of tile j as it has landed: zeroes for keys that no row sees or
+        // whose page is none (rows: the tile's); of keys that some rows see
+        // and others do not, the elements that are not finite become zeros
+        // and the key is remembered
+        auto clean = [&](int j, uint32_t r, uint8_t* tile) {
+          const int slot = open_poison(j), kb = T.first_key(j);
+          const unsigned there = __ballot_sync(0xffffffffu, r < kNoPage);
+#pragma unroll 4
+          for (int i = 0; i < 32; ++i) {
+            const int key = 4 * i + (lt >> 4);
+            const bool page = (there >> (key >> 4)) & 1u;
+            if (page && seen_by_all(kb + key)) continue;
+            uint4* at = reinterpret_cast<uint4*>(tile + tile_byte(key, lt & 15));
+            if (!page || !seen(kb + key)) {
+              *at = make_uint4(0u, 0u, 0u, 0u);
+              continue;
+            }
+            const uint4 v = *at;
+            uint32_t w[4] = {v.x, v.y, v.z, v.w}, odd = 0u;
             // an exponent of all ones carries into the sign's place
 #pragma unroll
             for (int e = 0; e < 4; ++e) odd |= ((w[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-            const bool none = !((there >> (4 * h + (i >> 1))) & 1u) || !seen(kb + key);
-            if (odd == 0u && !none) continue;
-            if (none) {
-              w[0] = w[1] = w[2] = w[3] = 0u;
-            } else {
+            if (odd == 0u) continue;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
-                if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
-              }
-              remember(slot, key);
+            for (int e = 0; e < 4; ++e) {
+              if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
+              if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
             }
-            *reinterpret_cast<uint4*>(d + (8 * h + i) * 1024) = make_uint4(w[0], w[1], w[2], w[3]);
+            remember(slot, key);
+            *at = make_uint4(w[0], w[1], w[2], w[3]);
           }
-        }
-      };
-      // Small pages: K and V by cp.async.  A tile's K is announced once its V
-      // is on the way, its V once the next tile's K is, or with its own data
-      // where there is nothing to start meanwhile or it is cleaned.
-      int v_open = -1;  // tile number whose V is on the way
-      for (int i = 0; i < nt; ++i) {
-        const int j = j0 + i, kb = T.first_key(j);
-        const uint32_t here = rows;
-        if (i + 1 < nt) rows = to_row(j + 1, page_n);
-        page_n = i + 2 < nt ? fetch_page(j + 2) : -1;
-        const bool hand = by_hand(j, here);
-        const int kbuf = i % RG::NK, vbuf = i % RG::NV;
-        if (P.box != 0) {
-          if (!hand) continue;
-          if (!wait_turn(sh.vgo, v_turn, vbuf)) break;
-          clean(j, here, sV + vbuf * kTile);
-          announce(&sh.vfull[vbuf]);
-          continue;
-        }
-        if (v_open >= 0 && !all_ok(mbar_done(&sh.kgo[kbuf], (k_turn >> kbuf) & 1u))) {
-          cp_async_wait<0>();  // (nothing to start meanwhile)
-          announce(&sh.vfull[v_open]);
-          v_open = -1;
-        }
-        if (!wait_turn(sh.kgo, k_turn, kbuf)) break;
-        if (warp == 8) publish(i, here, 0u);
-        copy(sK + kbuf * kTile, kvb, here, kb, hand, Int<16>());
-        if (v_open >= 0) {
-          cp_async_wait<1>();
-          announce(&sh.vfull[v_open]);
-          v_open = -1;
-        }
-        if (!wait_turn(sh.vgo, v_turn, vbuf)) break;
-        copy(sV + vbuf * kTile, kvb + 256, here, kb, hand, Int<16>());
-        cp_async_wait<1>();
-        announce(&sh.kfull[kbuf]);
-        if (hand) {
-          cp_async_wait<0>();
-          __syncwarp();
-          clean(j, here, sV + vbuf * kTile);
-          announce(&sh.vfull[vbuf]);
-        } else {
-          v_open = vbuf;
-        }
-      }
-      cp_async_wait<0>();
-      if (v_open >= 0) announce(&sh.vfull[v_open]);
-    } else {
-      // V: 16 codes a lane and load; the next tile's codes are in flight while
-      // this one's are converted
-      auto load = [&](int j, uint32_t r, uint4 (&v)[8]) {
-        const int kb = T.first_key(j);
-        const bool masked = tile_masked(j);
-        const uint8_t* src = kvb + 128 + (lt & 7) * 16;
-        uint32_t base[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) base[i] = __shfl_sync(0xffffffffu, r, i);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const bool ok = base[i] < kNoPage && (!masked || seen(kb + 16 * i + (lt >> 3)));
-          v[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (ok) v[i] = *reinterpret_cast<const uint4*>(src + static_cast<unsigned long long>(base[i] + (lt >> 3)) * kRow);
-        }
-      };
-      auto start_k = [&](int i, uint32_t r) {  // false: a wait gave up
-        if (P.box != 0) return true;
-        if (!wait_turn(sh.kgo, k_turn, i % RG::NK)) return false;
-        if (warp == 8) publish(i, r, scale_word(r));
-        copy(sK + (i % RG::NK) * RG::kKey, kvb, r, T.first_key(j0 + i), tile_masked(j0 + i), Int<8>());
-        return true;
-      };
-      auto end_k = [&](int i) {
-        if (P.box != 0) return;
-        cp_async_wait<0>();
-        announce(&sh.kfull[i % RG::NK]);
-      };
-      uint4 cur[8], nxt[8];
-      load(j0, rows, cur);
-      bool ok = start_k(0, rows);
-      if (ok) end_k(0);
-      const int dst0 = tile_byte(lt >> 3, 2 * (lt & 7)), dst1 = tile_byte(lt >> 3, 2 * (lt & 7) + 1);
-      for (int i = 0; i < nt && ok; ++i) {
-        const int j = j0 + i;
-        const bool more = i + 1 < nt;
-        if (more) {
-          rows = to_row(j + 1, page_n);
+        };
+        // Small pages: K and V by cp.async.  A tile's K is announced once its V
+        // is on the way, its V once the next tile's K is, or with its own data
+        // where there is nothing to start meanwhile or it is cleaned.
+        int v_open = -1;  // the buffer whose V is on the way
+        for (int i = 0; i < nt; ++i) {
+          const int j = j0 + i, kb = T.first_key(j);
+          const uint32_t here = rows;
+          if (i + 1 < nt) rows = to_row(j + 1, page_n);
           page_n = i + 2 < nt ? fetch_page(j + 2) : -1;
-          load(j + 1, rows, nxt);
-          ok = start_k(i + 1, rows);
-          if (!ok) break;
-        }
-        ok = all_ok(mbar_wait(&sh.vempty[i % RG::NV], ((i / RG::NV) & 1) ^ 1, P.err));
-        if (!ok) break;
-        const int slot = tile_masked(j) ? open_poison(j) : -1;
-        uint8_t* dst = sV + (i % RG::NV) * kTile;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int key = 16 * q + (lt >> 3);
-          uint32_t w[4] = {cur[q].x, cur[q].y, cur[q].z, cur[q].w}, h[8];
-          if (slot >= 0) {
-            bool odd = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-              for (int c = 0; c < 32; c += 8)
-                if (((w[e] >> c) & 0x7Fu) == 0x7Fu) {
-                  w[e] &= ~(0xFFu << c);
-                  odd = true;
-                }
-            if (odd) remember(slot, key);
+          const bool hand = by_hand(j, here);
+          const int kbuf = i % RG::NK, vbuf = i % RG::NV;
+          if (P.box != 0) {
+            if (!hand) continue;
+            if (!wait_turn(sh.vgo, v_turn, vbuf)) break;
+            clean(j, here, sV + vbuf * kTile);
+            announce(&sh.vfull[vbuf]);
+            continue;
           }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) e4m3x4_to_f16x2x2(w[e], h[2 * e], h[2 * e + 1]);
-          *reinterpret_cast<uint4*>(dst + dst0 + 2048 * q) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(dst + dst1 + 2048 * q) = make_uint4(h[4], h[5], h[6], h[7]);
+          if (v_open >= 0 && !all_ok(mbar_done(&sh.kgo[kbuf], (k_turn >> kbuf) & 1u))) {
+            cp_async_wait<0>();  // (nothing to start meanwhile)
+            announce(&sh.vfull[v_open]);
+            v_open = -1;
+          }
+          if (!wait_turn(sh.kgo, k_turn, kbuf)) break;
+          if (lt < 32) publish(i, here, 0u);
+          copy(sK + kbuf * kTile, kvb, here, kb, hand, Int<16>());
+          if (v_open >= 0) {
+            cp_async_wait<1>();
+            announce(&sh.vfull[v_open]);
+            v_open = -1;
+          }
+          if (!wait_turn(sh.vgo, v_turn, vbuf)) break;
+          copy(sV + vbuf * kTile, kvb + 256, here, kb, hand, Int<16>());
+          cp_async_wait<1>();
+          announce(&sh.kfull[kbuf]);
+          if (hand) {
+            cp_async_wait<0>();
+            clean(j, here, sV + vbuf * kTile);  // (each thread its own chunks)
+            announce(&sh.vfull[vbuf]);
+          } else {
+            v_open = vbuf;
+          }
         }
-        announce(&sh.vfull[i % RG::NV]);
-        if (more) end_k(i + 1);
+        cp_async_wait<0>();
+        if (v_open >= 0) announce(&sh.vfull[v_open]);
+      } else {
+        // Small pages: this tile's codes by cp.async while the last one's V is
+        // converted.
+        auto start = [&](int i, uint32_t r) {  // false: a wait gave up
+          if (P.box != 0) return true;
+          if (!wait_turn(sh.kgo, k_turn, i % RG::NK)) return false;
+          if (lt < 32) publish(i, r, scale_word(r));
+          const bool hand = by_hand(j0 + i, r);
+          copy(sK + (i % RG::NK) * RG::kKey, kvb, r, T.first_key(j0 + i), hand, Int<8>());
+          // (V's codes: each thread converts what it copied, so the buffer is
+          // its own to refill)
+          copy(sR + (i % RG::NR) * kAtom, kvb + 128, r, T.first_key(j0 + i), hand, Int<8>());
+          return true;
+        };
+        auto end = [&](int i) {
+          if (P.box != 0) return;
+          cp_async_wait<0>();
+          announce(&sh.kfull[i % RG::NK]);
+        };
+        uint32_t here = rows;
+        bool ok = start(0, here);
+        if (ok) end(0);
+        const int c = lt & 7, k0 = lt >> 3;
+        for (int i = 0; i < nt && ok; ++i) {
+          const int j = j0 + i, kb = T.first_key(j), vbuf = i % RG::NV, rbuf = i % RG::NR;
+          const bool more = i + 1 < nt;
+          const uint32_t next = more ? to_row(j + 1, page_n) : kUnseen;
+          page_n = i + 2 < nt ? fetch_page(j + 2) : -1;
+          if (more) ok = start(i + 1, next);
+          if (ok && P.box != 0) ok = all_ok(mbar_wait(&sh.rfull[rbuf], (i / RG::NR) & 1, P.err));
+          ok = ok && all_ok(mbar_wait(&sh.vempty[vbuf], ((i / RG::NV) & 1) ^ 1, P.err));
+          if (!ok) break;
+          const bool hand = by_hand(j, here);
+          const int slot = hand ? open_poison(j) : 0;
+          const unsigned there = __ballot_sync(0xffffffffu, here < kNoPage);
+          const uint8_t* src = sR + rbuf * kAtom + tile_byte(k0, c);
+          uint8_t* d0 = sV + vbuf * kTile + tile_byte(k0, 2 * c);
+          uint8_t* d1 = sV + vbuf * kTile + tile_byte(k0, 2 * c + 1);
+#pragma unroll 4
+          for (int q = 0; q < 16; ++q) {
+            const int key = 8 * q + k0;
+            const uint4 v = *reinterpret_cast<const uint4*>(src + 1024 * q);
+            uint32_t w[4] = {v.x, v.y, v.z, v.w}, f[8];
+            if (hand) {
+              if (!((there >> (key >> 4)) & 1u) || !seen(kb + key)) {
+                w[0] = w[1] = w[2] = w[3] = 0u;
+              } else if (!seen_by_all(kb + key)) {
+                bool odd = false;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) cur[q] = nxt[q];
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                  for (int b = 0; b < 32; b += 8)
+                    if (((w[e] >> b) & 0x7Fu) == 0x7Fu) {
+                      w[e] &= ~(0xFFu << b);
+                      odd = true;
+                    }
+                if (odd) remember(slot, key);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) e4m3x4_to_f16x2x2(w[e], f[2 * e], f[2 * e + 1]);
+            *reinterpret_cast<uint4*>(d0 + 1024 * q) = make_uint4(f[0], f[1], f[2], f[3]);
+            *reinterpret_cast<uint4*>(d1 + 1024 * q) = make_uint4(f[4], f[5], f[6], f[7]);
+          }
+          announce(&sh.vfull[vbuf]);
+          if (P.box != 0 && lane == 0) mbar_arrive(&sh.rempty[rbuf]);
+          if (more) end(i + 1);
+          here = next;
+        }
+        cp_async_wait<0>();
       }
-      cp_async_wait<0>();
-    }
-    if (lt == 0) sh.poison_n = min(masked_n, kPoison);
-    mbar_arrive(&sh.loads_done);
-  } else if (warp >= 12) {
-    // ------------------------------------------------------------ MMA
-    regs_down<kMmaRegs>();
-    if (warp == 12) {
+      if (lt == 0) sh.poison_n = min(masked_n, kPoison);
+      mbar_arrive(&sh.loads_done);
+    } else if (warp == kSoftWarps) {
+      // ---------------------------------------------------------- MMA
       constexpr uint32_t fmt = KVT == 0 ? 1u : 0u;  // bf16 or f16
       const uint32_t id_s = umma_idesc(fmt, 128, 128);  // (format 0 is e4m3 among 8-bit operands)
       const uint32_t id_o = id_s | (1u << 16);          // B is N-major
@@ -601,19 +626,15 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
             mma_ss_e4m3(tmem + 128 * x, a + ((atom + off) >> 4), b + (off >> 4), id_s, kk != 0 ? 1u : 0u);
         }
       };
-      // O += P V of tile number i, a half of its keys at a time
+      // O += P V of tile number i
       auto values = [&](int x, int i) {
         const uint32_t b = v0 + (((i % RG::NV) * kTile) >> 4);
+        if (!all_ok(mbar_wait(&sh.p_ready[x], i & 1, P.err))) return false;
+        tc_fence_after_sync();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!all_ok(mbar_wait(&sh.p_ready[x][h], i & 1, P.err))) return false;
-          tc_fence_after_sync();
-#pragma unroll
-          for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-            mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * kk, b + ((kk * 2048) >> 4), id_o,
-                   i == 0 && kk == 0 ? 0u : 1u);
-          if (h == 0) mma_commit(&sh.half_done[x]);
-        }
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * kk, b + ((kk * 2048) >> 4), id_o,
+                 i == 0 && kk == 0 ? 0u : 1u);
         return true;
       };
       auto wait_k = [&](int i) {
@@ -655,8 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         }
       }
       mma_commit(&sh.o_full);
-    } else if (warp == 13) {
-      // ---------------------------------------------------------- loads by TMA
+    } else if (warp == kSoftWarps + 1) {
+      // ---------------------------------------------------------- TMA
       int page_n = nt > 1 ? fetch_page(j0 + 1) : -1;
       uint32_t rows = to_row(j0, fetch_page(j0)), word = scale_word(rows);
       // the boxes of one tile that hold keys of the cache, on `full` with
@@ -668,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         for (int k = 0; k < 128; k += P.box) n += ((there >> (k >> 4)) & blocks) != 0u;
         if (lane == 0) {
           mbar_arrive_expect_tx(full, n * atoms * P.box * 128);
-          if (arrivals > 1) mbar_arrive_n(full, arrivals - 1);
+          if (arrivals > 1) mbar_arrive(full);
         }
         __syncwarp();
         for (int k = 0; k < 128; k += P.box) {
@@ -692,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         if (!all_ok(mbar_wait(&sh.kempty[kbuf], ((i / RG::NK) & 1) ^ 1, P.err))) break;
         if (P.box != 0) {
           publish(i, here, word_here);
-          tile(&sh.kfull[kbuf], 4, sK + kbuf * RG::kKey, here, 0, KVT == 0 ? 2 : 1);
+          tile(&sh.kfull[kbuf], 2, sK + kbuf * RG::kKey, here, 0, KVT == 0 ? 2 : 1);
         } else if (lane == 0) {
           mbar_arrive(&sh.kgo[kbuf]);
         }
@@ -703,34 +724,39 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           } else if (by_hand(j, here)) {
             tile(&sh.vgo[vbuf], 1, sV + vbuf * kTile, here, 128, 2);
           } else {
-            tile(&sh.vfull[vbuf], 4, sV + vbuf * kTile, here, 128, 2);
+            tile(&sh.vfull[vbuf], 2, sV + vbuf * kTile, here, 128, 2);
           }
+        } else if (P.box != 0) {
+          const int rbuf = i % RG::NR;
+          if (!all_ok(mbar_wait(&sh.rempty[rbuf], ((i / RG::NR) & 1) ^ 1, P.err))) break;
+          tile(&sh.rfull[rbuf], 1, sR + rbuf * kAtom, here, 128, 1);
         }
       }
     }
-  } else if (warp < 4 || two) {
+  } else if (warp < 8 || two) {
     // ------------------------------------------------------------ softmax
     regs_up<kSoftmaxRegs>();
-    // ---- Q of the warp's own 32 M rows, a half-warp per row, eight in flight
+    // M row im of tile x; this thread's 64 keys (at the end: dims) of it
+    const int x = warp >> 3, hf = (warp >> 2) & 1, im = 32 * (warp & 3) + lane, m = 128 * x + im;
+    const int pair = 1 + 4 * x + (warp & 3);  // the barrier of the row's two warps
+    const bool live = im < R * G && x * R + im / G < nrows;
+    // its position (-1: before the start)
+    const int p = live ? max(P.logical[row0 + x * R + im / G], -1) : 0;
+    // ---- Q of the two warps' 32 M rows, sixteen each, a half-warp per row
     {
-      const int r = (warp >> 2) * R + (tid & 127) / G;
-      sh.pos[tid] = (tid & 127) < R * G && r < nrows ? max(P.logical[row0 + r], -1) : INT_MIN;
-    }
-#pragma unroll 1
-    for (int b = 0; b < 32; b += 16) {
-      const int lane16 = lane & 15;
+      uint8_t* tile = sQ + x * kTile;
+      const int lane16 = lane & 15, im0 = 32 * (warp & 3) + 16 * hf + (lane >> 4);
       uint4 v[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const int m = 32 * warp + b + 2 * u + (lane >> 4), im = m & 127, r = (warp >> 2) * R + im / G;
+        const int im = im0 + 2 * u, r = x * R + im / G;
         v[u] = make_uint4(0u, 0u, 0u, 0u);
         if (im < R * G && r < nrows)
           v[u] = *reinterpret_cast<const uint4*>(P.q + (static_cast<long long>(row0 + r) * P.hq + kvh * G + im % G) * 128 + 8 * lane16);
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const int m = 32 * warp + b + 2 * u + (lane >> 4), im = m & 127;
-        uint8_t* tile = sQ + (warp >> 2) * kTile;
+        const int im = im0 + 2 * u;
         float qs = 0.08838834764831845f * kLog2e;
         if constexpr (KVT == 0) {
           *reinterpret_cast<uint4*>(tile + tile_byte(im, lane16)) = v[u];
@@ -772,55 +798,37 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
           *reinterpret_cast<uint2*>(dst + kAtom) = make_uint2(lo[0], lo[1]);
         }
-        if (lane16 == 0) sh.qs[m] = qs;
+        if (lane16 == 0) sh.qs[128 * x + im] = qs;
       }
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.q_ready);
-    const int x = warp >> 2, m = tid;  // M row m & 127 of tile x
+    pair_sync(pair);
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t ts = tmem + 128 * x + lanes, to = tmem + 256 + 128 * x + lanes;
+    const uint32_t ts = tmem + 128 * x + lanes, to = tmem + 256 + 128 * x + 64 * hf + lanes;
     const float qs = fabsf(sh.qs[m]);
-    const int p = sh.pos[m];
-    // the tile's own bounds decide which key tiles need masks
-    const int hi_all = __reduce_min_sync(0xffffffffu, p == INT_MIN ? INT_MAX : p);
-    const int lo_all = __reduce_max_sync(0xffffffffu, p == INT_MIN ? INT_MIN : p - P.window + 1);
+    // the 32 rows' own bounds decide which key tiles need masks
+    const int hi_all = __reduce_min_sync(0xffffffffu, live ? p : INT_MAX);
+    const int lo_all = __reduce_max_sync(0xffffffffu, live ? p - P.window + 1 : INT_MIN);
     float ref = -INFINITY, l = sh.qs[m] < 0.f ? __int_as_float(0x7fffffff) : 0.f;
+    // (a wait that gives up ends the waiting, not the loop: the two warps
+    // always meet)
     bool ok = true;
+#pragma unroll 1
     for (int j = 0; j < nt; ++j) {
-      const int kb = T.first_key(j0 + j), slot = j % kSlots;
-      // its masks and scales, then its scores.  (A slot's next tile is
+      const int kb = T.first_key(j0 + j) + 64 * hf, slot = j % kSlots;
+      // the tile's masks and scales, then its scores.  (A slot's next tile is
       // published only after both softmaxes are done with this one: its K
-      // waits for a ring buffer that S of tile j + 2 frees.)
-      ok = all_ok(mbar_wait(&sh.info[slot], (j / kSlots) & 1, P.err) && mbar_wait(&sh.s_full[x], j & 1, P.err));
-      if (!ok) break;
+      // waits for a ring buffer that S of a later tile frees.)
+      ok = all_ok(ok && mbar_wait(&sh.info[slot], (j / kSlots) & 1, P.err) && mbar_wait(&sh.s_full[x], j & 1, P.err));
       tc_fence_after_sync();
-      const bool plain = kb + 127 <= hi_all && (kb >= lo_all || kb + 127 < P.sinks) && sh.check[slot] == 0;
-      uint32_t sc[8];  // (block scales)
+      const bool plain = kb + 63 <= hi_all && (kb >= lo_all || kb + 63 < P.sinks) && sh.check[slot] == 0;
+      uint32_t sc[4];  // (block scales)
       if constexpr (KVT == 2) {
-        const uint4 a = *reinterpret_cast<const uint4*>(&sh.scale[slot][0]);
-        const uint4 b = *reinterpret_cast<const uint4*>(&sh.scale[slot][4]);
+        const uint4 a = *reinterpret_cast<const uint4*>(&sh.scale[slot][4 * hf]);
         sc[0] = a.x; sc[1] = a.y; sc[2] = a.z; sc[3] = a.w;
-        sc[4] = b.x; sc[5] = b.y; sc[6] = b.z; sc[7] = b.w;
       }
-      // S of columns 64 h .. 64 h + 63: asked for, and there with its masks
-      auto ask_s = [&](int h, uint32_t (&r)[2][32]) {
-        tmem_ld32_issue(ts + 64 * h, r[0]);
-        tmem_ld32_issue(ts + 64 * h + 32, r[1]);
-      };
-      auto mask_s = [&](int h, uint32_t (&r)[2][32]) {
-        if (plain) return;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int k0 = 64 * h + 32 * c;
-          const int hi = p - kb + 1 - k0, lo = p - P.window + 1 - kb - k0, sk = P.sinks - kb - k0;
-          uint32_t vis = low_bits(hi) & (~low_bits(lo) | low_bits(sk));
-          if (sh.check[slot] != 0) vis &= sh.valid[slot][2 * h + c];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) r[c][i] = (vis & (1u << i)) != 0u ? r[c][i] : 0xFF800000u;
-        }
-      };
       // the largest of 16 scores
       auto max16 = [&](const uint32_t* rr) {
         float bm = max3(__uint_as_float(rr[0]), __uint_as_float(rr[1]), __uint_as_float(rr[2]));
@@ -838,119 +846,120 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         if constexpr (KVT == 2) return fmaf(bm, fmaxf(qs * bf16_lo(sc[b]), kLeast), bf16_hi(sc[b]));
         return bm * qs;
       };
-      // The weights of 64 keys are taken against the reference as it stands;
-      // only where one of them has grown too large (or a row has no reference
-      // yet) is it moved and the 64 done again.  (S is in place until P is
-      // stored.)  The first half's P is handed over while the second's is
-      // taken: its product runs meanwhile.
-      auto half = [&](int h, uint32_t (&r)[2][32]) {
-        bool moved = __any_sync(0xffffffffu, ref == -INFINITY);
-        uint32_t pk[32];
-        float sum;
+      // The weights are taken against the reference as it stands; only where
+      // one of the row's has grown too large (or a row has no reference yet)
+      // is it moved and the tile done again.  (S is in place until P is
+      // stored, and P is stored only after the two warps have met: the second
+      // half's lies over the first half's S.)
+      bool moved = __any_sync(0xffffffffu, ref == -INFINITY);
+      uint32_t pk[32];
+      float sum;
 #pragma unroll 1
-        while (true) {
-          if (moved) {
-            float mx = -INFINITY;
+      while (true) {
+        uint32_t r[2][32];
+        tmem_ld32_issue(ts + 64 * hf, r[0]);
+        tmem_ld32_issue(ts + 64 * hf + 32, r[1]);
+        tmem_wait_ld32(r[0]);
+        tmem_wait_ld32(r[1]);
+        if (!plain) {
 #pragma unroll
-            for (int b = 0; b < 4; ++b) mx = fmaxf(mx, exponent(max16(&r[b >> 1][16 * (b & 1)]), 4 * h + b));
-            // moves the reference up, the sums with it
-            const float mn = fmaxf(ref, mx + kRoom<KVT>);
-            const float al = ex2_ftz(ref - (mn == -INFINITY ? 0.f : mn));
-            l *= al;
-            if (h == 1) {  // (the first half's product is in O, or on its way)
-              ok = all_ok(mbar_wait(&sh.half_done[x], j & 1, P.err)) && ok;
-              tc_fence_after_sync();
-            }
-            if (j > 0 || h == 1) {  // (S of this tile is complete, so O of the last one is)
-              uint32_t o[32];
-#pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                tmem_ld32_issue(to + 32 * c, o);
-                tmem_wait_ld32(o);
+          for (int c = 0; c < 2; ++c) {
+            const int k0 = kb + 32 * c;
+            uint32_t vis = low_bits(p + 1 - k0) & (~low_bits(p - P.window + 1 - k0) | low_bits(P.sinks - k0));
+            if (sh.check[slot] != 0) vis &= sh.valid[slot][2 * hf + c];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-                tmem_st32(to + 32 * c, o);
-              }
-            }
-            ref = mn;
+            for (int i = 0; i < 32; ++i) r[c][i] = (vis & (1u << i)) != 0u ? r[c][i] : 0xFF800000u;
           }
-          const float neg = ref == -INFINITY ? 0.f : -ref;
-          unsigned long long sum2 = 0ull;  // (two sums, of even and odd keys)
-          uint32_t any_bits = 0u;
-          sum = 0.f;
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const uint32_t* rr = &r[b >> 1][16 * (b & 1)];
-            float f = qs, base = neg, inv_vs = 1.0f;
-            if constexpr (KVT == 2) {
-              f = fmaxf(f * bf16_lo(sc[4 * h + b]), kLeast);
-              base += bf16_hi(sc[4 * h + b]);
-              inv_vs = ex2_ftz(-bf16_hi(sc[4 * h + b]));
-            }
-            const unsigned long long f2 = f32x2_pack(f, f), base2 = f32x2_pack(base, base);
-            unsigned long long bs2 = KVT == 2 ? 0ull : sum2;
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              float p0, p1;
-              f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(rr[i]), __uint_as_float(rr[i + 1])), f2, base2), p0, p1);
-              p0 = ex2_ftz(p0);
-              p1 = ex2_ftz(p1);
-              bs2 = f32x2_add(bs2, f32x2_pack(p0, p1));
-              pk[8 * b + (i >> 1)] = KVT == 0 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) any_bits |= pk[8 * b + i] | pk[8 * b + i + 1];
-            if constexpr (KVT == 2)
-              sum = fmaf(f32x2_hsum(bs2), inv_vs, sum);
-            else
-              sum2 = bs2;
-          }
-          if constexpr (KVT != 2) sum = f32x2_hsum(sum2);
-          if (moved || !__any_sync(0xffffffffu, (any_bits & kTwo) != 0u)) break;
-          moved = true;
         }
-        l += sum;
-        tmem_st32(ts + 32 * h, pk);
-        tmem_wait_st();
-        tc_fence_before_sync();
-        mbar_arrive(&sh.p_ready[x][h]);
-      };
-      uint32_t r0[2][32], r1[2][32];
-      ask_s(0, r0);
-      tmem_wait_ld32(r0[0]);
-      tmem_wait_ld32(r0[1]);
-      ask_s(1, r1);
-      mask_s(0, r0);
-      half(0, r0);
-      tmem_wait_ld32(r1[0]);
-      tmem_wait_ld32(r1[1]);
-      mask_s(1, r1);
-      half(1, r1);
+        if (moved) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) mx = fmaxf(mx, exponent(max16(&r[b >> 1][16 * (b & 1)]), b));
+          sh.pair[j & 1][hf][m] = mx;
+          pair_sync(pair);
+          mx = fmaxf(mx, sh.pair[j & 1][hf ^ 1][m]);
+          // moves the reference up, the sums with it
+          const float mn = fmaxf(ref, mx + kRoom<KVT>);
+          const float al = ex2_ftz(ref - (mn == -INFINITY ? 0.f : mn));
+          l *= al;
+          if (j > 0) {  // (S of this tile is complete, so O of the last one is)
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[16];
+              tmem_ld16(to + 16 * c, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+              tmem_st16(to + 16 * c, o);
+            }
+          }
+          ref = mn;
+        }
+        const float neg_ref = ref == -INFINITY ? 0.f : -ref;
+        unsigned long long sum2 = 0ull;  // (two sums, of even and odd keys)
+        uint32_t any_bits = 0u;
+        sum = 0.f;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t* rr = &r[b >> 1][16 * (b & 1)];
+          float f = qs, base = neg_ref, inv_vs = 1.0f;
+          if constexpr (KVT == 2) {
+            f = fmaxf(f * bf16_lo(sc[b]), kLeast);
+            base += bf16_hi(sc[b]);
+            inv_vs = ex2_ftz(-bf16_hi(sc[b]));
+          }
+          const unsigned long long f2 = f32x2_pack(f, f), base2 = f32x2_pack(base, base);
+          unsigned long long bs2 = KVT == 2 ? 0ull : sum2;
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            float p0, p1;
+            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(rr[i]), __uint_as_float(rr[i + 1])), f2, base2), p0, p1);
+            p0 = ex2_ftz(p0);
+            p1 = ex2_ftz(p1);
+            bs2 = f32x2_add(bs2, f32x2_pack(p0, p1));
+            pk[8 * b + (i >> 1)] = KVT == 0 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) any_bits |= pk[8 * b + i] | pk[8 * b + i + 1];
+          if constexpr (KVT == 2)
+            sum = fmaf(f32x2_hsum(bs2), inv_vs, sum);
+          else
+            sum2 = bs2;
+        }
+        if constexpr (KVT != 2) sum = f32x2_hsum(sum2);
+        if (moved || !pair_any(pair, (any_bits & kTwo) != 0u)) break;
+        moved = true;
+      }
+      l += sum;
+      tmem_st32(ts + 32 * hf, pk);
+      tmem_wait_st();
+      tc_fence_before_sync();
+      mbar_arrive(&sh.p_ready[x]);
     }
     // ---- output
+    sh.pair[nt & 1][hf][m] = l;
+    pair_sync(pair);
+    l += sh.pair[nt & 1][hf ^ 1][m];
     ok = all_ok(ok && mbar_wait(&sh.o_full, 0, P.err) && mbar_wait(&sh.loads_done, 0, P.err));
     tc_fence_after_sync();
-    const int im = m & 127, rr = x * R + im / G;
-    const bool act = ok && im < R * G && rr < nrows;
-    const long long head = static_cast<long long>(row0 + rr) * P.hq + kvh * G + im % G;
+    const long long head = static_cast<long long>(row0 + x * R + im / G) * P.hq + kvh * G + im % G;
+    const long long ph = static_cast<long long>(split) * P.rows * P.hq + head;
     // (a NaN sum is not an empty row)
     const float inv = l == 0.f ? 0.f : (KVT == 1 ? P.v_scale : 1.0f) / l;
     bool poisoned = false;
     for (int b = 0; b < sh.poison_n; ++b)
       poisoned |= (sh.poison[b][0] | sh.poison[b][1] | sh.poison[b][2] | sh.poison[b][3]) != 0u;
-    const long long ph = static_cast<long long>(split) * P.rows * P.hq + head;
-    // the warp's 32 rows cross to whole-row stores through its own rows of
-    // the Q tile, which no MMA reads any more
+    // the warp's 32 rows and 64 dims cross to coalesced stores through their
+    // own place in the Q tile, which no MMA reads any more
     uint8_t* tile = sQ + x * kTile;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < 2; ++c) {
       uint32_t o[32];
       tmem_ld32_issue(to + 32 * c, o);
       tmem_wait_ld32(o);
       float f[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * inv;
-      if (act)
+      if (live && ok)
       if (poisoned) {  // what the row sees of the remembered elements
 #pragma unroll 1
         for (int b = 0; b < sh.poison_n * 128; ++b) {
@@ -959,7 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           if (key > p || !(key > p - P.window || key < P.sinks)) continue;
           const int blk = key / P.page;
           const int pid = P.block_table[static_cast<long long>(req) * P.bt_stride + blk];
-          const long long at = ((static_cast<long long>(pid) * P.hkv + kvh) * P.page + key - blk * P.page) * 256 + 128 + 32 * c;
+          const long long at = ((static_cast<long long>(pid) * P.hkv + kvh) * P.page + key - blk * P.page) * 256 + 128 + 64 * hf + 32 * c;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const float v = KVT == 0 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(P.kv)[at + i]) << 16)
@@ -969,45 +978,44 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         }
       }
       if (P.splits > 1) {
-        if (!act) continue;
-        float4* po = reinterpret_cast<float4*>(P.part_o + ph * 128 + 32 * c);
+        if (!live || !ok) continue;
+        float4* po = reinterpret_cast<float4*>(P.part_o + ph * 128 + 64 * hf + 32 * c);
 #pragma unroll
         for (int q = 0; q < 8; ++q) po[q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
       } else {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<uint4*>(tile + tile_byte(im, 4 * c + q)) =
+          *reinterpret_cast<uint4*>(tile + tile_byte(im, 8 * hf + 4 * c + q)) =
               make_uint4(pack_bf16x2(f[8 * q], f[8 * q + 1]), pack_bf16x2(f[8 * q + 2], f[8 * q + 3]),
                          pack_bf16x2(f[8 * q + 4], f[8 * q + 5]), pack_bf16x2(f[8 * q + 6], f[8 * q + 7]));
       }
     }
     if (P.splits > 1) {
-      if (act) P.part_lse[ph] = l == 0.f ? -INFINITY : ref + log2f(l);
+      if (live && ok && hf == 0) P.part_lse[ph] = l == 0.f ? -INFINITY : ref + log2f(l);
     } else if (ok) {
       __syncwarp();
-#pragma unroll 1
-      for (int b = 0; b < 32; b += 16) {
-        const int c16 = lane & 15;
-        uint4 gate[8];
+      // four rows at a time, eight lanes each
+      const int c8 = 8 * hf + (lane & 7), im0 = 32 * (warp & 3) + (lane >> 3);
+      uint4 gate[8];
+      auto at = [&](int i2) {
+        return (static_cast<long long>(row0 + x * R + i2 / G) * P.hq + kvh * G + i2 % G) * 128 + 8 * c8;
+      };
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int i2 = (32 * warp + b + 2 * u + (lane >> 4)) & 127, r2 = x * R + i2 / G;
-          const long long at = (static_cast<long long>(row0 + r2) * P.hq + kvh * G + i2 % G) * 128 + 8 * c16;
-          gate[u] = i2 < R * G && r2 < nrows ? load_gate(P, at) : make_uint4(0u, 0u, 0u, 0u);
-        }
+      for (int u = 0; u < 8; ++u) {
+        const int i2 = im0 + 4 * u;
+        gate[u] = i2 < R * G && x * R + i2 / G < nrows ? load_gate(P, at(i2)) : make_uint4(0u, 0u, 0u, 0u);
+      }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int i2 = (32 * warp + b + 2 * u + (lane >> 4)) & 127, r2 = x * R + i2 / G;
-          if (i2 >= R * G || r2 >= nrows) continue;
-          store_gated(P, (static_cast<long long>(row0 + r2) * P.hq + kvh * G + i2 % G) * 128 + 8 * c16,
-                      *reinterpret_cast<const uint4*>(tile + tile_byte(i2, c16)), gate[u]);
-        }
+      for (int u = 0; u < 8; ++u) {
+        const int i2 = im0 + 4 * u;
+        if (i2 < R * G && x * R + i2 / G < nrows)
+          store_gated(P, at(i2), *reinterpret_cast<const uint4*>(tile + tile_byte(i2, c8)), gate[u]);
       }
     }
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kSoftWarps) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
