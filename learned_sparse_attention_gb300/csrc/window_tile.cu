@@ -357,12 +357,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   const bool page_pow2 = (P.page & (P.page - 1)) == 0;
   const int page_shift = __ffs(P.page) - 1;
   auto seen = [&](int key) { return key <= pmax && (key >= wlo || key < P.sinks); };
-  // every row of the CTA sees it
-  auto seen_by_all = [&](int key) { return !neg && key <= pmin && (key >= wlo_all || key < P.sinks); };
+  // every row of the CTA sees keys a .. b; none does any of them
+  auto all_seen = [&](int a, int b) { return !neg && b <= pmin && (a >= wlo_all || b < P.sinks); };
+  auto none_seen = [&](int a, int b) { return a > pmax || (b < wlo && a >= P.sinks); };
   // some row of the CTA does not see all of tile j
   auto tile_masked = [&](int j) {
     const int kb = T.first_key(j);
-    return neg || !((kb >= wlo_all || kb + 127 < P.sinks) && kb + 127 <= pmin);
+    return !all_seen(kb, kb + 127);
   };
   // Page id, then cache row, of the first key of 16-key block (lane & 7) of
   // tile j; kUnseen where there is nothing to see, kNoPage where the page is
@@ -464,29 +465,33 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         auto clean = [&](int j, uint32_t r, uint8_t* tile) {
           const int slot = open_poison(j), kb = T.first_key(j);
           const unsigned there = __ballot_sync(0xffffffffu, r < kNoPage);
-#pragma unroll 4
-          for (int i = 0; i < 32; ++i) {
-            const int key = 4 * i + (lt >> 4);
-            const bool page = (there >> (key >> 4)) & 1u;
-            if (page && seen_by_all(kb + key)) continue;
-            uint4* at = reinterpret_cast<uint4*>(tile + tile_byte(key, lt & 15));
-            if (!page || !seen(kb + key)) {
-              *at = make_uint4(0u, 0u, 0u, 0u);
-              continue;
-            }
-            const uint4 v = *at;
-            uint32_t w[4] = {v.x, v.y, v.z, v.w}, odd = 0u;
-            // an exponent of all ones carries into the sign's place
+#pragma unroll 1
+          for (int g = 0; g < 128; g += 16) {
+            const bool page = (there >> (g >> 4)) & 1u;
+            if (page && all_seen(kb + g, kb + g + 15)) continue;
+            const bool none = !page || none_seen(kb + g, kb + g + 15);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) odd |= ((w[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-            if (odd == 0u) continue;
+            for (int i = 0; i < 4; ++i) {
+              const int key = g + 4 * i + (lt >> 4);
+              uint4* at = reinterpret_cast<uint4*>(tile + tile_byte(key, lt & 15));
+              if (none || !seen(kb + key)) {
+                *at = make_uint4(0u, 0u, 0u, 0u);
+                continue;
+              }
+              const uint4 v = *at;
+              uint32_t w[4] = {v.x, v.y, v.z, v.w}, odd = 0u;
+              // an exponent of all ones carries into the sign's place
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
-              if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
+              for (int e = 0; e < 4; ++e) odd |= ((w[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+              if (odd == 0u || all_seen(kb + key, kb + key)) continue;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
+                if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
+              }
+              remember(slot, key);
+              *at = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            remember(slot, key);
-            *at = make_uint4(w[0], w[1], w[2], w[3]);
           }
         };
         // Small pages: K and V by cp.async.  A tile's K is announced once its V
@@ -572,15 +577,32 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           const uint8_t* src = sR + rbuf * kAtom + tile_byte(k0, c);
           uint8_t* d0 = sV + vbuf * kTile + tile_byte(k0, 2 * c);
           uint8_t* d1 = sV + vbuf * kTile + tile_byte(k0, 2 * c + 1);
-#pragma unroll 4
-          for (int q = 0; q < 16; ++q) {
-            const int key = 8 * q + k0;
-            const uint4 v = *reinterpret_cast<const uint4*>(src + 1024 * q);
-            uint32_t w[4] = {v.x, v.y, v.z, v.w}, f[8];
-            if (hand) {
-              if (!((there >> (key >> 4)) & 1u) || !seen(kb + key)) {
-                w[0] = w[1] = w[2] = w[3] = 0u;
-              } else if (!seen_by_all(kb + key)) {
+          auto convert = [&](int q, uint4 v) {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t f[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) e4m3x4_to_f16x2x2(w[e], f[2 * e], f[2 * e + 1]);
+            *reinterpret_cast<uint4*>(d0 + 1024 * q) = make_uint4(f[0], f[1], f[2], f[3]);
+            *reinterpret_cast<uint4*>(d1 + 1024 * q) = make_uint4(f[4], f[5], f[6], f[7]);
+          };
+          if (!hand) {
+#pragma unroll
+            for (int q = 0; q < 16; q += 8) {
+              uint4 v[8];
+#pragma unroll
+              for (int u = 0; u < 8; ++u) v[u] = *reinterpret_cast<const uint4*>(src + 1024 * (q + u));
+#pragma unroll
+              for (int u = 0; u < 8; ++u) convert(q + u, v[u]);
+            }
+          } else {
+#pragma unroll 1
+            for (int q = 0; q < 16; ++q) {
+              const int key = 8 * q + k0;
+              uint4 v = *reinterpret_cast<const uint4*>(src + 1024 * q);
+              if (!((there >> (q >> 1)) & 1u) || !seen(kb + key)) {
+                v = make_uint4(0u, 0u, 0u, 0u);
+              } else if (!all_seen(kb + key, kb + key)) {
+                uint32_t w[4] = {v.x, v.y, v.z, v.w};
                 bool odd = false;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -591,12 +613,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
                       odd = true;
                     }
                 if (odd) remember(slot, key);
+                v = make_uint4(w[0], w[1], w[2], w[3]);
               }
+              convert(q, v);
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) e4m3x4_to_f16x2x2(w[e], f[2 * e], f[2 * e + 1]);
-            *reinterpret_cast<uint4*>(d0 + 1024 * q) = make_uint4(f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<uint4*>(d1 + 1024 * q) = make_uint4(f[4], f[5], f[6], f[7]);
           }
           announce(&sh.vfull[vbuf]);
           if (P.box != 0 && lane == 0) mbar_arrive(&sh.rempty[rbuf]);
