@@ -56,14 +56,16 @@ constexpr int kTile = 128 * 256;  // bytes of 128 rows of 128 16-bit values, two
 constexpr int kAtom = 128 * 128;
 constexpr int kSlots = 4;        // tiles whose scales and page masks are kept
 constexpr int kPoison = 32;      // masked tiles that can remember odd V elements
-// A row's reference is set so that its largest weight is 2^-kRoom, and moved
-// when a weight reaches 2: rooms of 2^8 and (f16 weights, whose subnormals
-// begin at 2^-14) 2^5.  That a weight has reached 2 shows in the top bit of
-// its exponent, so a tile is checked by or-ing its packed weights: half the
-// instructions of a maximum.
+// A row's reference is moved when a weight has grown by 2^8 (bf16) or 2^10.
+// bf16 weights: it is set so that the largest is 2^-7; that one has reached 2
+// shows in the top bit of its exponent, so a tile is checked by or-ing its
+// packed weights, half the instructions of a maximum.  f16 weights, whose
+// subnormals begin at 2^-14, are set to 1 and their packed maximum is taken
+// (the same trick with room for 2^5 moved references so often that a chunk
+// took 560 instead of 536 us).
 template <int KVT>
-constexpr float kRoom = KVT == 0 ? 7.0f : 4.0f;
-constexpr uint32_t kTwo = 0x40004000u;  // (bf16 and f16 alike)
+constexpr float kRoom = KVT == 0 ? 7.0f : 0.0f;
+constexpr uint32_t kTwo = 0x40004000u;
 constexpr float kLeast = 1.2e-38f;  // a score's factor is never 0: masked scores are -inf
 
 // The rings.  e4m3 caches: K tiles stay codes, half the size, and V's codes
@@ -917,6 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         const float neg_ref = ref == -INFINITY ? 0.f : -ref;
         unsigned long long sum2 = 0ull;  // (two sums, of even and odd keys)
         uint32_t any_bits = 0u;
+        __half2 top = __float2half2_rn(0.f);
         sum = 0.f;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -939,14 +942,22 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
             pk[8 * b + (i >> 1)] = KVT == 0 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
           }
 #pragma unroll
-          for (int i = 0; i < 8; i += 2) any_bits |= pk[8 * b + i] | pk[8 * b + i + 1];
+          for (int i = 0; i < 8; i += 2) {
+            const uint32_t a = pk[8 * b + i], c = pk[8 * b + i + 1];
+            if constexpr (KVT == 0)
+              any_bits |= a | c;
+            else
+              top = __hmax2(top, __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&c)));
+          }
           if constexpr (KVT == 2)
             sum = fmaf(f32x2_hsum(bs2), inv_vs, sum);
           else
             sum2 = bs2;
         }
         if constexpr (KVT != 2) sum = f32x2_hsum(sum2);
-        if (moved || !pair_any(pair, (any_bits & kTwo) != 0u)) break;
+        const bool large = KVT == 0 ? (any_bits & kTwo) != 0u
+                                    : __hgt(__hmax(__low2half(top), __high2half(top)), __float2half(1024.f));
+        if (moved || !pair_any(pair, large)) break;
         moved = true;
       }
       l += sum;
