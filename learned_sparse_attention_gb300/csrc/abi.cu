@@ -671,8 +671,8 @@ struct WindowPlan {
 WindowPlan window_plan(const qsa_gqa_cfg* g, const qsa_window_args* a) {
   const int group = g->num_q_heads / g->num_kv_heads;
   const long long n = window_tokens(a);
-  if (static_cast<long long>(a->rows) * group >= 16ll * a->reqs)
-    return {true, window_tile_splits(a->rows, g->num_kv_heads, group, n, sm_count())};
+  if (static_cast<long long>(a->rows) * group >= 24ll * a->reqs)
+    return {true, window_tile_splits(a->rows, a->reqs, g->num_kv_heads, group, n, sm_count())};
   return {false, row_gqa_splits(a->rows, g->num_kv_heads, n, g->kv_dtype, sm_count())};
 }
 

@@ -165,7 +165,7 @@ cudaError_t launch_row_gqa(const RowGqaParams& p, cudaStream_t stream);
 cudaError_t launch_row_merge(const RowGqaParams& p, cudaStream_t stream);
 // Window attention by tiles of 128 (row, head) pairs of one request.
 int window_tile_rows(int group);  // rows of a CTA
-int window_tile_splits(int rows, int hkv, int group, long long max_tokens, int sms);
+int window_tile_splits(int rows, int reqs, int hkv, int group, long long max_tokens, int sms);
 // tmap: the cache as [blocks * Hkv * page, 256] with a box of 128 bytes x
 // p.box rows (128-byte swizzle), read when p.box != 0.
 cudaError_t launch_window_tile(const RowGqaParams& p, const CUtensorMap& tmap, cudaStream_t stream);

@@ -1070,9 +1070,11 @@ cudaError_t launch_kind(const RowGqaParams& p, const CUtensorMap& tmap, const di
 
 int window_tile_rows(int group) { return 2 * (128 / group); }
 
-int window_tile_splits(int rows, int hkv, int group, long long max_tokens, int sms) {
+int window_tile_splits(int rows, int reqs, int hkv, int group, long long max_tokens, int sms) {
   const int per = window_tile_rows(group);
-  const long long ctas = static_cast<long long>((rows + per - 1) / per) * hkv;
+  long long groups = (rows + per - 1) / per;  // at least, and one for each request with rows
+  if (groups < reqs) groups = reqs < rows ? reqs : rows;
+  const long long ctas = groups * hkv;
   if (ctas <= 0) return 1;
   const long long tiles = (max_tokens + 127) / 128 + 1;
   long long s = sms / ctas;
