@@ -12,20 +12,21 @@
 // of the softmax adds p_t / vs_t, so neither scale costs a multiplication of
 // the K or V tile.
 //
-// 8-bit caches are multiplied as they are: the e4m3 codes are the B operand
-// of m16n8k32 MMAs, and q and p are each split into two e4m3 terms, x = hi +
-// lo / 32, whose 8 significant bits are those of a bf16 operand (q, a bf16
-// value, loses nothing).  The terms are the two halves of the MMA's 16 rows:
-// rows 0-7 the hi of up to 8 heads, rows 8-15 their lo.  So no code is ever
-// converted, and V is transposed by ldmatrix alone.
+// e4m3 codes become f16 right before their MMA (exact, two a conversion), q is
+// f16 times a power of two per head (exact but for elements 2^-28 below its
+// largest), p is f16.  (m16n8k32 MMAs on the codes, with q and p as two e4m3
+// terms, are correct too, but this part has none in hardware: 900
+// instructions a slab instead of 400.)
 //
 // Bound: HBM (256 or 512 contiguous bytes of each token and KV head).  One CTA
 // per (row, KV head, split), four warps, each with its own cp.async ring over
 // slabs of 16 (bf16) or 32 tokens; a warp finds its slabs' cache rows itself,
 // two slabs ahead of their copies, so the loop has no block barrier.  Both
-// products have the heads on M and the tokens (S = Q K^T) or dims (O = P V)
-// on N, so a lane's scores are the P fragment it needs next; for m16n8k32 that
-// takes K's rows in the order tau (below).  Splits leave fp32 partials that a
+// products have the heads on M (16: one or two blocks of 8) and the tokens
+// (S = Q K^T) or dims (O = P V) on N, so a lane's scores are the P fragment it
+// needs next.  Of e4m3 rows a lane holds 4 consecutive bytes where bf16 rows
+// give it 2 + 2: dims (K) and tokens (V) are taken in that order, by q's
+// fragments and by K's rows (tau, below).  Splits leave fp32 partials that a
 // second kernel joins in a fixed order.
 #include "kv_scale.cuh"
 #include "qsa_device.cuh"
@@ -40,15 +41,6 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kBadRow = 0xFFFFFFFFu;
 
-// D(16x8 fp32) += A(16x32 e4m3, row) * B(32x8 e4m3, col)
-__device__ __forceinline__ void mma_e4m3_16832(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                               uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
-      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 // Two 16x16 byte matrices, transposed: lanes 0-15 point at the rows of the
 // first, 16-31 of the second.  Lane (g, t) gets, of each, the four bytes of
 // rows 4t .. 4t+3 in column g (r[0], r[2]) and in column g + 8 (r[1], r[3]).
@@ -57,33 +49,11 @@ __device__ __forceinline__ void ldmatrix_b8_trans(uint32_t (&r)[4], const void* 
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(smem_addr(p)));
 }
-__device__ __forceinline__ uint16_t f16x2_to_e4m3x2(uint32_t v) {
-  uint16_t out;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(out) : "r"(v));
-  return out;
-}
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
-  uint32_t out;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(out) : "h"(v));
-  return out;
-}
 // 4-byte asynchronous copy of src_bytes bytes, the rest zero.
 __device__ __forceinline__ void cp_async4(void* dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src),
                "r"(src_bytes)
                : "memory");
-}
-
-// x0, x1 (f16x2, at most 256) as two e4m3 terms, hi + lo / 32.
-__device__ __forceinline__ void split_e4m3x2(uint32_t x, uint16_t& hi, uint16_t& lo) {
-  hi = f16x2_to_e4m3x2(x);
-  const uint32_t back = e4m3x2_to_f16x2(hi);
-  const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&back)),
-                            __float2half2_rn(32.0f));
-  lo = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&r));
-}
-__device__ __forceinline__ uint32_t pack16(uint16_t a, uint16_t b) {
-  return static_cast<uint32_t>(a) | (static_cast<uint32_t>(b) << 16);
 }
 
 // Layout by cache type: KVT 0 bf16, 1 e4m3 with static scales, 2 e4m3 with
@@ -95,10 +65,8 @@ struct RowPlan {
   static constexpr int kRowB = kE4m3 ? 128 : 256;     // bytes of a token's K (or V)
   static constexpr int kSlab = TS * kRowB * 2;        // 8 KB: K rows, then V rows
   static constexpr int kStages = 3;
-  // the margin by which a weight may pass the reference, and where a new
-  // reference puts the largest weight (log2): f16/e4m3 terms up to 2^8
+  // the margin (log2) by which a weight may pass the reference
   static constexpr float kUp = 8.0f;
-  static constexpr float kTop = kE4m3 ? 4.0f : 0.0f;
   static constexpr int kSmem = kWarps * kStages * kSlab;
 };
 
@@ -109,15 +77,13 @@ __device__ __forceinline__ int swz_k(int tok) {
   return KVT == 0 ? tok & 7 : (tok & 1) | ((tok >> 1) & 6);
 }
 
-// HB: blocks of 8 query heads (groups of 16: 2).  bf16 holds both on one M
-// of 16; e4m3 takes an M of 16 (hi and lo) for each.
+// HB: blocks of 8 query heads (groups of 16: 2), the halves of an M of 16.
 template <int KVT, int HB>
-__global__ void __launch_bounds__(kThreads) row_gqa_kernel(const RowGqaParams P) {
+__global__ void __launch_bounds__(kThreads, 2) row_gqa_kernel(const RowGqaParams P) {
   using RP = RowPlan<KVT>;
   constexpr int TS = RP::TS, ST = RP::kStages;
-  constexpr int MB = RP::kE4m3 ? HB : 1;     // MMA row blocks
-  constexpr int NS = RP::kE4m3 ? 1 : HB;     // heads of a lane in each of them
   constexpr int NBK = TS / 8;                // column blocks of S
+  constexpr int NT = TS / 4;                 // tokens of a lane: 4 or 8
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t s_raw[kWarps][ST][KVT == 2 ? 32 : 1];  // scale words as copied
   __shared__ float4 s_scl[kWarps][3][KVT == 2 ? 8 : 1];      // ks, log2 vs, 1 / vs of a slab
@@ -181,66 +147,57 @@ __global__ void __launch_bounds__(kThreads) row_gqa_kernel(const RowGqaParams P)
 #pragma unroll
   for (int i = 0; i <= ST; ++i) tok[i] = fetch_tok(i);
 
-  // ---- Q as A fragments: row g of block mb is head 8 mb + g; rows g + 8 are
-  // heads 8 .. 15 (bf16) or the lo terms of rows g (e4m3)
-  constexpr int KK = RP::kE4m3 ? 4 : 8;
-  uint32_t qa[MB][KK][4];
-  float qs[MB];  // e4m3: what a block's scores are multiplied by
-  if constexpr (RP::kE4m3) {
+  // ---- Q as A fragments, 16 dims each: row g is head g, row g + 8 head 8 + g.
+  // qs: what a head's scores are multiplied by (D^-1/2 log2 e and, e4m3, the
+  // power of two taken out of q and the static K scale; block scales come per
+  // token)
+  uint32_t qa[8][4];
+  float qs[HB];
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
-      const int h = 8 * mb + g;
-      const uint16_t* qh = P.q + (static_cast<long long>(row) * P.hq + kvh * G + min(h, G - 1)) * 128;
-      uint2 v[KK][2];
+  for (int hb = 0; hb < 2; ++hb) {
+    const int h = 8 * hb + g;
+    const bool act = hb < HB && h < G;
+    const uint16_t* qh = P.q + (static_cast<long long>(row) * P.hq + kvh * G + min(h, G - 1)) * 128;
+    if (hb >= HB) {
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) qa[kk][hb] = qa[kk][2 + hb] = 0u;
+    } else if constexpr (RP::kE4m3) {
+      uint2 v[8];
       float peak = 0.f;
       bool odd = false;  // an infinity or a NaN
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk)
+      for (int kk = 0; kk < 8; ++kk) {
+        v[kk] = act ? *reinterpret_cast<const uint2*>(qh + 16 * kk + 4 * t) : make_uint2(0u, 0u);
+        const float x[4] = {bf16_lo(v[kk].x), bf16_hi(v[kk].x), bf16_lo(v[kk].y), bf16_hi(v[kk].y)};
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          v[kk][u] = h < G ? *reinterpret_cast<const uint2*>(qh + 32 * kk + 16 * u + 4 * t) : make_uint2(0u, 0u);
-          const float x[4] = {bf16_lo(v[kk][u].x), bf16_hi(v[kk][u].x), bf16_lo(v[kk][u].y), bf16_hi(v[kk][u].y)};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            odd |= !(fabsf(x[e]) <= 3.39e38f);
-            peak = fmaxf(peak, fabsf(x[e]));
-          }
+        for (int e = 0; e < 4; ++e) {
+          odd |= !(fabsf(x[e]) <= 3.39e38f);
+          peak = fmaxf(peak, fabsf(x[e]));
         }
+      }
 #pragma unroll
       for (int o = 1; o <= 2; o <<= 1) {
         peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, o));
-        odd |= __shfl_xor_sync(0xffffffffu, odd, o);
+        odd |= __shfl_xor_sync(0xffffffffu, static_cast<int>(odd), o) != 0;
       }
-      // a power of two that brings the head's largest |q| into [128, 256)
+      // a power of two that brings the head's largest |q| into [2^14, 2^15)
       // (two factors: 2^e itself may leave fp32)
-      const int e = peak > 0.f ? max(__float_as_int(peak) >> 23, 1) - 127 - 7 : 0;
+      const int e = peak > 0.f ? max(__float_as_int(peak) >> 23, 1) - 127 - 14 : 0;
       const float f0 = exp2i(-(e / 2)), f1 = exp2i(-(e - e / 2));
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk)
+      for (int kk = 0; kk < 8; ++kk) {
+        qa[kk][hb] = pack_f16x2(bf16_lo(v[kk].x) * f0 * f1, bf16_hi(v[kk].x) * f0 * f1);
+        qa[kk][2 + hb] = pack_f16x2(bf16_lo(v[kk].y) * f0 * f1, bf16_hi(v[kk].y) * f0 * f1);
+      }
+      qs[hb < HB ? hb : 0] = odd ? __int_as_float(0x7fffffff)
+                                 : exp2i(e / 2) * (0.08838834764831845f * kLog2e * (KVT == 1 ? P.k_scale : 1.0f)) * exp2i(e - e / 2);
+    } else {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          uint16_t h0, l0, h1, l1;
-          split_e4m3x2(pack_f16x2(bf16_lo(v[kk][u].x) * f0 * f1, bf16_hi(v[kk][u].x) * f0 * f1), h0, l0);
-          split_e4m3x2(pack_f16x2(bf16_lo(v[kk][u].y) * f0 * f1, bf16_hi(v[kk][u].y) * f0 * f1), h1, l1);
-          qa[mb][kk][2 * u] = pack16(h0, h1);
-          qa[mb][kk][2 * u + 1] = pack16(l0, l1);
-        }
-      // D^-1/2 log2 e and the static K scale with it; block scales come per token
-      qs[mb] = odd ? __int_as_float(0x7fffffff)
-                   : exp2i(e / 2) * (0.08838834764831845f * kLog2e * (KVT == 1 ? P.k_scale : 1.0f)) * exp2i(e - e / 2);
-    }
-  } else {
-    qs[0] = 0.08838834764831845f * kLog2e;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int h = 8 * s + g;
-      const uint16_t* qh = P.q + (static_cast<long long>(row) * P.hq + kvh * G + min(h, G - 1)) * 128;
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          qa[0][kk][2 * u + s] =
-              s < HB && h < G ? *reinterpret_cast<const uint32_t*>(qh + 16 * kk + 8 * u + 2 * t) : 0u;
+      for (int kk = 0; kk < 8; ++kk) {
+        qa[kk][hb] = act ? *reinterpret_cast<const uint32_t*>(qh + 16 * kk + 2 * t) : 0u;
+        qa[kk][2 + hb] = act ? *reinterpret_cast<const uint32_t*>(qh + 16 * kk + 8 + 2 * t) : 0u;
+      }
+      qs[hb < HB ? hb : 0] = 0.08838834764831845f * kLog2e;
     }
   }
 
@@ -302,18 +259,15 @@ __global__ void __launch_bounds__(kThreads) row_gqa_kernel(const RowGqaParams P)
   // the slab to copy next, and the one after it
   int tok_n = tok[ST - 1], pg_n = pg[ST - 1], tok_nn = tok[ST];
 
-  float o[MB][16][4];
-  float m[MB][NS], l[MB][NS];
+  float o[16][4];
+  float m[HB], l[HB];
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb) {
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      m[mb][s] = -INFINITY;
-      l[mb][s] = 0.f;
-    }
-#pragma unroll
-    for (int nb = 0; nb < 16; ++nb) o[mb][nb][0] = o[mb][nb][1] = o[mb][nb][2] = o[mb][nb][3] = 0.f;
+  for (int hb = 0; hb < HB; ++hb) {
+    m[hb] = -INFINITY;
+    l[hb] = 0.f;
   }
+#pragma unroll
+  for (int nb = 0; nb < 16; ++nb) o[nb][0] = o[nb][1] = o[nb][2] = o[nb][3] = 0.f;
 
   int stage = 0;
   for (int it = 0; it < cnt; ++it) {
@@ -331,7 +285,7 @@ __global__ void __launch_bounds__(kThreads) row_gqa_kernel(const RowGqaParams P)
     const uint8_t* sK = ring + stage * RP::kSlab;
     const uint8_t* sV = sK + TS * RP::kRowB;
     const uint32_t vm = vmask[0];
-    float ks[2 * NBK], lv[2 * NBK], iv[2 * NBK];  // of the lane's tokens (block scales)
+    float ks[NT], lv[NT], iv[NT];  // of the lane's tokens (block scales)
     if constexpr (KVT == 2) {
       const uint32_t w = s_raw[warp][stage][lane] >> ((odd_pair[0] >> lane & 1u) * 16);
       const int ek = scale_exp(w & 0xFFu), ev = scale_exp((w >> 8) & 0xFFu);
@@ -351,121 +305,99 @@ __global__ void __launch_bounds__(kThreads) row_gqa_kernel(const RowGqaParams P)
     // ---- S = Q K^T.  Column c of block nb is token tau(nb, c):
     //   bf16   8 nb + c;   e4m3  16 (nb / 2) + 4 (c / 2) + 2 (nb % 2) + c % 2
     // so that a lane's columns 2t, 2t + 1 are the tokens of its P fragment.
-    float s[MB][NBK][4];
+    float s[NBK][4];
 #pragma unroll
     for (int nb = 0; nb < NBK; ++nb) {
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb) s[mb][nb][0] = s[mb][nb][1] = s[mb][nb][2] = s[mb][nb][3] = 0.f;
+      s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
       const int c = lane & 7;
       const int tk = RP::kE4m3 ? 16 * (nb >> 1) + 4 * (c >> 1) + 2 * (nb & 1) + (c & 1) : 8 * nb + c;
 #pragma unroll
-      for (int j = 0; j < KK / 2; ++j) {  // four 16-byte chunks: two MMA steps
+      for (int j = 0; j < RP::kRowB / 64; ++j) {  // four 16-byte chunks
         uint32_t b[4];
         ldmatrix_x4(b, sK + tk * RP::kRowB + (((4 * j + (lane >> 3)) ^ swz_k<KVT>(tk)) << 4));
+        if constexpr (RP::kE4m3) {
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-          if constexpr (RP::kE4m3) {
-            mma_e4m3_16832(s[mb][nb], qa[mb][2 * j], b[0], b[1]);
-            mma_e4m3_16832(s[mb][nb], qa[mb][2 * j + 1], b[2], b[3]);
-          } else {
-            mma_bf16_16816(s[mb][nb], qa[mb][2 * j], b[0], b[1]);
-            mma_bf16_16816(s[mb][nb], qa[mb][2 * j + 1], b[2], b[3]);
+          for (int u = 0; u < 4; ++u) {
+            uint32_t f0, f1;
+            e4m3x4_to_f16x2x2(b[u], f0, f1);
+            mma_f16_16816(s[nb], qa[4 * j + u], f0, f1);
           }
+        } else {
+          mma_bf16_16816(s[nb], qa[2 * j], b[0], b[1]);
+          mma_bf16_16816(s[nb], qa[2 * j + 1], b[2], b[3]);
         }
       }
     }
 
     // ---- weights.  Entry e of block nb: the lane's token number 2 nb + e
-    uint32_t pa[MB][4];
+    uint32_t pa[TS / 16][4];
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
+    for (int hb = 0; hb < HB; ++hb) {
+      float z[NT];  // exponents (log2) without the reference
 #pragma unroll
-      for (int sI = 0; sI < NS; ++sI) {
-        float z[2 * NBK];  // exponents (log2) without the reference
+      for (int i = 0; i < NT; ++i) {
+        z[i] = s[i >> 1][2 * hb + (i & 1)] * qs[hb];
+        if constexpr (KVT == 2) z[i] = fmaf(z[i], ks[i], lv[i]);
+      }
+      constexpr uint32_t kFull = TS == 32 ? 0xffffffffu : 0xffffu;
+      if (vm != kFull) {
 #pragma unroll
-        for (int i = 0; i < 2 * NBK; ++i) {
-          const int nb = i >> 1, e = i & 1;
-          if constexpr (RP::kE4m3) {
-            z[i] = fmaf(s[mb][nb][2 + e], 0.03125f, s[mb][nb][e]) * qs[mb];
-            if constexpr (KVT == 2) z[i] = fmaf(z[i], ks[i], lv[i]);
-          } else {
-            z[i] = s[0][nb][2 * sI + e] * qs[0];
-          }
+        for (int i = 0; i < NT; ++i) {
+          const int tk = RP::kE4m3 ? 16 * (i >> 2) + 4 * t + (i & 3) : 8 * (i >> 1) + 2 * t + (i & 1);
+          if (!((vm >> tk) & 1u)) z[i] = -INFINITY;
         }
-        constexpr uint32_t kFull = TS == 32 ? 0xffffffffu : 0xffffu;
-        if (vm != kFull) {
+      }
+      float mx = z[0];
 #pragma unroll
-          for (int i = 0; i < 2 * NBK; ++i) {
-            const int tk = RP::kE4m3 ? 16 * (i >> 2) + 4 * t + (i & 3) : 8 * (i >> 1) + 2 * t + (i & 1);
-            if (!((vm >> tk) & 1u)) z[i] = -INFINITY;
-          }
+      for (int i = 1; i < NT; ++i) mx = fmaxf(mx, z[i]);
+      float& mr = m[hb];
+      // (no reference yet: any score passes it)
+      if (__any_sync(0xffffffffu, mx > mr + RP::kUp)) {
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(mr, mx);
+        const float al = ex2_ftz(mr - (mn == -INFINITY ? 0.f : mn));
+        l[hb] *= al;
+#pragma unroll
+        for (int nb = 0; nb < 16; ++nb) {
+          o[nb][2 * hb] *= al;
+          o[nb][2 * hb + 1] *= al;
         }
-        float mx = z[0];
+        mr = mn;
+      }
+      const float ref = mr == -INFINITY ? 0.f : mr;
+      float sum = 0.f;
 #pragma unroll
-        for (int i = 1; i < 2 * NBK; ++i) mx = fmaxf(mx, z[i]);
-        float& mr = m[mb][sI];
-        // (no reference yet: any score passes it)
-        if (__any_sync(0xffffffffu, mx > mr + RP::kUp)) {
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(mr, mx - RP::kTop);
-          const float al = ex2_ftz(mr - (mn == -INFINITY ? 0.f : mn));
-          l[mb][sI] *= al;
+      for (int i = 0; i < NT; ++i) {
+        z[i] = ex2_ftz(z[i] - ref);
+        sum = KVT == 2 ? fmaf(z[i], iv[i], sum) : sum + z[i];
+      }
+      l[hb] += sum;
 #pragma unroll
-          for (int nb = 0; nb < 16; ++nb) {
-            o[mb][nb][2 * sI] *= al;
-            o[mb][nb][2 * sI + 1] *= al;
-            if constexpr (RP::kE4m3) {
-              o[mb][nb][2] *= al;
-              o[mb][nb][3] *= al;
-            }
-          }
-          mr = mn;
-        }
-        const float ref = mr == -INFINITY ? 0.f : mr;
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 2 * NBK; ++i) {
-          z[i] = ex2_ftz(z[i] - ref);
-          sum = KVT == 2 ? fmaf(z[i], iv[i], sum) : sum + z[i];
-        }
-        l[mb][sI] += sum;
-        if constexpr (RP::kE4m3) {
-          uint16_t hi[NBK], lw[NBK];
-#pragma unroll
-          for (int nb = 0; nb < NBK; ++nb) split_e4m3x2(pack_f16x2(z[2 * nb], z[2 * nb + 1]), hi[nb], lw[nb]);
-          pa[mb][0] = pack16(hi[0], hi[1]);
-          pa[mb][1] = pack16(lw[0], lw[1]);
-          pa[mb][2] = pack16(hi[NBK - 2], hi[NBK - 1]);
-          pa[mb][3] = pack16(lw[NBK - 2], lw[NBK - 1]);
-        } else {
-          pa[0][sI] = pack_bf16x2(z[0], z[1]);
-          pa[0][2 + sI] = pack_bf16x2(z[2], z[3]);
-          if constexpr (NS == 1) pa[0][1] = pa[0][3] = 0u;
-        }
+      for (int u = 0; u < TS / 16; ++u) {
+        pa[u][hb] = RP::kE4m3 ? pack_f16x2(z[4 * u], z[4 * u + 1]) : pack_bf16x2(z[4 * u], z[4 * u + 1]);
+        pa[u][2 + hb] = RP::kE4m3 ? pack_f16x2(z[4 * u + 2], z[4 * u + 3]) : pack_bf16x2(z[4 * u + 2], z[4 * u + 3]);
+        if constexpr (HB == 1) pa[u][1] = pa[u][3] = 0u;
       }
     }
 
     // ---- O += P V
-    if constexpr (RP::kE4m3) {
 #pragma unroll
-      for (int d = 0; d < 8; ++d) {  // 16 dims
-        uint32_t b[4];
+    for (int d = 0; d < 8; ++d) {  // 16 dims
+      uint32_t b[4];
+      if constexpr (RP::kE4m3) {
         ldmatrix_b8_trans(b, sV + lane * 128 + ((d ^ (lane & 7)) << 4));
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-          mma_e4m3_16832(o[mb][2 * d], pa[mb], b[0], b[2]);
-          mma_e4m3_16832(o[mb][2 * d + 1], pa[mb], b[1], b[3]);
+        for (int u = 0; u < 4; ++u) {
+          uint32_t f0, f1;
+          e4m3x4_to_f16x2x2(b[u], f0, f1);
+          mma_f16_16816(o[2 * d + (u & 1)], pa[u >> 1], f0, f1);
         }
-      }
-    } else {
-#pragma unroll
-      for (int d = 0; d < 8; ++d) {
-        uint32_t b[4];
+      } else {
         const int tk = lane & 15;
         ldmatrix_x4_trans(b, sV + tk * 256 + (((2 * d + (lane >> 4)) ^ (tk & 7)) << 4));
-        mma_bf16_16816(o[0][2 * d], pa[0], b[0], b[1]);
-        mma_bf16_16816(o[0][2 * d + 1], pa[0], b[2], b[3]);
+        mma_bf16_16816(o[2 * d], pa[0], b[0], b[1]);
+        mma_bf16_16816(o[2 * d + 1], pa[0], b[2], b[3]);
       }
     }
 #pragma unroll
@@ -487,23 +419,17 @@ __global__ void __launch_bounds__(kThreads) row_gqa_kernel(const RowGqaParams P)
   float* co = cl + kWarps * HN;
 #pragma unroll
   for (int hb = 0; hb < HB; ++hb) {
-    constexpr bool kE = RP::kE4m3;
-    const int mb = kE ? hb : 0, sI = kE ? 0 : hb;
-    float sum = l[mb][sI];
+    float sum = l[hb];
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
     const int at = warp * HN + 8 * hb + g;
     if (t == 0) {
-      cm[at] = m[mb][sI];
+      cm[at] = m[hb];
       cl[at] = sum;
     }
 #pragma unroll
-    for (int nb = 0; nb < 16; ++nb) {
-      float2 v;
-      v.x = kE ? fmaf(o[mb][nb][2], 0.03125f, o[mb][nb][0]) : o[mb][nb][2 * sI];
-      v.y = kE ? fmaf(o[mb][nb][3], 0.03125f, o[mb][nb][1]) : o[mb][nb][2 * sI + 1];
-      *reinterpret_cast<float2*>(co + at * LD + 8 * nb + 2 * t) = v;
-    }
+    for (int nb = 0; nb < 16; ++nb)
+      *reinterpret_cast<float2*>(co + at * LD + 8 * nb + 2 * t) = make_float2(o[nb][2 * hb], o[nb][2 * hb + 1]);
   }
   __syncthreads();
   const int d0 = (threadIdx.x & 15) * 8;
@@ -596,11 +522,15 @@ cudaError_t launch_kind(const RowGqaParams& p, cudaStream_t stream) {
 
 }  // namespace
 
+// As many splits as keep the CTAs in one wave at two per SM (shared memory):
+// a second wave, or a row cut finer than that, costs more than it evens out
+// (64 rows x 4 KV heads of 4100 tokens, e4m3: 1 split 50 us, 2 splits 60 us;
+// 8 rows x 8 of 4103: 4 splits 27 us, 5 splits 30 us).
 int row_gqa_splits(int rows, int hkv, long long max_tokens, int kv_dtype, int sms) {
   const long long base = static_cast<long long>(rows) * hkv;
   if (base <= 0) return 1;
   const int least = (kv_dtype == QSA_DTYPE_BF16 ? 16 : 32) * kWarps * 2;  // two slabs a warp
-  long long s = 4ll * sms / base;
+  long long s = 2ll * sms / base;
   const long long most = (max_tokens + least - 1) / least;
   if (s > most) s = most;
   if (s > 128) s = 128;
