@@ -19,7 +19,7 @@
 // Bound: memory.  A row is read once and written once; the arithmetic is an
 // eighth of an instruction a byte.  Layout: half-warps hold a 128-dim head
 // (16 bytes a lane).  With block scales a CTA holds a run's keys and values
-// of one KV head in registers between the maximum and the rounding (B / 8
+// of one KV head in registers between the maximum and the rounding (2, 4 or 8
 // tokens a half-warp), so they are read once.
 #include "kv_scale.cuh"
 #include "qsa_device.cuh"
@@ -32,6 +32,7 @@ namespace {
 
 constexpr int kD = 128;
 constexpr int kThreads = 128;
+constexpr int kHalves = kThreads / 16;  // half-warps of a CTA
 
 __device__ __forceinline__ RopeParams rope_of(const AppendParams& P) {
   return RopeParams{P.cos_sin, P.max_pos, P.mrope, P.sec_h, P.sec_w, P.err};
@@ -69,29 +70,54 @@ __device__ __forceinline__ void load_gain(const uint16_t* w, int lane16, float (
   for (int e = 0; e < 8; ++e) g[e] += 1.0f;
 }
 
-// q = RoPE(GemmaRMSNorm(q)) and the gate of one row; the 8 half-warps take
-// its heads in turn.
-__device__ __forceinline__ void query_row(const AppendParams& P, int row, const float (&g)[8]) {
+// q = RoPE(GemmaRMSNorm(q)) and the gate of rows row0, row0 + step, ...: each
+// half-warp takes four heads at a time, and the next four's loads (and the
+// next row's position) are on the way while these are worked on.
+__device__ __forceinline__ void query_rows(const AppendParams& P, int row0, int step) {
+  constexpr int U = 2;
   const int hw = threadIdx.x >> 4, lane16 = threadIdx.x & 15;
-  const uint16_t* x = P.qkv + static_cast<long long>(row) * (2 * P.hq + 2 * P.hkv) * kD;
-  int64_t pos[3];
-  load_pos(P, row, pos);
-  float c[8], s[8];
-  rope_coeffs(rope_of(P), lane16, pos, c, s);
-  for (int base = 0; base < P.hq; base += 8) {  // (the norm's shuffles span the warp)
-    const int h = base + hw;
-    const bool act = h < P.hq;
-    float xq[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    uint4 gv = make_uint4(0u, 0u, 0u, 0u);
-    if (act) {
-      load8_bf16(x + (2 * h) * kD + 8 * lane16, xq);
-      gv = *reinterpret_cast<const uint4*>(x + (2 * h + 1) * kD + 8 * lane16);
+  float g[8];
+  load_gain(P.q_norm_w, lane16, g);
+  auto load = [&](int row, int base, uint4 (&q)[U], uint4 (&gate)[U]) {
+    const uint16_t* x = P.qkv + static_cast<long long>(row) * (2 * P.hq + 2 * P.hkv) * kD + 8 * lane16;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = base + hw + kHalves * u;
+      q[u] = gate[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < P.rows && h < P.hq) {
+        q[u] = *reinterpret_cast<const uint4*>(x + (2 * h) * kD);
+        gate[u] = *reinterpret_cast<const uint4*>(x + (2 * h + 1) * kD);
+      }
     }
-    norm_rope(xq, g, P.eps, lane16, c, s);
-    if (act) {
-      const long long o = (static_cast<long long>(row) * P.hq + h) * kD + 8 * lane16;
-      *reinterpret_cast<uint4*>(P.q_out + o) = pack8_bf16(xq);
-      *reinterpret_cast<uint4*>(P.gate_out + o) = gv;
+  };
+  uint4 q[U], gate[U];
+  load(row0, 0, q, gate);
+  int64_t pos[3];
+  load_pos(P, row0, pos);
+  for (int row = row0; row < P.rows; row += step) {
+    float c[8], s[8];
+    rope_coeffs(rope_of(P), lane16, pos, c, s);
+    if (row + step < P.rows) load_pos(P, row + step, pos);
+    for (int base = 0; base < P.hq; base += kHalves * U) {  // (the norm's shuffles span the warp)
+      uint4 nq[U], ngate[U];
+      const bool last = base + kHalves * U >= P.hq;
+      load(last ? row + step : row, last ? 0 : base + kHalves * U, nq, ngate);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = base + hw + kHalves * u;
+        if (base + kHalves * u < P.hq) {  // (the same for the whole CTA)
+          float f[8];
+          unpack8(q[u], f);
+          norm_rope(f, g, P.eps, lane16, c, s);
+          if (h < P.hq) {
+            const long long o = (static_cast<long long>(row) * P.hq + h) * kD + 8 * lane16;
+            *reinterpret_cast<uint4*>(P.q_out + o) = pack8_bf16(f);
+            *reinterpret_cast<uint4*>(P.gate_out + o) = gate[u];
+          }
+        }
+        q[u] = nq[u];
+        gate[u] = ngate[u];
+      }
     }
   }
 }
@@ -112,7 +138,7 @@ __device__ __forceinline__ void plain_kv_row(const AppendParams& P, int row) {
   float c[8], s[8], g[8];
   rope_coeffs(rope_of(P), lane16, pos, c, s);
   load_gain(P.k_norm_w, lane16, g);
-  for (int base = 0; base < P.hkv; base += 8) {
+  for (int base = 0; base < P.hkv; base += kHalves) {
     const int h = base + hw;
     const bool act = h < P.hkv;
     float xk[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -138,25 +164,26 @@ __device__ __forceinline__ void plain_kv_row(const AppendParams& P, int row) {
   }
 }
 
-// Whether row i + 1 goes on with row i's run.
+// Whether row i + 1 goes on with row i's run (blocks of kHalves * NT tokens).
+template <int NT>
 __device__ __forceinline__ bool goes_on(const AppendParams& P, int i) {
   if (i < 0 || i + 1 >= P.rows) return false;
   const long long a = P.slots[i], b = P.slots[i + 1];
-  return a >= 0 && b > a && a / P.scale_block == b / P.scale_block;
+  return a >= 0 && b > a && ((a ^ b) & ~(static_cast<long long>(kHalves) * NT - 1)) == 0;
 }
 
 // The run that begins at row i, one KV head, into a cache with block scales.
-// NT: tokens of a block per half-warp (B / 8).
+// NT: tokens of a block per half-warp.
 template <int NT>
 __device__ __forceinline__ void scaled_run(const AppendParams& P, int i, int h, const float (&g)[8]) {
-  __shared__ float s_peak[8][2];
+  __shared__ float s_peak[kHalves][2];
   const int hw = threadIdx.x >> 4, lane16 = threadIdx.x & 15, lane = threadIdx.x & 31;
-  constexpr int B = 8 * NT;
+  constexpr int B = kHalves * NT;
   const long long slot = P.slots[i];
   const long long blk = slot / P.page;
   // a row that repeats its predecessor's place or steps back inside one
   // block would race with that run
-  const bool back = i > 0 && P.slots[i - 1] >= slot && P.slots[i - 1] / B == slot / B;
+  const bool back = i > 0 && P.slots[i - 1] >= slot && ((P.slots[i - 1] ^ slot) & ~(B - 1ll)) == 0;
   if (blk >= P.num_blocks || back) {
     if (h == 0 && threadIdx.x == 0) flag_error(P.err);
     return;
@@ -165,7 +192,7 @@ __device__ __forceinline__ void scaled_run(const AppendParams& P, int i, int h, 
   int m = 0;
 #pragma unroll
   for (int w = 0; w < (B + 31) / 32; ++w) {
-    const unsigned on = __ballot_sync(0xffffffffu, goes_on(P, i + 32 * w + lane));
+    const unsigned on = __ballot_sync(0xffffffffu, goes_on<NT>(P, i + 32 * w + lane));
     if (m == 32 * w) m += on == 0xffffffffu ? 32 : __ffs(~on) - 1;
   }
   m = min(m + 1, B);
@@ -175,21 +202,26 @@ __device__ __forceinline__ void scaled_run(const AppendParams& P, int i, int h, 
   uint8_t* kv = static_cast<uint8_t*>(P.kv);
   const int ek_old = scale_exp(sc[0]), ev_old = scale_exp(sc[1]);
 
+  // the run's keys, values and positions, all asked for before any is used
+  uint4 kr[NT], v[NT];
+  int64_t pos[NT][3];
+#pragma unroll
+  for (int u = 0; u < NT; ++u) {
+    if (kHalves * u >= m) continue;  // (the same for the whole CTA)
+    const int row = i + min(hw + kHalves * u, m - 1);
+    const uint16_t* x = P.qkv + (static_cast<long long>(row) * (2 * P.hq + 2 * P.hkv) + 2 * P.hq + h) * kD + 8 * lane16;
+    kr[u] = *reinterpret_cast<const uint4*>(x);
+    v[u] = *reinterpret_cast<const uint4*>(x + P.hkv * kD);
+    load_pos(P, row, pos[u]);
+  }
   float k[NT][8];
-  uint4 v[NT];
   float pk = 0.f, pv = 0.f;
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
-    const int j = hw + 8 * u;
-    if (8 * u >= m) continue;  // (the same for the whole CTA)
-    const int row = i + min(j, m - 1);
-    const uint16_t* x = P.qkv + (static_cast<long long>(row) * (2 * P.hq + 2 * P.hkv) + 2 * P.hq + h) * kD;
-    int64_t pos[3];
-    load_pos(P, row, pos);
-    load8_bf16(x + 8 * lane16, k[u]);
-    v[u] = *reinterpret_cast<const uint4*>(x + P.hkv * kD + 8 * lane16);
+    if (kHalves * u >= m) continue;
     float c[8], s[8], xv[8];
-    rope_coeffs(rope_of(P), lane16, pos, c, s);
+    rope_coeffs(rope_of(P), lane16, pos[u], c, s);
+    unpack8(kr[u], k[u]);
     norm_rope(k[u], g, P.eps, lane16, c, s);
     unpack8(v[u], xv);
 #pragma unroll
@@ -210,7 +242,7 @@ __device__ __forceinline__ void scaled_run(const AppendParams& P, int i, int h, 
   }
   __syncthreads();  // (also: every thread has read the old scales)
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
+  for (int w = 0; w < kHalves; ++w) {
     pk = fmaxf(pk, s_peak[w][0]);
     pv = fmaxf(pv, s_peak[w][1]);
   }
@@ -233,7 +265,7 @@ __device__ __forceinline__ void scaled_run(const AppendParams& P, int i, int h, 
   const float sk = exp2i(-ek), sv = exp2i(-ev);
 #pragma unroll
   for (int u = 0; u < NT; ++u) {
-    const int j = hw + 8 * u;
+    const int j = hw + kHalves * u;
     if (j >= m) continue;
     // (ascending slots inside the block, not necessarily adjacent)
     const long long r = row0 + (P.slots[i + j] - slot);
@@ -244,14 +276,23 @@ __device__ __forceinline__ void scaled_run(const AppendParams& P, int i, int h, 
   }
 }
 
+// Queries alone, row by row.  Launched to run beside the K/V kernel, which it
+// needs nothing of; CTA 0 waits for that one's end, so that this kernel's end
+// is both's.
+__global__ void __launch_bounds__(kThreads, 5) query_kernel(const AppendParams P) {
+  query_rows(P, blockIdx.x, P.q_ctas);
+  if (blockIdx.x == 0) griddep_wait();
+}
+
 // CTAs [0, kv_ctas) write K and V: with block scales CTA (c, h) the runs of
 // KV head h that begin in rows [c * chunk, (c + 1) * chunk), otherwise CTA c
-// those rows.  The others prepare queries, row by row.
-// NT: B / 8 with block scales, 0 without.
+// those rows.  The others prepare queries, a row each.
+// NT: B / kHalves with block scales, 0 without.
 template <int NT>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams P) {
   const int lane16 = threadIdx.x & 15;
   int cta = blockIdx.x;
+  griddep_launch_dependents();
   if (cta < P.kv_ctas) {
     const int h = NT > 0 ? cta % P.hkv : 0;
     const int i0 = (NT > 0 ? cta / P.hkv : cta) * P.chunk;
@@ -259,34 +300,50 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams P) 
     if constexpr (NT > 0) {
       float g[8];
       load_gain(P.k_norm_w, lane16, g);
-      for (int i = i0; i < i1; ++i)
-        if (P.slots[i] >= 0 && !goes_on(P, i - 1)) scaled_run<NT>(P, i, h, g);
+      for (int b = i0; b < i1; b += 32) {  // 32 rows at a time: where runs begin
+        const int i = b + (threadIdx.x & 31);
+        unsigned first = __ballot_sync(0xffffffffu, i < i1 && P.slots[i] >= 0 && !goes_on<NT>(P, i - 1));
+        for (; first != 0u; first &= first - 1u) scaled_run<NT>(P, b + __ffs(first) - 1, h, g);
+      }
     } else {
       for (int i = i0; i < i1; ++i) plain_kv_row(P, i);
     }
     return;
   }
-  cta -= P.kv_ctas;
-  float g[8];
-  load_gain(P.q_norm_w, lane16, g);
-  for (int row = cta; row < P.rows; row += P.q_ctas) query_row(P, row, g);
+  query_rows(P, cta - P.kv_ctas, P.rows);
+}
+
+template <int NT>
+cudaError_t launch_nt(AppendParams p, cudaStream_t stream) {
+  // From 1024 rows on K and V have a launch of their own, a CTA for each block
+  // of rows and KV head, and the queries another of CTAs that run through many
+  // rows: the registers of the first kind would keep the second from having
+  // its loads in flight, and a CTA for each of 16 384 rows and heads takes
+  // longer to start than to run.  Below, where a launch weighs more, one
+  // launch of a CTA per row (and KV head).
+  const bool many = p.rows >= 1024;
+  p.chunk = NT > 0 && many ? kHalves * NT : 1;
+  const int chunks = (p.rows + p.chunk - 1) / p.chunk;
+  p.kv_ctas = NT > 0 ? chunks * p.hkv : chunks;
+  p.q_ctas = p.q_out == nullptr ? 0 : p.rows;
+  if (!many)
+    return launch_kernel(append_kernel<NT>, dim3(p.kv_ctas + p.q_ctas), dim3(kThreads), 0, stream, false, p);
+  const cudaError_t e = launch_kernel(append_kernel<NT>, dim3(p.kv_ctas), dim3(kThreads), 0, stream, false, p);
+  if (e != cudaSuccess || p.q_ctas == 0) return e;
+  const int most = sm_count() * 5;
+  if (p.q_ctas > most) p.q_ctas = most;
+  return launch_kernel(query_kernel, dim3(p.q_ctas), dim3(kThreads), 0, stream, true, p);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(AppendParams p, cudaStream_t stream) {
   if (p.rows == 0) return cudaSuccess;
-  const bool scaled = p.kv_dtype == QSA_DTYPE_E4M3_BLOCK;
-  p.chunk = scaled && p.rows >= 1024 ? p.scale_block : 1;
-  const int chunks = (p.rows + p.chunk - 1) / p.chunk;
-  p.kv_ctas = scaled ? chunks * p.hkv : chunks;
-  p.q_ctas = p.q_out != nullptr ? p.rows : 0;
-  const dim3 grid(p.kv_ctas + p.q_ctas);
-  switch (scaled ? p.scale_block : 0) {
-    case 0: return launch_kernel(append_kernel<0>, grid, dim3(kThreads), 0, stream, false, p);
-    case 16: return launch_kernel(append_kernel<2>, grid, dim3(kThreads), 0, stream, false, p);
-    case 32: return launch_kernel(append_kernel<4>, grid, dim3(kThreads), 0, stream, false, p);
-    case 64: return launch_kernel(append_kernel<8>, grid, dim3(kThreads), 0, stream, false, p);
+  switch (p.kv_dtype == QSA_DTYPE_E4M3_BLOCK ? p.scale_block : 0) {
+    case 0: return launch_nt<0>(p, stream);
+    case 16: return launch_nt<2>(p, stream);
+    case 32: return launch_nt<4>(p, stream);
+    case 64: return launch_nt<8>(p, stream);
     default: return cudaErrorInvalidValue;
   }
 }
