@@ -71,7 +71,7 @@ __device__ __forceinline__ void load_gain(const uint16_t* w, int lane16, float (
 }
 
 // q = RoPE(GemmaRMSNorm(q)) and the gate of rows row0, row0 + step, ...: each
-// half-warp takes four heads at a time, and the next four's loads (and the
+// half-warp takes two heads at a time, and the next two's loads (and the
 // next row's position) are on the way while these are worked on.
 __device__ __forceinline__ void query_rows(const AppendParams& P, int row0, int step) {
   constexpr int U = 2;

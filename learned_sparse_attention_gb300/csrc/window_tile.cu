@@ -463,29 +463,25 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         // V of tile j as it has landed: zeroes for keys that no row sees or
         // whose page is none (rows: the tile's); of keys that some rows see
         // and others do not, the elements that are not finite become zeros
-        // and the key is remembered
+        // and the key is remembered.  A half-warp takes a key; the ranges of
+        // both kinds are few and short, and found once (these two warps get
+        // few of their schedulers' slots).
         auto clean = [&](int j, uint32_t r, uint8_t* tile) {
           const int slot = open_poison(j), kb = T.first_key(j);
-          const unsigned there = __ballot_sync(0xffffffffu, r < kNoPage);
-#pragma unroll 1
-          for (int g = 0; g < 128; g += 16) {
-            const bool page = (there >> (g >> 4)) & 1u;
-            if (page && all_seen(kb + g, kb + g + 15)) continue;
-            const bool none = !page || none_seen(kb + g, kb + g + 15);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int key = g + 4 * i + (lt >> 4);
-              uint4* at = reinterpret_cast<uint4*>(tile + tile_byte(key, lt & 15));
-              if (none || !seen(kb + key)) {
-                *at = make_uint4(0u, 0u, 0u, 0u);
-                continue;
-              }
+          const int c = lt & 15, k0 = lt >> 4;
+          auto zero = [&](int from, int to) {
+            for (int key = from + k0; key < to; key += 4)
+              *reinterpret_cast<uint4*>(tile + tile_byte(key, c)) = make_uint4(0u, 0u, 0u, 0u);
+          };
+          auto check = [&](int from, int to) {
+            for (int key = from + k0; key < to; key += 4) {
+              uint4* at = reinterpret_cast<uint4*>(tile + tile_byte(key, c));
               const uint4 v = *at;
               uint32_t w[4] = {v.x, v.y, v.z, v.w}, odd = 0u;
               // an exponent of all ones carries into the sign's place
 #pragma unroll
               for (int e = 0; e < 4; ++e) odd |= ((w[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-              if (odd == 0u || all_seen(kb + key, kb + key)) continue;
+              if (odd == 0u) continue;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
@@ -494,6 +490,21 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
               remember(slot, key);
               *at = make_uint4(w[0], w[1], w[2], w[3]);
             }
+          };
+          // within the tile: the sinks end at s1; the windows begin at a0, all
+          // of them have begun at a1, the first ends at b0, all at b1
+          auto in = [&](int key) { return min(max(key - kb, 0), 128); };
+          const int s1 = in(P.sinks), a0 = max(in(wlo), s1), a1 = max(in(neg ? INT_MAX : wlo_all), s1);
+          const int b0 = neg ? 0 : in(pmin + 1), b1 = in(pmax + 1);
+          zero(s1, min(a0, b1));
+          zero(b1, 128);
+          check(min(a0, b1), min(max(a1, b0), b1));
+          if (b0 < a0) check(b0, min(s1, b1));  // (sinks that lie in the rows' own future)
+          if (a1 < b0) check(b0, b1);
+          if (!all_ok(r != kNoPage)) {  // blocks of 16 keys on no page
+            __syncwarp();
+            for (int g = 0; g < 8; ++g)
+              if (__shfl_sync(0xffffffffu, r, g) == kNoPage) zero(16 * g, 16 * g + 16);
           }
         };
         // Small pages: K and V by cp.async.  A tile's K is announced once its V

@@ -9,6 +9,7 @@ raise instead of falling back to anything else.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -366,10 +367,36 @@ def _scales_fit(gcfg, scales):
 
 def _same_device(*tensors):
     """The device all tensors are on (None ones left out)."""
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
-    return devs.pop()
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    if dev is None:
+        raise ValueError("no tensors")
+    return dev
+
+
+def _on(device):
+    """Makes the tensors' device current for a call; nothing to do where it is."""
+    if device.type != "cuda" or device.index == torch._C._cuda_getDevice():
+        return _HERE
+    return torch.cuda.device(device)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _raw_stream(device, stream=None):
+    """The given stream's handle, or that of the device's current stream
+    (without the Stream object that torch.cuda.current_stream() makes: a few
+    microseconds, as much as the small calls take)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def kv_append(cfg, gcfg, m: QsaMainPrep, positions, cos_sin, scales: QsaKvScales | None = None,
@@ -377,11 +404,12 @@ def kv_append(cfg, gcfg, m: QsaMainPrep, positions, cos_sin, scales: QsaKvScales
     """Keys and values into the paged cache, normalised and rotated on the way,
     with q and gate beside them where `m` has them (qsa_kv_append)."""
     _scales_fit(gcfg, scales)
-    with torch.cuda.device(_same_device(positions, cos_sin, m._tensors["kv"])):
+    dev = _same_device(positions, cos_sin, m._tensors["kv"])
+    with _on(dev):
         st = load().qsa_kv_append(
             ctypes.byref(cfg), ctypes.byref(gcfg), ctypes.byref(m),
             None if scales is None else ctypes.byref(scales), _ptr(positions, torch.int64),
-            _ptr(cos_sin, torch.float32), positions.shape[0], _stream(stream))
+            _ptr(cos_sin, torch.float32), positions.shape[0], _raw_stream(dev, stream))
     _check("qsa_kv_append", st)
 
 
@@ -389,14 +417,15 @@ def sparse_gqa_scaled(gcfg, scales: QsaKvScales, q, kv, block_table, packed, tok
                       out, ws, stream=None):
     """Stage 4 over a cache with block scales (qsa_sparse_gqa_scaled)."""
     _scales_fit(gcfg, scales)
-    with torch.cuda.device(_same_device(q, kv, block_table, packed, token_to_req, gate, out, ws)):
+    dev = _same_device(q, kv, block_table, packed, token_to_req, gate, out, ws)
+    with _on(dev):
         st = load().qsa_sparse_gqa_scaled(
             ctypes.byref(gcfg), ctypes.byref(scales), _ptr(q, torch.bfloat16),
             _ptr(kv, torch.uint8), _ptr(block_table, torch.int32), block_table.shape[1],
             _ptr(packed, torch.int32), packed.shape[1], _ptr(token_to_req, torch.int32),
             _ptr(gate, torch.bfloat16), _ptr(out, torch.bfloat16), q.shape[0],
             block_table.shape[0], _ptr(ws, torch.uint8), 0 if ws is None else ws.numel(),
-            _stream(stream))
+            _raw_stream(dev, stream))
     _check("qsa_sparse_gqa_scaled", st)
 
 
@@ -439,9 +468,10 @@ def window_gqa(gcfg, args: QsaWindowArgs, ws=None, stream=None):
     """Attention over the last `window` tokens and the first `sinks`
     (qsa_window_gqa); ws: uint8, window_workspace_bytes() long."""
     _scales_fit(gcfg, args._scales)
-    with torch.cuda.device(args._device):
+    with _on(args._device):
         st = load().qsa_window_gqa(ctypes.byref(gcfg), ctypes.byref(args), _ptr(ws, torch.uint8),
-                                   0 if ws is None else ws.numel(), _stream(stream))
+                                   0 if ws is None else ws.numel(),
+                                   _raw_stream(args._device, stream))
     _check("qsa_window_gqa", st)
 
 
