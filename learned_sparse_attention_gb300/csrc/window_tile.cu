@@ -463,18 +463,19 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         // V of tile j as it has landed: zeroes for keys that no row sees or
         // whose page is none (rows: the tile's); of keys that some rows see
         // and others do not, the elements that are not finite become zeros
-        // and the key is remembered.  A half-warp takes a key; the ranges of
-        // both kinds are few and short, and found once (these two warps get
-        // few of their schedulers' slots).
+        // and the key is remembered.  A half-warp takes a key, each thread
+        // the chunks that it copies where it does; the ranges of both kinds
+        // are few and short, and found once (these two warps get few of
+        // their schedulers' slots).
         auto clean = [&](int j, uint32_t r, uint8_t* tile) {
           const int slot = open_poison(j), kb = T.first_key(j);
           const int c = lt & 15, k0 = lt >> 4;
           auto zero = [&](int from, int to) {
-            for (int key = from + k0; key < to; key += 4)
+            for (int key = from + ((k0 - from) & 3); key < to; key += 4)
               *reinterpret_cast<uint4*>(tile + tile_byte(key, c)) = make_uint4(0u, 0u, 0u, 0u);
           };
           auto check = [&](int from, int to) {
-            for (int key = from + k0; key < to; key += 4) {
+            for (int key = from + ((k0 - from) & 3); key < to; key += 4) {
               uint4* at = reinterpret_cast<uint4*>(tile + tile_byte(key, c));
               const uint4 v = *at;
               uint32_t w[4] = {v.x, v.y, v.z, v.w}, odd = 0u;
@@ -491,21 +492,26 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
               *at = make_uint4(w[0], w[1], w[2], w[3]);
             }
           };
+          const unsigned there = __ballot_sync(0xffffffffu, r != kNoPage);
+          if (there != 0xffffffffu) {  // blocks of 16 keys on no page: key by key
+            for (int key = k0; key < 128; key += 4) {
+              if (!((there >> (key >> 4)) & 1u) || !seen(kb + key))
+                zero(key, key + 1);
+              else if (!all_seen(kb + key, kb + key))
+                check(key, key + 1);
+            }
+            return;
+          }
           // within the tile: the sinks end at s1; the windows begin at a0, all
-          // of them have begun at a1, the first ends at b0, all at b1
+          // of them have begun at a1, the first row ends at b0, the last at b1
           auto in = [&](int key) { return min(max(key - kb, 0), 128); };
-          const int s1 = in(P.sinks), a0 = max(in(wlo), s1), a1 = max(in(neg ? INT_MAX : wlo_all), s1);
+          const int s1 = in(P.sinks), a0 = max(in(wlo), s1), a1 = neg ? 128 : max(in(wlo_all), s1);
           const int b0 = neg ? 0 : in(pmin + 1), b1 = in(pmax + 1);
           zero(s1, min(a0, b1));
           zero(b1, 128);
-          check(min(a0, b1), min(max(a1, b0), b1));
-          if (b0 < a0) check(b0, min(s1, b1));  // (sinks that lie in the rows' own future)
-          if (a1 < b0) check(b0, b1);
-          if (!all_ok(r != kNoPage)) {  // blocks of 16 keys on no page
-            __syncwarp();
-            for (int g = 0; g < 8; ++g)
-              if (__shfl_sync(0xffffffffu, r, g) == kNoPage) zero(16 * g, 16 * g + 16);
-          }
+          check(b0, min(s1, b1));                    // sinks that lie ahead of some row
+          check(a0, min(a1, b1));                    // keys that some window has left
+          check(max(max(a0, b0), min(a1, b1)), b1);  // keys ahead of some row
         };
         // Small pages: K and V by cp.async.  A tile's K is announced once its V
         // is on the way, its V once the next tile's K is, or with its own data
@@ -978,6 +984,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       mbar_arrive(&sh.p_ready[x]);
     }
     // ---- output
+    // (the gate's half row into L2 while the last products run)
+    if (live && P.gate != nullptr && P.splits == 1)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(
+          P.gate + (static_cast<long long>(row0 + x * R + im / G) * P.hq + kvh * G + im % G) * 128 + 64 * hf));
     sh.pair[nt & 1][hf][m] = l;
     pair_sync(pair);
     l += sh.pair[nt & 1][hf ^ 1][m];
