@@ -426,8 +426,8 @@ typedef struct qsa_kv_scales {
  * Offsets after the run keep their codes: they belong to no token yet.
  *  - Slots < 0 write nothing for their row (padding); slots past the cache are
  *    masked and counted.
- *  - A row whose slot repeats its predecessor's or steps back inside one scale
- *    block is not written, and counted.  Runs of one call that are not
+ *  - A run whose first slot repeats the slot before it or steps back inside
+ *    that one's scale block is not written, and counted.  Runs of one call that are not
  *    neighbours must lie in different scale blocks: they would race.
  *  - A scale block belongs to one sequence: sequences that share a page share
  *    whole scale blocks that are full.
@@ -472,8 +472,8 @@ qsa_status qsa_sparse_gqa_scaled(const qsa_gqa_cfg* gcfg, const qsa_kv_scales* s
  *                 qsa_kv_append (NULL unless QSA_DTYPE_E4M3_BLOCK)
  *  block_table    [reqs, bt_stride]; entries of pages that no row of the call
  *                 sees may be stale or -1, and tokens that no row sees may
- *                 hold anything.  A visible token on a page outside the cache
- *                 is left out of the sum and counted
+ *                 hold anything.  A visible token past the table or on a
+ *                 page outside the cache is left out of the sum and counted
  *  ws             qsa_window_workspace_bytes() bytes, 256-byte aligned (NULL
  *                 where that is 0); its contents need not be kept or cleared
  */
@@ -513,8 +513,8 @@ size_t qsa_workspace_bytes(const qsa_cfg* cfg, const qsa_gqa_cfg* gcfg,
 int32_t qsa_step_launches(const qsa_cfg* cfg, const qsa_gqa_cfg* gcfg, int32_t rows,
                           int32_t reqs, int32_t skip_topk);
 
-/* Split-KV factor qsa_sparse_gqa uses for `rows` rows (1 = no split, no
- * scratch).  0 if invalid. */
+/* Split-KV factor qsa_sparse_gqa (qsa_sparse_gqa_scaled for its kv_dtype) uses
+ * for `rows` rows (1 = no split, no scratch).  0 if invalid. */
 int32_t qsa_gqa_splits(const qsa_gqa_cfg* gcfg, int32_t rows, int32_t packed_width);
 
 /* Static description of a status code. */

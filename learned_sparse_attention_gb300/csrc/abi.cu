@@ -610,16 +610,19 @@ qsa_status fill_row_gqa(RowGqaParams* p, const qsa_gqa_cfg* g, const qsa_kv_scal
   p->kv_dtype = g->kv_dtype;
   p->k_scale = g->k_scale;
   p->v_scale = g->v_scale;
-  p->err = error_word();
-  return p->err != nullptr ? QSA_OK : QSA_ERR_CUDA;
+  return QSA_OK;
 }
 
-// The split of the rows and its partials in ws.
+// The split of the rows and its partials in ws, and, the checks being done,
+// the device's error word.
 qsa_status place_splits(RowGqaParams* p, const qsa_gqa_cfg* g, int splits, void* ws, size_t ws_bytes) {
   p->splits = splits;
   const size_t need = row_ws_bytes(g, p->rows, splits);
+  if (need != 0 && (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < need))
+    return QSA_ERR_WORKSPACE;
+  p->err = error_word();
+  if (p->err == nullptr) return QSA_ERR_CUDA;
   if (need == 0) return QSA_OK;
-  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < need) return QSA_ERR_WORKSPACE;
   p->part_o = static_cast<float*>(ws);
   p->part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + row_partial_bytes(g, p->rows, splits));
   return QSA_OK;
@@ -687,9 +690,10 @@ qsa_status do_window(const qsa_gqa_cfg* g, const qsa_window_args* a, void* ws, s
   if (st != QSA_OK) return st;
   p.qsl = a->query_start_loc;
   p.logical = a->logical_positions;
-  // (a cache holds fewer tokens than 2^30; sums of positions stay in int32)
-  p.window = a->window < (1 << 30) ? a->window : 1 << 30;
-  p.sinks = a->sinks < (1 << 30) ? a->sinks : 1 << 30;
+  p.window = a->window;
+  p.sinks = a->sinks;
+  const long long keys = static_cast<long long>(a->bt_stride) * p.page;
+  p.keys = static_cast<int>(keys < kMaxKeys ? keys : kMaxKeys);
   const WindowPlan plan = window_plan(g, a);
   st = place_splits(&p, g, plan.splits, ws, ws_bytes);
   if (st != QSA_OK) return st;
@@ -1023,6 +1027,8 @@ int32_t qsa_step_launches(const qsa_cfg* cfg, const qsa_gqa_cfg* gcfg, int32_t r
 
 int32_t qsa_gqa_splits(const qsa_gqa_cfg* gcfg, int32_t rows, int32_t packed_width) {
   if (check_gcfg(gcfg, /*block_scales=*/true) != QSA_OK || rows <= 0 || packed_width < 2) return 0;
+  if (gcfg->kv_dtype == QSA_DTYPE_E4M3_BLOCK)
+    return row_gqa_splits(rows, gcfg->num_kv_heads, packed_width - 1, gcfg->kv_dtype, sm_count());
   return gqa_num_splits(rows, gcfg->num_kv_heads, packed_width, sm_count());
 }
 

@@ -133,6 +133,9 @@ int gqa_num_splits(int rows, int hkv, int packed_width, int sms);
 cudaError_t launch_sparse_gqa(const GqaParams& p, cudaStream_t stream, bool pdl,
                               bool zero_tickets = true);
 
+// Positions and token counts of window calls, with room for a tile above.
+constexpr int kMaxKeys = 0x7FFFFFFF - 255;
+
 // Attention of single rows: over the packed selection (packed != null) or
 // over the last `window` tokens and the first `sinks`.
 struct RowGqaParams {
@@ -151,6 +154,7 @@ struct RowGqaParams {
   int kv_dtype;
   float k_scale, v_scale;
   int window, sinks;
+  int keys;                // window only: tokens of a row of the table, at most kMaxKeys
   int box;                 // keys of a TMA box of the window tiles, 0: no TMA
   int splits;
   float* part_o;           // [splits, rows, Hq, 128] (splits > 1)

@@ -108,10 +108,12 @@ __global__ void __launch_bounds__(kThreads, 2) row_gqa_kernel(const RowGqaParams
     }
   } else {
     if (!row_live(P, row, req)) return;
-    const int p = P.logical[row];
-    ns = min(P.sinks, p + 1);
+    const int p = window_position(P, row);
+    const int end = min(p + 1, P.keys);  // (a position may lie past the table)
+    ns = min(P.sinks, end);
     lo = max(ns, p - P.window + 1);
-    n = p < 0 ? 0 : ns + max(0, p + 1 - lo);
+    n = p < 0 ? 0 : ns + max(0, end - lo);
+    if (p >= P.keys && threadIdx.x == 0 && (P.window > 0 || P.sinks > P.keys)) flag_error(P.err);
   }
   const int nslab = (n + TS - 1) / TS;
   const int per = (nslab + P.splits - 1) / P.splits;

@@ -21,6 +21,12 @@ __device__ __forceinline__ bool row_live(const RowGqaParams& P, int row, int req
   return req >= 0 && req < P.reqs && row >= P.qsl[req] && row < P.qsl[req + 1];
 }
 
+// A window call's position of a row, -1 before the start.  (Room above it for
+// the bounds of its key tile; no table reaches there.)
+__device__ __forceinline__ int window_position(const RowGqaParams& P, int row) {
+  return max(-1, min(P.logical[row], kMaxKeys));
+}
+
 // 1 / (1 + 2^(-x log2 e)) by the PTX approximate reciprocal (1 ulp): 0 for a
 // gate far below 0, where the exponential is an infinity.
 __device__ __forceinline__ float sigmoid_of(float x) {

@@ -34,7 +34,8 @@
 //
 // A V element that is not finite in a tile that some rows do not see would
 // reach them as 0 * inf: such elements are zeroed in the ring, remembered by
-// key, and added to the rows that see them at the end.
+// key, and added to the rows that see them at the end.  Rows before their
+// request's start see nothing and set no masks: their sums are not used.
 // Every wait is bounded (mbar_wait); a timeout sets the error word.
 #include <cuda_fp16.h>
 
@@ -55,7 +56,7 @@ constexpr int kThreads = (kSoftWarps + 4) * 32;
 constexpr int kTile = 128 * 256;  // bytes of 128 rows of 128 16-bit values, two 64-dim atoms
 constexpr int kAtom = 128 * 128;
 constexpr int kSlots = 4;        // tiles whose scales and page masks are kept
-constexpr int kPoison = 32;      // masked tiles that can remember odd V elements
+constexpr int kPoison = 32;      // tiles that can remember odd V elements
 // A row's reference is moved when a weight has grown by 2^8 (bf16) or 2^10.
 // bf16 weights: it is set so that the largest is 2^-7; that one has reached 2
 // shows in the top bit of its exponent, so a tile is checked by or-ing its
@@ -82,9 +83,9 @@ struct TileShared {
   uint64_t kfull[3], kempty[3], kgo[3], vfull[2], vempty[2], vgo[2], rfull[2], rempty[2];
   uint64_t info[kSlots], s_full[2], p_ready[2], q_ready, o_full, loads_done;
   uint32_t tmem;
-  int poison_n;
-  int poison_tile[kPoison];        // first key
+  int poison_tile[kPoison];        // first key, or -1 from the first free entry on
   uint32_t poison[kPoison][4];     // keys with an odd V element
+  uint32_t odd_keys[2][4];         // those of the tile that warp 18, 19 is at
   uint32_t valid[kSlots][4];       // keys on pages of the cache
   int check[kSlots];               // some key is not
   alignas(16) uint32_t scale[kSlots][8];  // of each 16 keys, two bf16: ks, and log2 vs above it
@@ -250,11 +251,28 @@ struct Tiles {
   __device__ __forceinline__ int first_key(int j) const { return (j < ns ? j : w0 + j - ns) * 128; }
 };
 
+__device__ __noinline__ void file_poison(TileShared* sh, int kb, uint32_t* odd_keys, unsigned long long* err) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    int b = 0;
+    for (; b < kPoison; ++b) {
+      const int was = atomicCAS(&sh->poison_tile[b], -1, kb);
+      if (was == -1 || was == kb) break;
+    }
+    if (b == kPoison) flag_error(err);
+    for (int w = 0; w < 4; ++w) {
+      if (b < kPoison) atomicOr(&sh->poison[b][w], odd_keys[w]);
+      odd_keys[w] = 0u;
+    }
+  }
+  __syncwarp();
+}
+
 // KVT 0 bf16, 1 e4m3 with static scales, 2 e4m3 with block scales
 template <int KVT>
 __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_constant__ CUtensorMap tmap, const RowGqaParams P) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int s_pmin, s_pmax, s_neg;
+  __shared__ int s_pmin, s_pmax;
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   uint8_t* sQ = smem_raw + pad;
   using RG = Rings<KVT>;
@@ -277,37 +295,36 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   if (tid == 0) {
     s_pmin = INT_MAX;
     s_pmax = -1;
-    s_neg = 0;
-    sh.poison_n = 0;
   }
+  if (tid < kPoison) sh.poison_tile[tid] = -1;
   if (tid < kPoison * 4) sh.poison[tid >> 2][tid & 3] = 0u;
+  if (tid < 8) sh.odd_keys[tid >> 2][tid & 3] = 0u;
   __syncthreads();
   if (tid < nrows) {
-    const int p = P.logical[row0 + tid];
-    if (p >= 0) {
+    const int p = window_position(P, row0 + tid);
+    if (p >= 0) {  // (others see nothing)
       atomicMin(&s_pmin, p);
       atomicMax(&s_pmax, p);
-    } else {
-      s_neg = 1;
     }
   }
   __syncthreads();
   const int pmin = s_pmin, pmax = s_pmax;
-  const bool neg = s_neg != 0;  // some row sees nothing
   const int wlo = pmax < 0 ? 0 : max(0, pmin - P.window + 1);     // first key of any window
   const int wlo_all = pmax < 0 ? 0 : max(0, pmax - P.window + 1); // of every window
   Tiles T;
   {
-    const int sinks = min(P.sinks, pmax + 1);
+    const int keys = min(pmax + 1, P.keys);  // (a position may lie past the table)
+    const int sinks = min(P.sinks, keys);
     T.ns = (sinks + 127) >> 7;
     T.w0 = max(T.ns, wlo >> 7);
-    const int end = P.window > 0 ? (pmax >> 7) + 1 : 0;
+    const int end = P.window > 0 ? (keys + 127) >> 7 : 0;
     T.n = pmax < 0 ? 0 : T.ns + max(0, end - T.w0);
   }
   const int per = (T.n + P.splits - 1) / P.splits;
   const int j0 = split * per, nt = max(0, min(T.n, j0 + per) - j0);
   const bool two = nrows > R;
 
+  if (pmax >= P.keys && tid == 0 && (P.window > 0 || P.sinks > P.keys)) flag_error(P.err);
   if (nt == 0) {  // nothing to see here: zeros, or an empty split
     for (int i = tid; i < nrows * G * 16; i += kThreads) {
       const int d0 = (i & 15) * 8, h = (i >> 4) % G, r = (i >> 4) / G;
@@ -360,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   const int page_shift = __ffs(P.page) - 1;
   auto seen = [&](int key) { return key <= pmax && (key >= wlo || key < P.sinks); };
   // every row of the CTA sees keys a .. b; none does any of them
-  auto all_seen = [&](int a, int b) { return !neg && b <= pmin && (a >= wlo_all || b < P.sinks); };
+  auto all_seen = [&](int a, int b) { return b <= pmin && (a >= wlo_all || b < P.sinks); };
   auto none_seen = [&](int a, int b) { return a > pmax || (b < wlo && a >= P.sinks); };
   // some row of the CTA does not see all of tile j
   auto tile_masked = [&](int j) {
@@ -417,14 +434,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     if (warp >= kSoftWarps + 2) {
       // ---------------------------------------------------------- by hand
       const int lt = tid - (kSoftWarps + 2) * 32;  // 0 .. 63
-      int masked_n = 0;
-      auto remember = [&](int slot, int key) {
-        if (slot < kPoison) atomicOr(&sh.poison[slot][key >> 5], 1u << (key & 31));
-        else flag_error(P.err);
-      };
-      auto open_poison = [&](int j) {  // (the same in every thread)
-        if (lt == 0 && masked_n < kPoison) sh.poison_tile[masked_n] = T.first_key(j);
-        return masked_n++;
+      // an odd element at key `key` of a tile, and, once the warp is through
+      // the tile (some is its lane's answer), the tile with its odd keys
+      uint32_t* odd_keys = sh.odd_keys[warp & 1];
+      auto remember = [&](int key) { atomicOr(&odd_keys[key >> 5], 1u << (key & 31)); };
+      auto file = [&](int kb, bool some) {
+        if (!__any_sync(0xffffffffu, some)) return;
+        file_poison(&sh, kb, odd_keys, P.err);
       };
       auto announce = [&](uint64_t* bar) {
         fence_proxy_async_smem();
@@ -468,13 +484,16 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         // are few and short, and found once (these two warps get few of
         // their schedulers' slots).
         auto clean = [&](int j, uint32_t r, uint8_t* tile) {
-          const int slot = open_poison(j), kb = T.first_key(j);
+          const int kb = T.first_key(j);
           const int c = lt & 15, k0 = lt >> 4;
+          bool some = false;
           auto zero = [&](int from, int to) {
+#pragma unroll 1
             for (int key = from + ((k0 - from) & 3); key < to; key += 4)
               *reinterpret_cast<uint4*>(tile + tile_byte(key, c)) = make_uint4(0u, 0u, 0u, 0u);
           };
           auto check = [&](int from, int to) {
+#pragma unroll 1
             for (int key = from + ((k0 - from) & 3); key < to; key += 4) {
               uint4* at = reinterpret_cast<uint4*>(tile + tile_byte(key, c));
               const uint4 v = *at;
@@ -488,7 +507,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
                 if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
                 if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
               }
-              remember(slot, key);
+              remember(key);
+              some = true;
               *at = make_uint4(w[0], w[1], w[2], w[3]);
             }
           };
@@ -500,18 +520,20 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
               else if (!all_seen(kb + key, kb + key))
                 check(key, key + 1);
             }
+            file(kb, some);
             return;
           }
           // within the tile: the sinks end at s1; the windows begin at a0, all
           // of them have begun at a1, the first row ends at b0, the last at b1
           auto in = [&](int key) { return min(max(key - kb, 0), 128); };
-          const int s1 = in(P.sinks), a0 = max(in(wlo), s1), a1 = neg ? 128 : max(in(wlo_all), s1);
-          const int b0 = neg ? 0 : in(pmin + 1), b1 = in(pmax + 1);
+          const int s1 = in(P.sinks), a0 = max(in(wlo), s1), a1 = max(in(wlo_all), s1);
+          const int b0 = in(pmin + 1), b1 = in(pmax + 1);
           zero(s1, min(a0, b1));
           zero(b1, 128);
           check(b0, min(s1, b1));                    // sinks that lie ahead of some row
           check(a0, min(a1, b1));                    // keys that some window has left
           check(max(max(a0, b0), min(a1, b1)), b1);  // keys ahead of some row
+          file(kb, some);
         };
         // Small pages: K and V by cp.async.  A tile's K is announced once its V
         // is on the way, its V once the next tile's K is, or with its own data
@@ -591,7 +613,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           ok = ok && all_ok(mbar_wait(&sh.vempty[vbuf], ((i / RG::NV) & 1) ^ 1, P.err));
           if (!ok) break;
           const bool hand = by_hand(j, here);
-          const int slot = hand ? open_poison(j) : 0;
           const unsigned there = __ballot_sync(0xffffffffu, here < kNoPage);
           const uint8_t* src = sR + rbuf * kAtom + tile_byte(k0, c);
           uint8_t* d0 = sV + vbuf * kTile + tile_byte(k0, 2 * c);
@@ -614,6 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
               for (int u = 0; u < 8; ++u) convert(q + u, v[u]);
             }
           } else {
+            bool some = false;
 #pragma unroll 1
             for (int q = 0; q < 16; ++q) {
               const int key = 8 * q + k0;
@@ -631,11 +653,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
                       w[e] &= ~(0xFFu << b);
                       odd = true;
                     }
-                if (odd) remember(slot, key);
+                if (odd) remember(key);
+                some |= odd;
                 v = make_uint4(w[0], w[1], w[2], w[3]);
               }
               convert(q, v);
             }
+            file(kb, some);
           }
           announce(&sh.vfull[vbuf]);
           if (P.box != 0 && lane == 0) mbar_arrive(&sh.rempty[rbuf]);
@@ -644,7 +668,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         }
         cp_async_wait<0>();
       }
-      if (lt == 0) sh.poison_n = min(masked_n, kPoison);
       mbar_arrive(&sh.loads_done);
     } else if (warp == kSoftWarps) {
       // ---------------------------------------------------------- MMA
@@ -779,8 +802,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     const int x = warp >> 3, hf = (warp >> 2) & 1, im = 32 * (warp & 3) + lane, m = 128 * x + im;
     const int pair = 1 + 4 * x + (warp & 3);  // the barrier of the row's two warps
     const bool live = im < R * G && x * R + im / G < nrows;
-    // its position (-1: before the start)
-    const int p = live ? max(P.logical[row0 + x * R + im / G], -1) : 0;
+    // its position; a row before the start computes what it likes and is
+    // zero at the end
+    auto position = [&] { return live ? window_position(P, row0 + x * R + im / G) : -1; };
+    const int p = max(position(), 0);
     // ---- Q of the two warps' 32 M rows, sixteen each, a half-warp per row
     {
       uint8_t* tile = sQ + x * kTile;
@@ -848,9 +873,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     const uint32_t ts = tmem + 128 * x + lanes, to = tmem + 256 + 128 * x + 64 * hf + lanes;
     const float qs = fabsf(sh.qs[m]);
     // the 32 rows' own bounds decide which key tiles need masks
-    const int hi_all = __reduce_min_sync(0xffffffffu, live ? p : INT_MAX);
-    const int lo_all = __reduce_max_sync(0xffffffffu, live ? p - P.window + 1 : INT_MIN);
-    float ref = -INFINITY, l = sh.qs[m] < 0.f ? __int_as_float(0x7fffffff) : 0.f;
+    const int hi_all = __reduce_min_sync(0xffffffffu, position() >= 0 ? p : INT_MAX);
+    const int lo_all = __reduce_max_sync(0xffffffffu, position() >= 0 ? p - P.window + 1 : INT_MIN);
+    // (a row that sees nothing never asks for a reference)
+    float ref = position() >= 0 ? -INFINITY : 0.f, l = sh.qs[m] < 0.f ? __int_as_float(0x7fffffff) : 0.f;
     // (a wait that gives up ends the waiting, not the loop: the two warps
     // always meet)
     bool ok = true;
@@ -996,10 +1022,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     const long long head = static_cast<long long>(row0 + x * R + im / G) * P.hq + kvh * G + im % G;
     const long long ph = static_cast<long long>(split) * P.rows * P.hq + head;
     // (a NaN sum is not an empty row)
-    const float inv = l == 0.f ? 0.f : (KVT == 1 ? P.v_scale : 1.0f) / l;
-    bool poisoned = false;
-    for (int b = 0; b < sh.poison_n; ++b)
-      poisoned |= (sh.poison[b][0] | sh.poison[b][1] | sh.poison[b][2] | sh.poison[b][3]) != 0u;
+    const bool sees = position() >= 0, empty = !sees || l == 0.f;
+    const float inv = (KVT == 1 ? P.v_scale : 1.0f) / l;
     // the warp's 32 rows and 64 dims cross to coalesced stores through their
     // own place in the Q tile, which no MMA reads any more
     uint8_t* tile = sQ + x * kTile;
@@ -1010,11 +1034,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       tmem_wait_ld32(o);
       float f[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * inv;
-      if (live && ok)
-      if (poisoned) {  // what the row sees of the remembered elements
+      for (int i = 0; i < 32; ++i) f[i] = empty ? 0.f : __uint_as_float(o[i]) * inv;
+      if (sees && ok) {  // what the row sees of the remembered elements
 #pragma unroll 1
-        for (int b = 0; b < sh.poison_n * 128; ++b) {
+        for (int b = 0; b < kPoison * 128 && sh.poison_tile[b >> 7] >= 0; ++b) {
           if (!((sh.poison[b >> 7][(b >> 5) & 3] >> (b & 31)) & 1u)) continue;
           const int key = sh.poison_tile[b >> 7] + (b & 127);
           if (key > p || !(key > p - P.window || key < P.sinks)) continue;
@@ -1043,7 +1066,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       }
     }
     if (P.splits > 1) {
-      if (live && ok && hf == 0) P.part_lse[ph] = l == 0.f ? -INFINITY : ref + log2f(l);
+      if (live && ok && hf == 0) P.part_lse[ph] = empty ? -INFINITY : ref + log2f(l);
     } else if (ok) {
       __syncwarp();
       // four rows at a time, eight lanes each

@@ -365,6 +365,20 @@ def _scales_fit(gcfg, scales):
         raise ValueError(f"scales has {scales._tensors.numel()} entries, the cache needs {need}")
 
 
+def _cache_fits(gcfg, kv):
+    """Likewise the cache itself, and a cache of the other element type."""
+    need = gcfg.num_blocks * gcfg.num_kv_heads * gcfg.page_size * 256
+    if kv.numel() < need:
+        raise ValueError(f"kv has {kv.numel()} entries, its configuration needs {need}")
+    if (kv.dtype == torch.bfloat16) != (gcfg.kv_dtype == DTYPE_BF16):
+        raise ValueError(f"kv has dtype {kv.dtype}, its configuration kv_dtype {gcfg.kv_dtype}")
+
+
+def _covers(t, need, name):
+    if t is not None and t.numel() < need:
+        raise ValueError(f"{name} has {t.numel()} entries, the call needs {need}")
+
+
 def _same_device(*tensors):
     """The device all tensors are on (None ones left out)."""
     dev = None
@@ -403,13 +417,23 @@ def kv_append(cfg, gcfg, m: QsaMainPrep, positions, cos_sin, scales: QsaKvScales
               stream=None):
     """Keys and values into the paged cache, normalised and rotated on the way,
     with q and gate beside them where `m` has them (qsa_kv_append)."""
+    t, rows = m._tensors, positions.shape[0]
     _scales_fit(gcfg, scales)
-    dev = _same_device(positions, cos_sin, m._tensors["kv"])
+    _cache_fits(gcfg, t["kv"])
+    hq, hkv = gcfg.num_q_heads, gcfg.num_kv_heads
+    _covers(t["main_qkv"], rows * (hq + hkv) * 256, "main_qkv")
+    _covers(t["slot_mapping"], rows, "slot_mapping")
+    _covers(t.get("main_q_out"), rows * hq * 128, "main_q_out")
+    _covers(t.get("main_gate_out"), rows * hq * 128, "main_gate_out")
+    _covers(positions, rows * 3, "positions")
+    _covers(cos_sin, cfg.max_position * cfg.rotary_dim, "cos_sin")
+    dev = _same_device(positions, cos_sin, t["kv"], t["main_qkv"], t["slot_mapping"],
+                       None if scales is None else scales._tensors)
     with _on(dev):
         st = load().qsa_kv_append(
             ctypes.byref(cfg), ctypes.byref(gcfg), ctypes.byref(m),
             None if scales is None else ctypes.byref(scales), _ptr(positions, torch.int64),
-            _ptr(cos_sin, torch.float32), positions.shape[0], _raw_stream(dev, stream))
+            _ptr(cos_sin, torch.float32), rows, _raw_stream(dev, stream))
     _check("qsa_kv_append", st)
 
 
@@ -417,13 +441,21 @@ def sparse_gqa_scaled(gcfg, scales: QsaKvScales, q, kv, block_table, packed, tok
                       out, ws, stream=None):
     """Stage 4 over a cache with block scales (qsa_sparse_gqa_scaled)."""
     _scales_fit(gcfg, scales)
-    dev = _same_device(q, kv, block_table, packed, token_to_req, gate, out, ws)
+    _cache_fits(gcfg, kv)
+    rows = q.shape[0]
+    need = rows * gcfg.num_q_heads * 128
+    _covers(q, need, "q")
+    _covers(out, need, "out")
+    _covers(gate, need, "gate")
+    _covers(packed, rows * packed.shape[1], "packed")
+    _covers(token_to_req, rows, "token_to_req")
+    dev = _same_device(q, kv, scales._tensors, block_table, packed, token_to_req, gate, out, ws)
     with _on(dev):
         st = load().qsa_sparse_gqa_scaled(
             ctypes.byref(gcfg), ctypes.byref(scales), _ptr(q, torch.bfloat16),
             _ptr(kv, torch.uint8), _ptr(block_table, torch.int32), block_table.shape[1],
             _ptr(packed, torch.int32), packed.shape[1], _ptr(token_to_req, torch.int32),
-            _ptr(gate, torch.bfloat16), _ptr(out, torch.bfloat16), q.shape[0],
+            _ptr(gate, torch.bfloat16), _ptr(out, torch.bfloat16), rows,
             block_table.shape[0], _ptr(ws, torch.uint8), 0 if ws is None else ws.numel(),
             _raw_stream(dev, stream))
     _check("qsa_sparse_gqa_scaled", st)
@@ -468,6 +500,8 @@ def window_gqa(gcfg, args: QsaWindowArgs, ws=None, stream=None):
     """Attention over the last `window` tokens and the first `sinks`
     (qsa_window_gqa); ws: uint8, window_workspace_bytes() long."""
     _scales_fit(gcfg, args._scales)
+    _cache_fits(gcfg, args._tensors[1])
+    _covers(args._tensors[0], args.rows * gcfg.num_q_heads * 128, "q")
     with _on(args._device):
         st = load().qsa_window_gqa(ctypes.byref(gcfg), ctypes.byref(args), _ptr(ws, torch.uint8),
                                    0 if ws is None else ws.numel(),

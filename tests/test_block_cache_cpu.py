@@ -153,6 +153,21 @@ def test_window_refusals(lib):
     assert lib.qsa_window_gqa(None, None, None, 0, None) == 1
 
 
+def test_split_rows_want_their_workspace(lib):
+    big = dict(rows=1, reqs=1, window=1 << 20, max_context=100000)
+    a = Q.QsaWindowArgs()
+    for k, v in big.items():
+        setattr(a, k, v)
+    need = lib.qsa_window_workspace_bytes(ctypes.byref(_gcfg()), ctypes.byref(a))
+    assert need > 0
+    for ws, n in ((None, need), (D256, need - 1), (ctypes.c_void_p(128), need)):
+        assert _window(lib, ws=ws, ws_bytes=n, **big) == 5
+    g = _gcfg()
+    assert lib.qsa_gqa_splits(ctypes.byref(g), 1, 4100) > 1
+    for ws, n in ((None, 1 << 30), (D256, 256), (ctypes.c_void_p(128), 1 << 30)):
+        assert _sparse(lib, rows=1, width=4100, ws=ws, ws_bytes=n) == 5
+
+
 def test_window_workspace_of_bad_sizes(lib):
     a = Q.QsaWindowArgs()
     a.rows = -1
@@ -168,6 +183,45 @@ def test_binding_refuses_host_tensors_and_small_scales(lib):
     s._tensors = torch.zeros(39, dtype=torch.uint8)
     with pytest.raises(ValueError):
         Q._scales_fit(_gcfg(), s)       # 10 blocks x 2 heads x 2 scale blocks x 2 = 80
+
+
+def test_binding_refuses_tensors_that_are_too_small():
+    """Each would be read or written past its end."""
+    g = Q.make_gqa_cfg(2, 1, 16, 3, kv_dtype=Q.DTYPE_E4M3_BLOCK)
+    cfg = Q.make_cfg(8, 4, 64, Q.DTYPE_BF16, 4, 10)
+    sc = _scales(block=16)
+    sc._tensors = torch.zeros(6, dtype=torch.uint8)
+    kv = torch.zeros((3, 1, 16, 256), dtype=torch.uint8)
+    bf = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16)  # noqa: E731
+    i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32)    # noqa: E731
+
+    def append(**kw):
+        t = dict(main_qkv=bf(4, 6 * 128), main_q_out=bf(4, 2, 128), main_gate_out=bf(4, 2, 128), kv=kv,
+                 slot_mapping=torch.zeros(4, dtype=torch.int64))
+        pos, cs = kw.pop("positions", torch.zeros((4, 1, 3), dtype=torch.int64)), kw.pop("cos_sin", torch.zeros(10, 64))
+        t.update(kw)
+        m = Q.QsaMainPrep()
+        m._tensors = t
+        Q.kv_append(cfg, g, m, pos, cs, scales=sc)
+
+    for name, small in dict(main_qkv=bf(3, 6 * 128), main_q_out=bf(3, 2, 128), main_gate_out=bf(4, 1, 128), kv=kv[:2],
+                            slot_mapping=torch.zeros(3, dtype=torch.int64), positions=torch.zeros((4, 1), dtype=torch.int64),
+                            cos_sin=torch.zeros(9, 64)).items():
+        with pytest.raises(ValueError, match=name):
+            append(**{name: small})
+    with pytest.raises(ValueError, match="kv has dtype"):
+        append(kv=kv.to(torch.bfloat16))
+
+    def sparse(**kw):
+        t = dict(q=bf(4, 2, 128), kv=kv, table=i32(1, 3), packed=i32(4, 9), t2r=i32(4), gate=None, out=bf(4, 2, 128))
+        t.update(kw)
+        Q.sparse_gqa_scaled(g, sc, t["q"], t["kv"], t["table"], t["packed"], t["t2r"], t["gate"], t["out"], None)
+
+    for name, small in dict(q=bf(4, 1, 128), kv=kv[:2], packed=i32(3, 9), t2r=i32(3), gate=bf(3, 2, 128), out=bf(4, 127)).items():
+        with pytest.raises(ValueError, match="token_to_req" if name == "t2r" else name):
+            sparse(**{name: small})
+    with pytest.raises(ValueError, match="CUDA"):
+        sparse()
 
 
 # ------------------------------------------------------------------ the oracle

@@ -264,3 +264,26 @@ def test_captured_and_replayed():
     torch.cuda.synchronize()
     c2.wq, c2.wk = c.wq, c.wk
     check_scaled(c2, slots, codes, scales)
+
+
+@pytest.mark.parametrize("rows", [40, 1100])
+def test_on_another_stream(rows):
+    """The call's work, queries included, is done when its stream is."""
+    c = Case(rows, blocks=60, seed=14)
+    slots = contiguous_slots(c, 32, rows)
+    codes, scales = c.codes.cuda(), c.scales.cuda()
+    t = c.tensors(codes, slots, True)
+    m, sc, pos, cs = Q.main_prep(t), Q.kv_scales(scales, c.block), c.positions.cuda(), c.cos_sin.cuda()
+    cfg, gcfg = c.cfg(Q.DTYPE_E4M3_BLOCK)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    Q.kv_append(cfg, gcfg, m, pos, cs, scales=sc, stream=s)
+    s.synchronize()
+    got = t["main_q_out"].clone()
+    check_scaled(c, slots, codes, scales)
+    codes2, scales2 = c.codes.cuda(), c.scales.cuda()
+    t2 = c.tensors(codes2, slots, True)
+    Q.kv_append(cfg, gcfg, Q.main_prep(t2), pos, cs, scales=Q.kv_scales(scales2, c.block))
+    torch.cuda.synchronize()
+    assert torch.equal(got, t2["main_q_out"]) and torch.equal(codes, codes2) and torch.equal(scales, scales2)
+    assert Q.check_errors() == 0

@@ -7,7 +7,7 @@ import torch
 
 from learned_sparse_attention_gb300 import qsa as Q
 from oracle import qsa_oracle as O
-from tests.attention_bounds import assert_row
+from tests.attention_bounds import assert_row, attend_row
 from tests.oracle_io import f64
 
 pytestmark = pytest.mark.gpu
@@ -334,6 +334,135 @@ def test_window_captured_and_on_two_streams():
     Q.window_gqa(*calls[0], ws, stream=s)
     s.synchronize()
     assert np.array_equal(f64(b.d["out"]), out_b)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "block"])
+@pytest.mark.parametrize("rows", [1, 70])
+def test_window_positions_past_the_table(kind, rows):
+    """Only the table's tokens are looked at, however far a position is."""
+    b = Batch([320], [rows], kind=kind, page=32, seed=13, hq=2, hkv=1, gate=False)
+    b.pos[:] = 2 ** 31 - 1 - np.arange(rows)[::-1]
+    out = b.window(2 ** 31 - 1, 2 ** 31 - 1)
+    assert Q.check_errors() > 0
+    for i in range(rows):
+        K, V = b.values(0, np.arange(320))
+        assert_row(out[i], f64(b.q[i]), K, V, None, f"row {i}")
+    assert (b.window(1000, 0) == 0).all()
+    assert Q.check_errors() > 0
+    out = b.window(0, 40)
+    assert Q.check_errors() == 0
+    for i in range(rows):
+        K, V = b.values(0, np.arange(40))
+        assert_row(out[i], f64(b.q[i]), K, V, None, f"row {i}")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "block"])
+def test_window_odd_values_beside_rows_before_the_start(kind):
+    """Values that are not finite in many tiles reach every row that sees them
+    and no row at a negative position."""
+    b = Batch([6000], [40], kind=kind, page=32, block=32, seed=14, hq=8, hkv=1, gate=False)
+    b.pos[5:20] = -np.arange(1, 16)
+    odd = np.arange(0, 6000, 130)
+    b.kv[torch.from_numpy(b.table[0, odd // 32].astype(np.int64)), 0, torch.from_numpy(odd % 32), D + 5] = \
+        0x7F if kind == "block" else float("nan")
+    out = b.window(100000, 0)
+    assert Q.check_errors() == 0
+    assert (out[5:20] == 0).all()
+    rest = np.r_[0:5, 20:40]
+    assert np.isnan(out[rest][:, :, 5]).all()
+    clean = np.arange(D) != 5
+    b.kv[torch.from_numpy(b.table[0, odd // 32].astype(np.int64)), 0, torch.from_numpy(odd % 32), D + 5] = 0
+    for i in (0, 4, 20, 39):
+        K, V = b.values(0, O.window_tokens(int(b.pos[i]), 100000, 0))
+        out[i][:, ~clean] = attend_row(f64(b.q[i]), K, V)[0][:, ~clean]
+        assert_row(out[i], f64(b.q[i]), K, V, None, f"row {i}")
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "block"])
+@pytest.mark.parametrize("page", [16, 64])
+def test_window_nan_codes_reach_only_rows_that_see_them(kind, page):
+    b = Batch([400], [70], kind=kind, page=page, block=16, seed=15, hq=2, hkv=1, gate=False)
+    toks = [345, 371, 399]   # left by the window, ahead of some rows, the last one's own
+    for tok in toks:
+        b.kv[b.table[0, tok // page], 0, tok % page, D + 9] = 0xFF
+    out = b.window(40, 0)
+    for i in range(b.n):
+        p = int(b.pos[i])
+        assert np.isnan(out[i][:, 9]).all() == any(p - 40 < t <= p for t in toks), p
+        assert np.isfinite(out[i][:, np.arange(D) != 9]).all(), p
+    assert Q.check_errors() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "block"])
+@pytest.mark.parametrize("rows", [1, 60])
+def test_window_far_into_a_large_cache(kind, rows):
+    """Pages whose bytes lie past 2^32."""
+    b = Batch([300], [rows], kind=kind, page=64, block=64, seed=16, hq=4, hkv=1)
+    row_bytes = 512 if kind == "bf16" else 256
+    ahead = 2 ** 32 // (64 * row_bytes) + 1
+    out_near = b.window(120, 3)
+    kv = torch.zeros((ahead + b.blocks,) + tuple(b.kv.shape[1:]), dtype=b.kv.dtype, device="cuda")
+    kv[ahead:] = b.d["kv"]
+    b.d["kv"], b.d["table"] = kv, b.d["table"] + ahead
+    if kind == "block":
+        b.d["scales"] = torch.cat([torch.zeros((ahead, 1, 1, 2), dtype=torch.uint8, device="cuda"), b.d["scales"]])
+        b.sc = Q.kv_scales(b.d["scales"], 64)
+    b.blocks += ahead
+    b.d["out"].fill_(7.0)
+    assert np.array_equal(b.window(120, 3), out_near)
+    assert Q.check_errors() == 0
+
+
+def test_calls_on_streams_side_by_side():
+    """Calls on three streams at once, each with a workspace of its own."""
+    batches = [Batch([4000, 2500], [1, 1], kind="block", page=64, block=32, seed=17, hq=8, hkv=2),
+               Batch([900], [300], kind="bf16", page=64, seed=18, hq=8, hkv=2),
+               Batch([2000] * 3, [1] * 3, kind="block", page=64, block=32, seed=19, hq=8, hkv=2)]
+    packed = packed_rows(batches[2], 1028, 3, [1024])
+    want = [batches[0].window(5000, 0), batches[1].window(400, 4), run_sparse(batches[2], packed)]
+    cfg = Q.make_cfg(8, 4, 1024, Q.DTYPE_BF16, 4, 1)
+    x = batches[2]
+    ws = [torch.empty(1 << 24, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    assert Q.workspace_bytes(cfg, x.gcfg(), 3, 3, 1) <= 1 << 24
+    args = []
+    for b, w, s in ((batches[0], 5000, 0), (batches[1], 400, 4)):
+        args.append(Q.window_args(b.d["q"], b.d["kv"], b.d["table"], b.d["t2r"], b.d["qsl"], b.d["pos"], b.d["out"], w, s,
+                                  max(b.contexts), gate=b.d["gate"], scales=b.sc))
+        assert Q.window_workspace_bytes(b.gcfg(), args[-1]) <= 1 << 24
+    pk = torch.from_numpy(packed).cuda()
+    for b in batches:
+        b.d["out"].fill_(3.0)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        for k in range(2):
+            Q.window_gqa(batches[k].gcfg(), args[k], ws[k], stream=streams[k])
+        Q.sparse_gqa_scaled(x.gcfg(), x.sc, x.d["q"], x.d["kv"], x.d["table"], pk, x.d["t2r"], x.d["gate"], x.d["out"], ws[2],
+                            stream=streams[2])
+    torch.cuda.synchronize()
+    for b, w in zip(batches, want):
+        assert np.array_equal(f64(b.d["out"]), w)
+
+
+def test_sparse_captured_and_replayed():
+    """Split rows as a graph, replayed on new selections."""
+    b = Batch([5000] * 4, [1] * 4, hq=8, hkv=2, page=64, block=32, seed=20)
+    packed = packed_rows(b, 2052, 1, [2048, 700])
+    run_sparse(b, packed)
+    d, pk = b.d, torch.from_numpy(packed).cuda()
+    cfg = Q.make_cfg(8, 4, 2048, Q.DTYPE_BF16, 4, 1)
+    ws = torch.empty(Q.workspace_bytes(cfg, b.gcfg(), 4, 4, 1), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Q.sparse_gqa_scaled(b.gcfg(), b.sc, d["q"], d["kv"], d["table"], pk, d["t2r"], d["gate"], d["out"], ws)
+    packed = packed_rows(b, 2052, 2, [33, 0, 2048, 1])
+    pk.copy_(torch.from_numpy(packed))
+    ws.fill_(0xFF)
+    graph.replay()
+    torch.cuda.synchronize()
+    check_sparse(b, packed, f64(d["out"]))
+    assert Q.check_errors() == 0
 
 
 # ------------------------------------------------------------------ together
