@@ -268,8 +268,11 @@ __device__ __noinline__ void file_poison(TileShared* sh, int kb, uint32_t* odd_k
   __syncwarp();
 }
 
-// KVT 0 bf16, 1 e4m3 with static scales, 2 e4m3 with block scales
-template <int KVT>
+// KVT 0 bf16, 1 e4m3 with static scales, 2 e4m3 with block scales.  TMA: pages
+// hold boxes (P.box != 0).  Kernels of their own, because 20 warps of different
+// work wait for instructions: with both paths in one, a chunk of 8192 rows on
+// a cache with block scales took 536 instead of 519 us.
+template <int KVT, bool TMA>
 __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_constant__ CUtensorMap tmap, const RowGqaParams P) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_pmin, s_pmax;
@@ -546,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           page_n = i + 2 < nt ? fetch_page(j + 2) : -1;
           const bool hand = by_hand(j, here);
           const int kbuf = i % RG::NK, vbuf = i % RG::NV;
-          if (P.box != 0) {
+          if (TMA) {
             if (!hand) continue;
             if (!wait_turn(sh.vgo, v_turn, vbuf)) break;
             clean(j, here, sV + vbuf * kTile);
@@ -584,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         // Small pages: this tile's codes by cp.async while the last one's V is
         // converted.
         auto start = [&](int i, uint32_t r) {  // false: a wait gave up
-          if (P.box != 0) return true;
+          if (TMA) return true;
           if (!wait_turn(sh.kgo, k_turn, i % RG::NK)) return false;
           if (lt < 32) publish(i, r, scale_word(r));
           const bool hand = by_hand(j0 + i, r);
@@ -595,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           return true;
         };
         auto end = [&](int i) {
-          if (P.box != 0) return;
+          if (TMA) return;
           cp_async_wait<0>();
           announce(&sh.kfull[i % RG::NK]);
         };
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           const uint32_t next = more ? to_row(j + 1, page_n) : kUnseen;
           page_n = i + 2 < nt ? fetch_page(j + 2) : -1;
           if (more) ok = start(i + 1, next);
-          if (ok && P.box != 0) ok = all_ok(mbar_wait(&sh.rfull[rbuf], (i / RG::NR) & 1, P.err));
+          if (ok && TMA) ok = all_ok(mbar_wait(&sh.rfull[rbuf], (i / RG::NR) & 1, P.err));
           ok = ok && all_ok(mbar_wait(&sh.vempty[vbuf], ((i / RG::NV) & 1) ^ 1, P.err));
           if (!ok) break;
           const bool hand = by_hand(j, here);
@@ -662,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
             file(kb, some);
           }
           announce(&sh.vfull[vbuf]);
-          if (P.box != 0 && lane == 0) mbar_arrive(&sh.rempty[rbuf]);
+          if (TMA && lane == 0) mbar_arrive(&sh.rempty[rbuf]);
           if (more) end(i + 1);
           here = next;
         }
@@ -773,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         }
         page_n = i + 2 < nt ? fetch_page(j + 2) : -1;
         if (!all_ok(mbar_wait(&sh.kempty[kbuf], ((i / RG::NK) & 1) ^ 1, P.err))) break;
-        if (P.box != 0) {
+        if (TMA) {
           publish(i, here, word_here);
           tile(&sh.kfull[kbuf], 2, sK + kbuf * RG::kKey, here, 0, KVT == 0 ? 2 : 1);
         } else if (lane == 0) {
@@ -781,14 +784,14 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         }
         if constexpr (KVT == 0) {
           if (!all_ok(mbar_wait(&sh.vempty[vbuf], ((i / RG::NV) & 1) ^ 1, P.err))) break;
-          if (P.box == 0) {
+          if (!TMA) {
             if (lane == 0) mbar_arrive(&sh.vgo[vbuf]);
           } else if (by_hand(j, here)) {
             tile(&sh.vgo[vbuf], 1, sV + vbuf * kTile, here, 128, 2);
           } else {
             tile(&sh.vfull[vbuf], 2, sV + vbuf * kTile, here, 128, 2);
           }
-        } else if (P.box != 0) {
+        } else if (TMA) {
           const int rbuf = i % RG::NR;
           if (!all_ok(mbar_wait(&sh.rempty[rbuf], ((i / RG::NR) & 1) ^ 1, P.err))) break;
           tile(&sh.rfull[rbuf], 1, sR + rbuf * kAtom, here, 128, 1);
@@ -1096,18 +1099,23 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   }
 }
 
-template <int KVT>
-cudaError_t launch_kind(const RowGqaParams& p, const CUtensorMap& tmap, const dim3& grid, cudaStream_t stream) {
+template <int KVT, bool TMA>
+cudaError_t launch_box(const RowGqaParams& p, const CUtensorMap& tmap, const dim3& grid, cudaStream_t stream) {
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(window_tile_kernel<KVT>,
+    const cudaError_t e = cudaFuncSetAttribute(window_tile_kernel<KVT, TMA>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<KVT>);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  return launch_kernel(window_tile_kernel<KVT>, grid, dim3(kThreads), kSmem<KVT>, stream, false, tmap, p);
+  return launch_kernel(window_tile_kernel<KVT, TMA>, grid, dim3(kThreads), kSmem<KVT>, stream, false, tmap, p);
+}
+
+template <int KVT>
+cudaError_t launch_kind(const RowGqaParams& p, const CUtensorMap& tmap, const dim3& grid, cudaStream_t stream) {
+  return p.box != 0 ? launch_box<KVT, true>(p, tmap, grid, stream) : launch_box<KVT, false>(p, tmap, grid, stream);
 }
 
 }  // namespace
