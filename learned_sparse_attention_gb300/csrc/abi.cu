@@ -502,9 +502,10 @@ qsa_status check_scales(const qsa_gqa_cfg* g, const qsa_kv_scales* s) {
   return g->page_size % s->scale_block == 0 ? QSA_OK : QSA_ERR_SHAPE;
 }
 
-// Row ids of the cache, (block * Hkv + head) * page + offset, have 32 bits.
+// Row ids of the cache, (block * Hkv + head) * page + offset, are coordinates
+// of TMA boxes: int32 (half a terabyte of codes).
 qsa_status check_row_ids(const qsa_gqa_cfg* g) {
-  return static_cast<long long>(g->num_blocks) * g->num_kv_heads * g->page_size < (1ll << 32) - 1
+  return static_cast<long long>(g->num_blocks) * g->num_kv_heads * g->page_size < (1ll << 31)
              ? QSA_OK
              : QSA_ERR_SHAPE;
 }
@@ -698,16 +699,13 @@ qsa_status do_window(const qsa_gqa_cfg* g, const qsa_window_args* a, void* ws, s
   st = place_splits(&p, g, plan.splits, ws, ws_bytes);
   if (st != QSA_OK) return st;
   if (!plan.tile) return cuda_status(launch_row_gqa(p, stream));
-  // boxes of the page's keys, up to a tile: pages of a multiple of 32 (the
-  // SM's TMA unit takes ~90 cycles a box; row coordinates are int32)
+  // boxes of a page's keys, or of a tile's where a page has more
   CUtensorMap tmap{};
   const long long cache_rows = static_cast<long long>(p.num_blocks) * p.hkv * p.page;
-  if (p.page % 32 == 0 && cache_rows < (1ll << 31)) {
-    p.box = p.page % 128 == 0 ? 128 : p.page % 64 == 0 ? 64 : 32;
-    if (!(p.kv_dtype == QSA_DTYPE_BF16 ? encode_bf16_2d(&tmap, a->kv, 256, cache_rows, p.box)
-                                       : encode_codes_2d(&tmap, a->kv, cache_rows, p.box)))
-      return QSA_ERR_CUDA;
-  }
+  p.box = p.page % 128 == 0 ? 128 : p.page % 64 == 0 ? 64 : p.page % 32 == 0 ? 32 : 16;
+  if (!(p.kv_dtype == QSA_DTYPE_BF16 ? encode_bf16_2d(&tmap, a->kv, 256, cache_rows, p.box)
+                                     : encode_codes_2d(&tmap, a->kv, cache_rows, p.box)))
+    return QSA_ERR_CUDA;
   return cuda_status(launch_window_tile(p, tmap, stream));
 }
 

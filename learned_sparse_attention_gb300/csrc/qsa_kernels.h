@@ -155,7 +155,7 @@ struct RowGqaParams {
   float k_scale, v_scale;
   int window, sinks;
   int keys;                // window only: tokens of a row of the table, at most kMaxKeys
-  int box;                 // keys of a TMA box of the window tiles, 0: no TMA
+  int box;                 // keys of a TMA box of the window tiles
   int splits;
   float* part_o;           // [splits, rows, Hq, 128] (splits > 1)
   float* part_lse;         // [splits, rows, Hq]
@@ -171,7 +171,7 @@ cudaError_t launch_row_merge(const RowGqaParams& p, cudaStream_t stream);
 int window_tile_rows(int group);  // rows of a CTA
 int window_tile_splits(int rows, int reqs, int hkv, int group, long long max_tokens, int sms);
 // tmap: the cache as [blocks * Hkv * page, 256] with a box of 128 bytes x
-// p.box rows (128-byte swizzle), read when p.box != 0.
+// p.box rows (128-byte swizzle).
 cudaError_t launch_window_tile(const RowGqaParams& p, const CUtensorMap& tmap, cudaStream_t stream);
 
 // Keys and values into the paged cache, q and gate beside them.

@@ -13,13 +13,10 @@
 //             them, P back over S's columns, at the end the gated output;
 //   16        issues the MMAs: S_A(j+1) right after O_A(j), so the softmax of
 //             one tile runs under the products of the other;
-//   17        loads by TMA.  It alone waits for the ring buffers that it or
-//             warps 18-19 fill with K (and V of bf16 caches) to be free, in
-//             order, and hands those that are not its own to them;
+//   17        loads by TMA, a box for each page's share of a tile;
 //   18, 19    what needs a thread's hand: V of tiles that some row does not
 //             see (keys that no row of the CTA sees become zeros, whatever the
-//             cache holds there), V of e4m3 caches from codes to f16 (exact),
-//             and tiles on pages of less than a TMA box, by cp.async.
+//             cache holds there), V of e4m3 caches from codes to f16 (exact).
 // Two warps to a row and tile because a warp alone on its scheduler issues an
 // instruction every other cycle at best: with one, the ~550 instructions of a
 // row's softmax took 1450 cycles, the two products 1060 a tile, and neither
@@ -80,7 +77,7 @@ struct Rings {
 };
 
 struct TileShared {
-  uint64_t kfull[3], kempty[3], kgo[3], vfull[2], vempty[2], vgo[2], rfull[2], rempty[2];
+  uint64_t kfull[3], kempty[3], vfull[2], vempty[2], vgo[2], rfull[2], rempty[2];
   uint64_t info[kSlots], s_full[2], p_ready[2], q_ready, o_full, loads_done;
   uint32_t tmem;
   int poison_tile[kPoison];        // first key, or -1 from the first free entry on
@@ -151,18 +148,6 @@ __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int32
       " [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(smem_addr(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
       : "memory");
-}
-// Whether the phase with the given parity is complete, without waiting.
-__device__ __forceinline__ bool mbar_done(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
 }
 // The largest of three.
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -268,11 +253,8 @@ __device__ __noinline__ void file_poison(TileShared* sh, int kb, uint32_t* odd_k
   __syncwarp();
 }
 
-// KVT 0 bf16, 1 e4m3 with static scales, 2 e4m3 with block scales.  TMA: pages
-// hold boxes (P.box != 0).  Kernels of their own, because 20 warps of different
-// work wait for instructions: with both paths in one, a chunk of 8192 rows on
-// a cache with block scales took 536 instead of 519 us.
-template <int KVT, bool TMA>
+// KVT 0 bf16, 1 e4m3 with static scales, 2 e4m3 with block scales.
+template <int KVT>
 __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_constant__ CUtensorMap tmap, const RowGqaParams P) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_pmin, s_pmax;
@@ -343,11 +325,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   }
 
   if (tid == 0) {
-    // (full: a lane of each of warps 18 and 19, or the TMA warp's for both)
+    // (vfull: a lane of each of warps 18 and 19, or the TMA warp's for both)
     for (int i = 0; i < 3; ++i) {
-      mbar_init(&sh.kfull[i], 2);
+      mbar_init(&sh.kfull[i], 1);
       mbar_init(&sh.kempty[i], 1);
-      mbar_init(&sh.kgo[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.vfull[i], 2);
@@ -374,8 +355,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   const uint32_t tmem = sh.tmem;
 
   const int32_t* bt_row = P.block_table + static_cast<long long>(req) * P.bt_stride;
-  const uint8_t* kvb = static_cast<const uint8_t*>(P.kv);
-  constexpr int kRow = KVT == 0 ? 512 : 256;  // bytes of a token and KV head
   const bool page_pow2 = (P.page & (P.page - 1)) == 0;
   const int page_shift = __ffs(P.page) - 1;
   auto seen = [&](int key) { return key <= pmax && (key >= wlo || key < P.sinks); };
@@ -450,31 +429,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
       };
-      // buffer b, from warp 17 (it is handed over again only once its tile
-      // has been loaded and read)
-      uint32_t k_turn = 0u, v_turn = 0u;
-      auto wait_turn = [&](uint64_t* bars, uint32_t& turns, int b) {
-        const bool ok = all_ok(mbar_wait(&bars[b], (turns >> b) & 1u, P.err));
-        turns ^= 1u << b;
-        return ok;
-      };
-      // 128 keys' K or V by cp.async: CH 16-byte chunks a key
-      auto copy = [&](uint8_t* dst, const uint8_t* src, uint32_t rows, int kb, bool masked, auto chunks) {
-        constexpr int CH = decltype(chunks)::value, PER = 64 / CH;  // keys a pass
-        const int c = lt % CH, k0 = lt / CH;
-#pragma unroll 2
-        for (int g = 0; g < 8; ++g) {  // 16 keys
-          const uint32_t r = __shfl_sync(0xffffffffu, rows, g);
-#pragma unroll
-          for (int i = 0; i < 16 / PER; ++i) {
-            const int key = 16 * g + i * PER + k0;
-            const bool ok = r < kNoPage && (!masked || seen(kb + key));
-            cp_async16(dst + tile_byte(key, c), src + c * 16 + static_cast<unsigned long long>(ok ? r + (key & 15) : 0u) * kRow,
-                       ok ? 16u : 0u);
-          }
-        }
-        cp_async_commit();
-      };
       int page_n = nt > 1 ? fetch_page(j0 + 1) : -1;
       uint32_t rows = to_row(j0, fetch_page(j0));
 
@@ -482,22 +436,21 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         // V of tile j as it has landed: zeroes for keys that no row sees or
         // whose page is none (rows: the tile's); of keys that some rows see
         // and others do not, the elements that are not finite become zeros
-        // and the key is remembered.  A half-warp takes a key, each thread
-        // the chunks that it copies where it does; the ranges of both kinds
-        // are few and short, and found once (these two warps get few of
-        // their schedulers' slots).
+        // and the key is remembered.  A half-warp takes a key; the ranges of
+        // both kinds are few and short, and found once (these two warps get
+        // few of their schedulers' slots).
         auto clean = [&](int j, uint32_t r, uint8_t* tile) {
           const int kb = T.first_key(j);
           const int c = lt & 15, k0 = lt >> 4;
           bool some = false;
           auto zero = [&](int from, int to) {
 #pragma unroll 1
-            for (int key = from + ((k0 - from) & 3); key < to; key += 4)
+            for (int key = from + k0; key < to; key += 4)
               *reinterpret_cast<uint4*>(tile + tile_byte(key, c)) = make_uint4(0u, 0u, 0u, 0u);
           };
           auto check = [&](int from, int to) {
 #pragma unroll 1
-            for (int key = from + ((k0 - from) & 3); key < to; key += 4) {
+            for (int key = from + k0; key < to; key += 4) {
               uint4* at = reinterpret_cast<uint4*>(tile + tile_byte(key, c));
               const uint4 v = *at;
               uint32_t w[4] = {v.x, v.y, v.z, v.w}, odd = 0u;
@@ -519,9 +472,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           if (there != 0xffffffffu) {  // blocks of 16 keys on no page: key by key
             for (int key = k0; key < 128; key += 4) {
               if (!((there >> (key >> 4)) & 1u) || !seen(kb + key))
-                zero(key, key + 1);
+                zero(key - k0, key + 1);
               else if (!all_seen(kb + key, kb + key))
-                check(key, key + 1);
+                check(key - k0, key + 1);
             }
             file(kb, some);
             return;
@@ -538,83 +491,28 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           check(max(max(a0, b0), min(a1, b1)), b1);  // keys ahead of some row
           file(kb, some);
         };
-        // Small pages: K and V by cp.async.  A tile's K is announced once its V
-        // is on the way, its V once the next tile's K is, or with its own data
-        // where there is nothing to start meanwhile or it is cleaned.
-        int v_open = -1;  // the buffer whose V is on the way
+        uint32_t turns = 0u;  // of each buffer, handed over by warp 17
         for (int i = 0; i < nt; ++i) {
-          const int j = j0 + i, kb = T.first_key(j);
+          const int j = j0 + i, vbuf = i % RG::NV;
           const uint32_t here = rows;
           if (i + 1 < nt) rows = to_row(j + 1, page_n);
           page_n = i + 2 < nt ? fetch_page(j + 2) : -1;
-          const bool hand = by_hand(j, here);
-          const int kbuf = i % RG::NK, vbuf = i % RG::NV;
-          if (TMA) {
-            if (!hand) continue;
-            if (!wait_turn(sh.vgo, v_turn, vbuf)) break;
-            clean(j, here, sV + vbuf * kTile);
-            announce(&sh.vfull[vbuf]);
-            continue;
-          }
-          if (v_open >= 0 && !all_ok(mbar_done(&sh.kgo[kbuf], (k_turn >> kbuf) & 1u))) {
-            cp_async_wait<0>();  // (nothing to start meanwhile)
-            announce(&sh.vfull[v_open]);
-            v_open = -1;
-          }
-          if (!wait_turn(sh.kgo, k_turn, kbuf)) break;
-          if (lt < 32) publish(i, here, 0u);
-          copy(sK + kbuf * kTile, kvb, here, kb, hand, Int<16>());
-          if (v_open >= 0) {
-            cp_async_wait<1>();
-            announce(&sh.vfull[v_open]);
-            v_open = -1;
-          }
-          if (!wait_turn(sh.vgo, v_turn, vbuf)) break;
-          copy(sV + vbuf * kTile, kvb + 256, here, kb, hand, Int<16>());
-          cp_async_wait<1>();
-          announce(&sh.kfull[kbuf]);
-          if (hand) {
-            cp_async_wait<0>();
-            clean(j, here, sV + vbuf * kTile);  // (each thread its own chunks)
-            announce(&sh.vfull[vbuf]);
-          } else {
-            v_open = vbuf;
-          }
+          if (!by_hand(j, here)) continue;
+          if (!all_ok(mbar_wait(&sh.vgo[vbuf], (turns >> vbuf) & 1u, P.err))) break;
+          turns ^= 1u << vbuf;
+          clean(j, here, sV + vbuf * kTile);
+          announce(&sh.vfull[vbuf]);
         }
-        cp_async_wait<0>();
-        if (v_open >= 0) announce(&sh.vfull[v_open]);
       } else {
-        // Small pages: this tile's codes by cp.async while the last one's V is
-        // converted.
-        auto start = [&](int i, uint32_t r) {  // false: a wait gave up
-          if (TMA) return true;
-          if (!wait_turn(sh.kgo, k_turn, i % RG::NK)) return false;
-          if (lt < 32) publish(i, r, scale_word(r));
-          const bool hand = by_hand(j0 + i, r);
-          copy(sK + (i % RG::NK) * RG::kKey, kvb, r, T.first_key(j0 + i), hand, Int<8>());
-          // (V's codes: each thread converts what it copied, so the buffer is
-          // its own to refill)
-          copy(sR + (i % RG::NR) * kAtom, kvb + 128, r, T.first_key(j0 + i), hand, Int<8>());
-          return true;
-        };
-        auto end = [&](int i) {
-          if (TMA) return;
-          cp_async_wait<0>();
-          announce(&sh.kfull[i % RG::NK]);
-        };
-        uint32_t here = rows;
-        bool ok = start(0, here);
-        if (ok) end(0);
         const int c = lt & 7, k0 = lt >> 3;
-        for (int i = 0; i < nt && ok; ++i) {
+        for (int i = 0; i < nt; ++i) {
           const int j = j0 + i, kb = T.first_key(j), vbuf = i % RG::NV, rbuf = i % RG::NR;
-          const bool more = i + 1 < nt;
-          const uint32_t next = more ? to_row(j + 1, page_n) : kUnseen;
+          const uint32_t here = rows;
+          if (i + 1 < nt) rows = to_row(j + 1, page_n);
           page_n = i + 2 < nt ? fetch_page(j + 2) : -1;
-          if (more) ok = start(i + 1, next);
-          if (ok && TMA) ok = all_ok(mbar_wait(&sh.rfull[rbuf], (i / RG::NR) & 1, P.err));
-          ok = ok && all_ok(mbar_wait(&sh.vempty[vbuf], ((i / RG::NV) & 1) ^ 1, P.err));
-          if (!ok) break;
+          if (!all_ok(mbar_wait(&sh.rfull[rbuf], (i / RG::NR) & 1, P.err) &&
+                      mbar_wait(&sh.vempty[vbuf], ((i / RG::NV) & 1) ^ 1, P.err)))
+            break;
           const bool hand = by_hand(j, here);
           const unsigned there = __ballot_sync(0xffffffffu, here < kNoPage);
           const uint8_t* src = sR + rbuf * kAtom + tile_byte(k0, c);
@@ -665,11 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
             file(kb, some);
           }
           announce(&sh.vfull[vbuf]);
-          if (TMA && lane == 0) mbar_arrive(&sh.rempty[rbuf]);
-          if (more) end(i + 1);
-          here = next;
+          if (lane == 0) mbar_arrive(&sh.rempty[rbuf]);
         }
-        cp_async_wait<0>();
       }
       mbar_arrive(&sh.loads_done);
     } else if (warp == kSoftWarps) {
@@ -745,26 +640,31 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       // ---------------------------------------------------------- TMA
       int page_n = nt > 1 ? fetch_page(j0 + 1) : -1;
       uint32_t rows = to_row(j0, fetch_page(j0)), word = scale_word(rows);
-      // the boxes of one tile that hold keys of the cache, on `full` with
-      // `arrivals` arrivals
-      auto tile = [&](uint64_t* full, uint32_t arrivals, uint8_t* dst, uint32_t r, int x, int atoms) {
-        const unsigned there = __ballot_sync(0xffffffffu, r < kNoPage) & 0xFFu;  // of 16-key blocks
-        const unsigned blocks = (1u << (P.box >> 4)) - 1u;                       // of a box
-        int n = 0;
-        for (int k = 0; k < 128; k += P.box) n += ((there >> (k >> 4)) & blocks) != 0u;
+      // The boxes of a tile that hold keys of the cache: a bit for each at its
+      // first 16-key block, whose lane has its cache row.
+      auto find_boxes = [&](uint32_t r, int& y) {
+        const unsigned there = __ballot_sync(0xffffffffu, r < kNoPage) & 0xFFu;
+        const int per = P.box >> 4;  // blocks of a box
+        const unsigned in = (there >> (lane & 7)) & ((1u << per) - 1u);
+        // (its first block may be one that nothing sees: count back)
+        const int first = in != 0u ? __ffs(in) - 1 : 0;
+        y = static_cast<int>(__shfl_sync(0xffffffffu, r, (lane & 7) + first)) - 16 * first;
+        return __ballot_sync(0xffffffffu, lane < 8 && lane % per == 0 && in != 0u);
+      };
+      // them at columns x .. (atoms of 128 bytes) on `full` with `arrivals`
+      // arrivals
+      auto tile = [&](uint64_t* full, uint32_t arrivals, uint8_t* dst, unsigned boxes, int y, int x, int atoms) {
         if (lane == 0) {
-          mbar_arrive_expect_tx(full, n * atoms * P.box * 128);
+          mbar_arrive_expect_tx(full, __popc(boxes) * atoms * P.box * 128);
           if (arrivals > 1) mbar_arrive(full);
         }
         __syncwarp();
-        for (int k = 0; k < 128; k += P.box) {
-          const unsigned in = (there >> (k >> 4)) & blocks;
-          if (in == 0u) continue;
-          // (the box's first block may be one that nothing sees: count back)
-          const int first = __ffs(in) - 1;
-          const int y = static_cast<int>(__shfl_sync(0xffffffffu, r, (k >> 4) + first)) - 16 * first;
-          tma_box(dst + k * 128, &tmap, x, y, full);
-          if (atoms == 2) tma_box(dst + kAtom + k * 128, &tmap, x + 64, y, full);
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          if (!((boxes >> b) & 1u)) continue;
+          const int yb = __shfl_sync(0xffffffffu, y, b);
+          tma_box(dst + b * 2048, &tmap, x, yb, full);
+          if (atoms == 2) tma_box(dst + kAtom + b * 2048, &tmap, x + 64, yb, full);
         }
       };
       for (int i = 0; i < nt; ++i) {
@@ -775,26 +675,22 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           word = scale_word(rows);
         }
         page_n = i + 2 < nt ? fetch_page(j + 2) : -1;
+        int y;
+        const unsigned boxes = find_boxes(here, y);
         if (!all_ok(mbar_wait(&sh.kempty[kbuf], ((i / RG::NK) & 1) ^ 1, P.err))) break;
-        if (TMA) {
-          publish(i, here, word_here);
-          tile(&sh.kfull[kbuf], 2, sK + kbuf * RG::kKey, here, 0, KVT == 0 ? 2 : 1);
-        } else if (lane == 0) {
-          mbar_arrive(&sh.kgo[kbuf]);
-        }
+        publish(i, here, word_here);
+        tile(&sh.kfull[kbuf], 1, sK + kbuf * RG::kKey, boxes, y, 0, KVT == 0 ? 2 : 1);
         if constexpr (KVT == 0) {
           if (!all_ok(mbar_wait(&sh.vempty[vbuf], ((i / RG::NV) & 1) ^ 1, P.err))) break;
-          if (!TMA) {
-            if (lane == 0) mbar_arrive(&sh.vgo[vbuf]);
-          } else if (by_hand(j, here)) {
-            tile(&sh.vgo[vbuf], 1, sV + vbuf * kTile, here, 128, 2);
+          if (by_hand(j, here)) {
+            tile(&sh.vgo[vbuf], 1, sV + vbuf * kTile, boxes, y, 128, 2);
           } else {
-            tile(&sh.vfull[vbuf], 2, sV + vbuf * kTile, here, 128, 2);
+            tile(&sh.vfull[vbuf], 2, sV + vbuf * kTile, boxes, y, 128, 2);
           }
-        } else if (TMA) {
+        } else {
           const int rbuf = i % RG::NR;
           if (!all_ok(mbar_wait(&sh.rempty[rbuf], ((i / RG::NR) & 1) ^ 1, P.err))) break;
-          tile(&sh.rfull[rbuf], 1, sR + rbuf * kAtom, here, 128, 1);
+          tile(&sh.rfull[rbuf], 1, sR + rbuf * kAtom, boxes, y, 128, 1);
         }
       }
     }
@@ -1099,23 +995,18 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   }
 }
 
-template <int KVT, bool TMA>
-cudaError_t launch_box(const RowGqaParams& p, const CUtensorMap& tmap, const dim3& grid, cudaStream_t stream) {
+template <int KVT>
+cudaError_t launch_kind(const RowGqaParams& p, const CUtensorMap& tmap, const dim3& grid, cudaStream_t stream) {
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(window_tile_kernel<KVT, TMA>,
+    const cudaError_t e = cudaFuncSetAttribute(window_tile_kernel<KVT>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<KVT>);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  return launch_kernel(window_tile_kernel<KVT, TMA>, grid, dim3(kThreads), kSmem<KVT>, stream, false, tmap, p);
-}
-
-template <int KVT>
-cudaError_t launch_kind(const RowGqaParams& p, const CUtensorMap& tmap, const dim3& grid, cudaStream_t stream) {
-  return p.box != 0 ? launch_box<KVT, true>(p, tmap, grid, stream) : launch_box<KVT, false>(p, tmap, grid, stream);
+  return launch_kernel(window_tile_kernel<KVT>, grid, dim3(kThreads), kSmem<KVT>, stream, false, tmap, p);
 }
 
 }  // namespace
