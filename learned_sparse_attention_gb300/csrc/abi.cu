@@ -607,6 +607,7 @@ qsa_status fill_row_gqa(RowGqaParams* p, const qsa_gqa_cfg* g, const qsa_kv_scal
   p->hkv = g->num_kv_heads;
   p->group = g->num_q_heads / g->num_kv_heads;
   p->page = g->page_size;
+  p->page_magic = static_cast<unsigned>(((1ull << 32) + g->page_size - 1) / g->page_size);
   p->num_blocks = g->num_blocks;
   p->kv_dtype = g->kv_dtype;
   p->k_scale = g->k_scale;

@@ -151,6 +151,7 @@ struct RowGqaParams {
   uint16_t* out;
   int bt_stride, packed_width;
   int rows, reqs, hq, hkv, group, page, num_blocks, scale_block;
+  unsigned page_magic;     // ceil(2^32 / page)
   int kv_dtype;
   float k_scale, v_scale;
   int window, sinks;

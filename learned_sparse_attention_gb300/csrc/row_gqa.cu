@@ -120,8 +120,6 @@ __global__ void __launch_bounds__(kThreads, 2) row_gqa_kernel(const RowGqaParams
   const int sb = split * per, se = min(nslab, sb + per);
   const int cnt = se > sb + warp ? (se - sb - warp + kWarps - 1) / kWarps : 0;  // slabs of this warp
   const int32_t* bt_row = P.block_table + static_cast<long long>(n > 0 ? req : 0) * P.bt_stride;
-  const bool page_pow2 = (P.page & (P.page - 1)) == 0;
-  const int page_shift = __ffs(P.page) - 1;
   // the tokens and pages of a warp's slab i: lane l < TS its l-th token
   auto fetch_tok = [&](int i) -> int {
     const int at = (sb + warp + kWarps * i) * TS + lane;
@@ -130,10 +128,9 @@ __global__ void __launch_bounds__(kThreads, 2) row_gqa_kernel(const RowGqaParams
     const int e = prow[at];
     return e < 0 ? -2 : e;  // (-1: no token; -2: an entry that is none)
   };
-  auto block_of = [&](int tok) { return page_pow2 ? tok >> page_shift : tok / P.page; };
   auto fetch_page = [&](int tok) -> int {
     if (tok < 0) return -1;
-    const int blk = block_of(tok);
+    const int blk = page_of(P, tok);
     return blk < P.bt_stride ? bt_row[blk] : -1;
   };
   bool bad = false;
@@ -143,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 2) row_gqa_kernel(const RowGqaParams
       bad = true;
       return kBadRow;
     }
-    return (static_cast<uint32_t>(page) * P.hkv + kvh) * static_cast<uint32_t>(P.page) + (tok - block_of(tok) * P.page);
+    return (static_cast<uint32_t>(page) * P.hkv + kvh) * static_cast<uint32_t>(P.page) + (tok - page_of(P, tok) * P.page);
   };
   int tok[ST + 1], pg[ST];
 #pragma unroll

@@ -27,6 +27,13 @@ __device__ __forceinline__ int window_position(const RowGqaParams& P, int row) {
   return max(-1, min(P.logical[row], kMaxKeys));
 }
 
+// n / page for n >= 0: the multiplication by ceil(2^32 / page) is at most one
+// too large.
+__device__ __forceinline__ int page_of(const RowGqaParams& P, int n) {
+  const unsigned b = __umulhi(static_cast<unsigned>(n), P.page_magic);
+  return static_cast<int>(b * P.page > static_cast<unsigned>(n) ? b - 1u : b);
+}
+
 // 1 / (1 + 2^(-x log2 e)) by the PTX approximate reciprocal (1 ulp): 0 for a
 // gate far below 0, where the exponential is an infinity.
 __device__ __forceinline__ float sigmoid_of(float x) {

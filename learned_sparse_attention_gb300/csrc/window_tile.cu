@@ -78,7 +78,7 @@ struct Rings {
 
 struct TileShared {
   uint64_t kfull[3], kempty[3], vfull[2], vempty[2], vgo[2], rfull[2], rempty[2];
-  uint64_t info[kSlots], s_full[2], p_ready[2], q_ready, o_full, loads_done;
+  uint64_t info[kSlots], s_full[2], p_ready[2], q_ready[2], o_full[2], loads_done;
   uint32_t tmem;
   int poison_tile[kPoison];        // first key, or -1 from the first free entry on
   uint32_t poison[kPoison][4];     // keys with an odd V element
@@ -205,6 +205,12 @@ __device__ __forceinline__ constexpr int tile_byte(int r, int c) {
   return (c >> 3) * kAtom + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // The two warps of a row meet (64 threads); with a vote, any's answer.
 __device__ __forceinline__ void pair_sync(int id) {
   asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
@@ -271,12 +277,64 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be uniform)
   const int kvh = blockIdx.y, split = blockIdx.z;
   const int G = P.group, R = 128 / G;
+  // the row and the head of an M row (below 256 + 16)
+  const unsigned g_magic = 65536u / G + 1u;
+  auto row_of = [&](int im) { return static_cast<int>(im * g_magic >> 16); };
+  auto head_of = [&](int im) { return im - row_of(im) * G; };
   griddep_launch_dependents();
+  // ---- barriers and TMEM, while the row group's loads are on their way
+  if (tid == kThreads - 1) {
+    // (vfull: a lane of each of warps 18 and 19, or the TMA warp's for both)
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&sh.kfull[i], 1);
+      mbar_init(&sh.kempty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.vfull[i], 2);
+      mbar_init(&sh.vempty[i], 1);
+      mbar_init(&sh.vgo[i], 1);
+      mbar_init(&sh.rfull[i], 1);
+      mbar_init(&sh.rempty[i], 2);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_ready[i], 256);
+      mbar_init(&sh.q_ready[i], 8);
+      mbar_init(&sh.o_full[i], 1);
+    }
+    for (int i = 0; i < kSlots; ++i) mbar_init(&sh.info[i], 1);
+    mbar_init(&sh.loads_done, 64);
+    fence_barrier_init();
+  }
+  if (warp == kSoftWarps) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
   const int4 grp = find_group(P.qsl, P.reqs, P.rows, 2 * R, blockIdx.x, P.err);
-  if (grp.x < 0) return;
+  tc_fence_after_sync();
+  const uint32_t tmem = sh.tmem;
+  auto free_tmem = [&] {
+    if (warp == kSoftWarps) tmem_dealloc(tmem, 512);
+  };
+  if (grp.x < 0) {
+    free_tmem();
+    return;
+  }
   const int row0 = grp.x, nrows = grp.y, req = grp.z;
 
-  // ---- positions of the CTA's rows
+  // ---- positions of the CTA's rows, and behind them the Q rows on their way:
+  // sixteen M rows a warp, a half-warp per row
+  const int own_pos = tid < nrows ? window_position(P, row0 + tid) : -1;
+  uint4 qv[8];
+  if (warp < kSoftWarps) {
+    const int im0 = 32 * (warp & 3) + 16 * ((warp >> 2) & 1) + (lane >> 4);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int im = im0 + 2 * u, r = (warp >> 3) * R + row_of(im);
+      qv[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (im < R * G && r < nrows)
+        qv[u] = *reinterpret_cast<const uint4*>(P.q + (static_cast<long long>(row0 + r) * P.hq + kvh * G + head_of(im)) * 128 + 8 * (lane & 15));
+    }
+  }
   if (tid == 0) {
     s_pmin = INT_MAX;
     s_pmax = -1;
@@ -285,12 +343,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   if (tid < kPoison * 4) sh.poison[tid >> 2][tid & 3] = 0u;
   if (tid < 8) sh.odd_keys[tid >> 2][tid & 3] = 0u;
   __syncthreads();
-  if (tid < nrows) {
-    const int p = window_position(P, row0 + tid);
-    if (p >= 0) {  // (others see nothing)
-      atomicMin(&s_pmin, p);
-      atomicMax(&s_pmax, p);
-    }
+  if (own_pos >= 0) {  // (others see nothing)
+    atomicMin(&s_pmin, own_pos);
+    atomicMax(&s_pmax, own_pos);
   }
   __syncthreads();
   const int pmin = s_pmin, pmax = s_pmax;
@@ -305,14 +360,14 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     const int end = P.window > 0 ? (keys + 127) >> 7 : 0;
     T.n = pmax < 0 ? 0 : T.ns + max(0, end - T.w0);
   }
-  const int per = (T.n + P.splits - 1) / P.splits;
+  const int per = P.splits > 1 ? (T.n + P.splits - 1) / P.splits : T.n;
   const int j0 = split * per, nt = max(0, min(T.n, j0 + per) - j0);
   const bool two = nrows > R;
 
   if (pmax >= P.keys && tid == 0 && (P.window > 0 || P.sinks > P.keys)) flag_error(P.err);
   if (nt == 0) {  // nothing to see here: zeros, or an empty split
     for (int i = tid; i < nrows * G * 16; i += kThreads) {
-      const int d0 = (i & 15) * 8, h = (i >> 4) % G, r = (i >> 4) / G;
+      const int d0 = (i & 15) * 8, h = head_of(i >> 4), r = row_of(i >> 4);
       const long long head = static_cast<long long>(row0 + r) * P.hq + kvh * G + h;
       if (P.splits > 1) {
         if (d0 == 0) P.part_lse[static_cast<long long>(split) * P.rows * P.hq + head] = -INFINITY;
@@ -321,42 +376,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         store_gated8(P, head * 128 + d0, z, load_gate(P, head * 128 + d0));
       }
     }
+    free_tmem();
     return;
   }
 
-  if (tid == 0) {
-    // (vfull: a lane of each of warps 18 and 19, or the TMA warp's for both)
-    for (int i = 0; i < 3; ++i) {
-      mbar_init(&sh.kfull[i], 1);
-      mbar_init(&sh.kempty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.vfull[i], 2);
-      mbar_init(&sh.vempty[i], 1);
-      mbar_init(&sh.vgo[i], 1);
-      mbar_init(&sh.rfull[i], 1);
-      mbar_init(&sh.rempty[i], 2);
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_ready[i], 256);
-    }
-    for (int i = 0; i < kSlots; ++i) mbar_init(&sh.info[i], 1);
-    mbar_init(&sh.q_ready, two ? 16 : 8);
-    mbar_init(&sh.o_full, 1);
-    mbar_init(&sh.loads_done, 64);
-    fence_barrier_init();
-  }
-  if (warp == kSoftWarps) {
-    tmem_alloc(&sh.tmem, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before_sync();
-  __syncthreads();
-  tc_fence_after_sync();
-  const uint32_t tmem = sh.tmem;
 
   const int32_t* bt_row = P.block_table + static_cast<long long>(req) * P.bt_stride;
-  const bool page_pow2 = (P.page & (P.page - 1)) == 0;
-  const int page_shift = __ffs(P.page) - 1;
+  const int scale_shift = KVT == 2 ? __ffs(P.scale_block) - 1 : 0;
   auto seen = [&](int key) { return key <= pmax && (key >= wlo || key < P.sinks); };
   // every row of the CTA sees keys a .. b; none does any of them
   auto all_seen = [&](int a, int b) { return b <= pmin && (a >= wlo_all || b < P.sinks); };
@@ -374,14 +400,14 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   auto fetch_page = [&](int j) -> int {
     const int k0 = block_key(j);
     if (!(k0 <= pmax && (k0 + 15 >= wlo || k0 < P.sinks))) return -1;
-    const int blk = page_pow2 ? k0 >> page_shift : k0 / P.page;
+    const int blk = page_of(P, k0);
     return blk < P.bt_stride ? bt_row[blk] : -1;
   };
   auto to_row = [&](int j, int page) -> uint32_t {
     const int k0 = block_key(j);
     if (!(k0 <= pmax && (k0 + 15 >= wlo || k0 < P.sinks))) return kUnseen;
     if (page < 0 || page >= P.num_blocks) return kNoPage;
-    const int blk = page_pow2 ? k0 >> page_shift : k0 / P.page;
+    const int blk = page_of(P, k0);
     return (static_cast<uint32_t>(page) * P.hkv + kvh) * static_cast<uint32_t>(P.page) + (k0 - blk * P.page);
   };
   // V of a tile that some row does not see, or that lies on a page that is
@@ -389,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   auto by_hand = [&](int j, uint32_t rows) { return tile_masked(j) || !all_ok(rows != kNoPage); };
   auto scale_word = [&](uint32_t rows) -> uint32_t {
     if (KVT != 2 || rows >= kNoPage) return 0x7F7Fu;
-    return *reinterpret_cast<const uint16_t*>(P.scales + 2ll * (rows / P.scale_block));
+    return *reinterpret_cast<const uint16_t*>(P.scales + 2ll * (rows >> scale_shift));
   };
   // what the softmax needs to know of tile number i, before its K is announced
   auto publish = [&](int i, uint32_t rows, uint32_t scales) {
@@ -602,11 +628,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         tc_fence_after_sync();
         return ok;
       };
-      bool ok = all_ok(mbar_wait(&sh.q_ready, 0, P.err)) && wait_k(0);
+      bool ok = all_ok(mbar_wait(&sh.q_ready[0], 0, P.err)) && wait_k(0);
       if (ok) {
         scores(0, 0);
         mma_commit(&sh.s_full[0]);
         if (two) {
+          ok = all_ok(mbar_wait(&sh.q_ready[1], 0, P.err));
+          tc_fence_after_sync();
           scores(1, 0);
           mma_commit(&sh.s_full[1]);
         }
@@ -621,6 +649,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           if (!ok) break;
           scores(0, i + 1);
           mma_commit(&sh.s_full[0]);
+        } else {
+          mma_commit(&sh.o_full[0]);
         }
         if (two) {
           ok = values(1, i);
@@ -635,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           mma_commit(&sh.kempty[(i + 1) % RG::NK]);
         }
       }
-      mma_commit(&sh.o_full);
+      mma_commit(&sh.o_full[1]);
     } else if (warp == kSoftWarps + 1) {
       // ---------------------------------------------------------- TMA
       int page_n = nt > 1 ? fetch_page(j0 + 1) : -1;
@@ -700,49 +730,38 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     // M row im of tile x; this thread's 64 keys (at the end: dims) of it
     const int x = warp >> 3, hf = (warp >> 2) & 1, im = 32 * (warp & 3) + lane, m = 128 * x + im;
     const int pair = 1 + 4 * x + (warp & 3);  // the barrier of the row's two warps
-    const bool live = im < R * G && x * R + im / G < nrows;
+    const bool live = im < R * G && x * R + row_of(im) < nrows;
     // its position; a row before the start computes what it likes and is
     // zero at the end
-    auto position = [&] { return live ? window_position(P, row0 + x * R + im / G) : -1; };
-    const int p = max(position(), 0);
+    auto position = [&] { return live ? window_position(P, row0 + x * R + row_of(im)) : -1; };
+    const int pos = position(), p = max(pos, 0);
     // ---- Q of the two warps' 32 M rows, sixteen each, a half-warp per row
     {
       uint8_t* tile = sQ + x * kTile;
       const int lane16 = lane & 15, im0 = 32 * (warp & 3) + 16 * hf + (lane >> 4);
-      uint4 v[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int im = im0 + 2 * u, r = x * R + im / G;
-        v[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (im < R * G && r < nrows)
-          v[u] = *reinterpret_cast<const uint4*>(P.q + (static_cast<long long>(row0 + r) * P.hq + kvh * G + im % G) * 128 + 8 * lane16);
-      }
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int im = im0 + 2 * u;
         float qs = 0.08838834764831845f * kLog2e;
         if constexpr (KVT == 0) {
-          *reinterpret_cast<uint4*>(tile + tile_byte(im, lane16)) = v[u];
+          *reinterpret_cast<uint4*>(tile + tile_byte(im, lane16)) = qv[u];
         } else {
-          const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-          float f[8], peak = 0.f;
-          bool odd = false;
+          const uint32_t w[4] = {qv[u].x, qv[u].y, qv[u].z, qv[u].w};
+          // the largest |q| as bf16 bits (0x7F80 and more: not finite)
+          uint32_t top = 0u;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            f[e] = e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
-            odd |= !(fabsf(f[e]) <= 3.39e38f);
-            peak = fmaxf(peak, fabsf(f[e]));
-          }
+          for (int e = 0; e < 4; ++e) top = max_u16x2(top, w[e] & 0x7FFF7FFFu);
+          top = max_u16x2(top, top >> 16);
 #pragma unroll
-          for (int o = 8; o >= 1; o >>= 1) {
-            peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, o));
-            odd |= __shfl_xor_sync(0xffffffffu, static_cast<int>(odd), o) != 0;
-          }
-          const int e = peak > 0.f ? max(__float_as_int(peak) >> 23, 1) - 127 - 7 : 0;
-          const float f0 = exp2i(-(e / 2)), f1 = exp2i(-(e - e / 2));
+          for (int o = 8; o >= 1; o >>= 1) top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const uint32_t peak = top & 0xFFFFu;
+          // (a row below 2^-119 keeps fewer bits: its scores are 0 beside 1)
+          const int e = peak != 0u ? max(static_cast<int>(peak >> 7) - 127 - 7, -126) : 0;
+          const float f0 = exp2i(-e);
+          float f[8];
           uint32_t hi[2], lo[2];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = odd ? 0.f : f[i] * f0 * f1;
+          for (int i = 0; i < 8; ++i) f[i] = (i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1])) * f0;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t h0 = f32x2_to_e4m3x2(f[4 * i], f[4 * i + 1]), h1 = f32x2_to_e4m3x2(f[4 * i + 2], f[4 * i + 3]);
@@ -754,8 +773,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
             lo[i] = static_cast<uint32_t>(f32x2_to_e4m3x2(f[4 * i] - y0.x, f[4 * i + 1] - y0.y)) |
                     (static_cast<uint32_t>(f32x2_to_e4m3x2(f[4 * i + 2] - y1.x, f[4 * i + 3] - y1.y)) << 16);
           }
-          qs = fmaxf(exp2i(e / 2) * (qs * (KVT == 1 ? P.k_scale : 1.0f)) * exp2i(e - e / 2), kLeast);
-          if (odd) qs = -1.0f;
+          qs = fmaxf(qs * (KVT == 1 ? P.k_scale : 1.0f) * exp2i(e), kLeast);
+          if (peak >= 0x7F80u) qs = -1.0f;
           // the hi terms' atom, then the lo terms'
           uint8_t* dst = tile + im * 128 + (((lane16 >> 1) ^ (im & 7)) << 4) + (lane16 & 1) * 8;
           *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
@@ -766,16 +785,20 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     }
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.q_ready);
+    if (lane == 0) mbar_arrive(&sh.q_ready[x]);
+    // (the gate's half row into L2 while there is time)
+    if (live && P.gate != nullptr && P.splits == 1)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(
+          P.gate + (static_cast<long long>(row0 + x * R + row_of(im)) * P.hq + kvh * G + head_of(im)) * 128 + 64 * hf));
     pair_sync(pair);
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + 128 * x + lanes, to = tmem + 256 + 128 * x + 64 * hf + lanes;
     const float qs = fabsf(sh.qs[m]);
     // the 32 rows' own bounds decide which key tiles need masks
-    const int hi_all = __reduce_min_sync(0xffffffffu, position() >= 0 ? p : INT_MAX);
-    const int lo_all = __reduce_max_sync(0xffffffffu, position() >= 0 ? p - P.window + 1 : INT_MIN);
+    const int hi_all = __reduce_min_sync(0xffffffffu, pos >= 0 ? p : INT_MAX);
+    const int lo_all = __reduce_max_sync(0xffffffffu, pos >= 0 ? p - P.window + 1 : INT_MIN);
     // (a row that sees nothing never asks for a reference)
-    float ref = position() >= 0 ? -INFINITY : 0.f, l = sh.qs[m] < 0.f ? __int_as_float(0x7fffffff) : 0.f;
+    float ref = pos >= 0 && sh.qs[m] > 0.f ? -INFINITY : 0.f, l = sh.qs[m] < 0.f ? __int_as_float(0x7fffffff) : 0.f;
     // (a wait that gives up ends the waiting, not the loop: the two warps
     // always meet)
     bool ok = true;
@@ -909,16 +932,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       mbar_arrive(&sh.p_ready[x]);
     }
     // ---- output
-    // (the gate's half row into L2 while the last products run)
-    if (live && P.gate != nullptr && P.splits == 1)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(
-          P.gate + (static_cast<long long>(row0 + x * R + im / G) * P.hq + kvh * G + im % G) * 128 + 64 * hf));
     sh.pair[nt & 1][hf][m] = l;
     pair_sync(pair);
     l += sh.pair[nt & 1][hf ^ 1][m];
-    ok = all_ok(ok && mbar_wait(&sh.o_full, 0, P.err) && mbar_wait(&sh.loads_done, 0, P.err));
+    ok = all_ok(ok && mbar_wait(&sh.o_full[x], 0, P.err) && mbar_wait(&sh.loads_done, 0, P.err));
     tc_fence_after_sync();
-    const long long head = static_cast<long long>(row0 + x * R + im / G) * P.hq + kvh * G + im % G;
+    const long long head = static_cast<long long>(row0 + x * R + row_of(im)) * P.hq + kvh * G + head_of(im);
     const long long ph = static_cast<long long>(split) * P.rows * P.hq + head;
     // (a NaN sum is not an empty row)
     const bool sees = position() >= 0, empty = !sees || l == 0.f;
@@ -940,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           if (!((sh.poison[b >> 7][(b >> 5) & 3] >> (b & 31)) & 1u)) continue;
           const int key = sh.poison_tile[b >> 7] + (b & 127);
           if (key > p || !(key > p - P.window || key < P.sinks)) continue;
-          const int blk = key / P.page;
+          const int blk = page_of(P, key);
           const int pid = P.block_table[static_cast<long long>(req) * P.bt_stride + blk];
           const long long at = ((static_cast<long long>(pid) * P.hkv + kvh) * P.page + key - blk * P.page) * 256 + 128 + 64 * hf + 32 * c;
 #pragma unroll
@@ -972,27 +991,25 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       const int c8 = 8 * hf + (lane & 7), im0 = 32 * (warp & 3) + (lane >> 3);
       uint4 gate[8];
       auto at = [&](int i2) {
-        return (static_cast<long long>(row0 + x * R + i2 / G) * P.hq + kvh * G + i2 % G) * 128 + 8 * c8;
+        return (static_cast<long long>(row0 + x * R + row_of(i2)) * P.hq + kvh * G + head_of(i2)) * 128 + 8 * c8;
       };
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int i2 = im0 + 4 * u;
-        gate[u] = i2 < R * G && x * R + i2 / G < nrows ? load_gate(P, at(i2)) : make_uint4(0u, 0u, 0u, 0u);
+        gate[u] = i2 < R * G && x * R + row_of(i2) < nrows ? load_gate(P, at(i2)) : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int i2 = im0 + 4 * u;
-        if (i2 < R * G && x * R + i2 / G < nrows)
+        if (i2 < R * G && x * R + row_of(i2) < nrows)
           store_gated(P, at(i2), *reinterpret_cast<const uint4*>(tile + tile_byte(i2, c8)), gate[u]);
       }
     }
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == kSoftWarps) {
-    tc_fence_after_sync();
-    tmem_dealloc(tmem, 512);
-  }
+  tc_fence_after_sync();
+  free_tmem();
 }
 
 template <int KVT>
