@@ -458,53 +458,38 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       int page_n = nt > 1 ? fetch_page(j0 + 1) : -1;
       uint32_t rows = to_row(j0, fetch_page(j0));
 
-      if constexpr (KVT == 0) {
-        // V of tile j as it has landed: zeroes for keys that no row sees or
-        // whose page is none (rows: the tile's); of keys that some rows see
-        // and others do not, the elements that are not finite become zeros
-        // and the key is remembered.  A half-warp takes a key; the ranges of
-        // both kinds are few and short, and found once (these two warps get
-        // few of their schedulers' slots).
-        auto clean = [&](int j, uint32_t r, uint8_t* tile) {
-          const int kb = T.first_key(j);
-          const int c = lt & 15, k0 = lt >> 4;
-          bool some = false;
-          auto zero = [&](int from, int to) {
+      // Goes through tile j's V, whose 16-key blocks are on cache rows r: zeroes
+      // for keys that no row sees or whose page is none; of keys that some rows
+      // see and others do not, the elements that are not finite become zeros
+      // and the key is remembered (check_key says whether it had some).  64 / S
+      // threads take a key; the ranges of both kinds are few and short, and
+      // found once (these two warps get few of their schedulers' slots).
+      auto mask_tile = [&](int j, uint32_t r, auto stride, auto zero_key, auto check_key) {
+        constexpr int S = decltype(stride)::value;
+        const int kb = T.first_key(j), k0 = lt / (64 / S);
+        bool some = false;
+        auto zero = [&](int from, int to) {
 #pragma unroll 1
-            for (int key = from + k0; key < to; key += 4)
-              *reinterpret_cast<uint4*>(tile + tile_byte(key, c)) = make_uint4(0u, 0u, 0u, 0u);
-          };
-          auto check = [&](int from, int to) {
+          for (int key = from + ((k0 - from) & (S - 1)); key < to; key += S) zero_key(key);
+        };
+        auto check = [&](int from, int to) {
 #pragma unroll 1
-            for (int key = from + k0; key < to; key += 4) {
-              uint4* at = reinterpret_cast<uint4*>(tile + tile_byte(key, c));
-              const uint4 v = *at;
-              uint32_t w[4] = {v.x, v.y, v.z, v.w}, odd = 0u;
-              // an exponent of all ones carries into the sign's place
-#pragma unroll
-              for (int e = 0; e < 4; ++e) odd |= ((w[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-              if (odd == 0u) continue;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
-                if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
-              }
+          for (int key = from + ((k0 - from) & (S - 1)); key < to; key += S)
+            if (check_key(key)) {
               remember(key);
               some = true;
-              *at = make_uint4(w[0], w[1], w[2], w[3]);
             }
-          };
-          const unsigned there = __ballot_sync(0xffffffffu, r != kNoPage);
-          if (there != 0xffffffffu) {  // blocks of 16 keys on no page: key by key
-            for (int key = k0; key < 128; key += 4) {
-              if (!((there >> (key >> 4)) & 1u) || !seen(kb + key))
-                zero(key - k0, key + 1);
-              else if (!all_seen(kb + key, kb + key))
-                check(key - k0, key + 1);
-            }
-            file(kb, some);
-            return;
+        };
+        const unsigned there = __ballot_sync(0xffffffffu, r != kNoPage);
+        if (there != 0xffffffffu) {  // blocks of 16 keys on no page: key by key
+#pragma unroll 1
+          for (int key = 0; key < 128; ++key) {
+            if (!((there >> (key >> 4)) & 1u) || !seen(kb + key))
+              zero(key, key + 1);
+            else if (!all_seen(kb + key, kb + key))
+              check(key, key + 1);
           }
+        } else {
           // within the tile: the sinks end at s1; the windows begin at a0, all
           // of them have begun at a1, the first row ends at b0, the last at b1
           auto in = [&](int key) { return min(max(key - kb, 0), 128); };
@@ -515,8 +500,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           check(b0, min(s1, b1));                    // sinks that lie ahead of some row
           check(a0, min(a1, b1));                    // keys that some window has left
           check(max(max(a0, b0), min(a1, b1)), b1);  // keys ahead of some row
-          file(kb, some);
-        };
+        }
+        file(kb, some);
+      };
+      if constexpr (KVT == 0) {
+        // V of masked tiles as it has landed
+        const int c = lt & 15;
         uint32_t turns = 0u;  // of each buffer, handed over by warp 17
         for (int i = 0; i < nt; ++i) {
           const int j = j0 + i, vbuf = i % RG::NV;
@@ -526,21 +515,38 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           if (!by_hand(j, here)) continue;
           if (!all_ok(mbar_wait(&sh.vgo[vbuf], (turns >> vbuf) & 1u, P.err))) break;
           turns ^= 1u << vbuf;
-          clean(j, here, sV + vbuf * kTile);
+          uint8_t* tile = sV + vbuf * kTile;
+          mask_tile(
+              j, here, Int<4>(),
+              [&](int key) { *reinterpret_cast<uint4*>(tile + tile_byte(key, c)) = make_uint4(0u, 0u, 0u, 0u); },
+              [&](int key) {
+                uint4* at = reinterpret_cast<uint4*>(tile + tile_byte(key, c));
+                const uint4 v = *at;
+                uint32_t w[4] = {v.x, v.y, v.z, v.w}, odd = 0u;
+                // an exponent of all ones carries into the sign's place
+#pragma unroll
+                for (int e = 0; e < 4; ++e) odd |= ((w[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                if (odd == 0u) return false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
+                  if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
+                }
+                *at = make_uint4(w[0], w[1], w[2], w[3]);
+                return true;
+              });
           announce(&sh.vfull[vbuf]);
         }
       } else {
         const int c = lt & 7, k0 = lt >> 3;
         for (int i = 0; i < nt; ++i) {
-          const int j = j0 + i, kb = T.first_key(j), vbuf = i % RG::NV, rbuf = i % RG::NR;
+          const int j = j0 + i, vbuf = i % RG::NV, rbuf = i % RG::NR;
           const uint32_t here = rows;
           if (i + 1 < nt) rows = to_row(j + 1, page_n);
           page_n = i + 2 < nt ? fetch_page(j + 2) : -1;
           if (!all_ok(mbar_wait(&sh.rfull[rbuf], (i / RG::NR) & 1, P.err) &&
                       mbar_wait(&sh.vempty[vbuf], ((i / RG::NV) & 1) ^ 1, P.err)))
             break;
-          const bool hand = by_hand(j, here);
-          const unsigned there = __ballot_sync(0xffffffffu, here < kNoPage);
           const uint8_t* src = sR + rbuf * kAtom + tile_byte(k0, c);
           uint8_t* d0 = sV + vbuf * kTile + tile_byte(k0, 2 * c);
           uint8_t* d1 = sV + vbuf * kTile + tile_byte(k0, 2 * c + 1);
@@ -552,42 +558,36 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
             *reinterpret_cast<uint4*>(d0 + 1024 * q) = make_uint4(f[0], f[1], f[2], f[3]);
             *reinterpret_cast<uint4*>(d1 + 1024 * q) = make_uint4(f[4], f[5], f[6], f[7]);
           };
-          if (!hand) {
 #pragma unroll
-            for (int q = 0; q < 16; q += 8) {
-              uint4 v[8];
+          for (int q = 0; q < 16; q += 8) {
+            uint4 v[8];
 #pragma unroll
-              for (int u = 0; u < 8; ++u) v[u] = *reinterpret_cast<const uint4*>(src + 1024 * (q + u));
+            for (int u = 0; u < 8; ++u) v[u] = *reinterpret_cast<const uint4*>(src + 1024 * (q + u));
 #pragma unroll
-              for (int u = 0; u < 8; ++u) convert(q + u, v[u]);
-            }
-          } else {
-            bool some = false;
-#pragma unroll 1
-            for (int q = 0; q < 16; ++q) {
-              const int key = 8 * q + k0;
-              uint4 v = *reinterpret_cast<const uint4*>(src + 1024 * q);
-              if (!((there >> (q >> 1)) & 1u) || !seen(kb + key)) {
-                v = make_uint4(0u, 0u, 0u, 0u);
-              } else if (!all_seen(kb + key, kb + key)) {
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                bool odd = false;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                  for (int b = 0; b < 32; b += 8)
-                    if (((w[e] >> b) & 0x7Fu) == 0x7Fu) {
-                      w[e] &= ~(0xFFu << b);
-                      odd = true;
-                    }
-                if (odd) remember(key);
-                some |= odd;
-                v = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-              convert(q, v);
-            }
-            file(kb, some);
+            for (int u = 0; u < 8; ++u) convert(q + u, v[u]);
           }
+          if (by_hand(j, here))  // (each thread the keys that it converted)
+            mask_tile(
+                j, here, Int<8>(),
+                [&](int key) {
+                  *reinterpret_cast<uint4*>(d0 + 1024 * (key >> 3)) = make_uint4(0u, 0u, 0u, 0u);
+                  *reinterpret_cast<uint4*>(d1 + 1024 * (key >> 3)) = make_uint4(0u, 0u, 0u, 0u);
+                },
+                [&](int key) {
+                  const uint4 v = *reinterpret_cast<const uint4*>(src + 1024 * (key >> 3));
+                  uint32_t w[4] = {v.x, v.y, v.z, v.w}, odd = 0u;
+                  // a NaN's seven ones carry into the sign's place
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) odd |= ((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                  if (odd == 0u) return false;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const uint32_t nan = ((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                    w[e] &= ~(nan | (nan - (nan >> 7)));
+                  }
+                  convert(key >> 3, make_uint4(w[0], w[1], w[2], w[3]));
+                  return true;
+                });
           announce(&sh.vfull[vbuf]);
           if (lane == 0) mbar_arrive(&sh.rempty[rbuf]);
         }
