@@ -156,7 +156,7 @@ struct RowGqaParams {
   float k_scale, v_scale;
   int window, sinks;
   int keys;                // window only: tokens of a row of the table, at most kMaxKeys
-  int box;                 // keys of a TMA box of the window tiles
+  int box;                 // keys of a TMA box of the window tiles: 16, 32 or 64
   int splits;
   float* part_o;           // [splits, rows, Hq, 128] (splits > 1)
   float* part_lse;         // [splits, rows, Hq]

@@ -13,7 +13,7 @@
 //             them, P back over S's columns, at the end the gated output;
 //   16        issues the MMAs: S_A(j+1) right after O_A(j), so the softmax of
 //             one tile runs under the products of the other;
-//   17        loads by TMA, a box for each page's share of a tile;
+//   17        loads by TMA, in boxes that pages are multiples of;
 //   18, 19    what needs a thread's hand: V of tiles that some row does not
 //             see (keys that no row of the CTA sees become zeros, whatever the
 //             cache holds there), V of e4m3 caches from codes to f16 (exact).
@@ -80,11 +80,13 @@ struct TileShared {
   uint64_t kfull[3], kempty[3], vfull[2], vempty[2], vgo[2], rfull[2], rempty[2];
   uint64_t info[kSlots], s_full[2], p_ready[2], q_ready[2], o_full[2], loads_done;
   uint32_t tmem;
-  int poison_tile[kPoison];        // first key, or -1 from the first free entry on
+  int poison_tile[kPoison];        // its number times 128, or -1 from the first free entry on
   uint32_t poison[kPoison][4];     // keys with an odd V element
   uint32_t odd_keys[2][4];         // those of the tile that warp 18, 19 is at
   uint32_t valid[kSlots][4];       // keys on pages of the cache
   int check[kSlots];               // some key is not
+  int first[kSlots][2];            // first key of each half, -1: of two stretches of keys, or not all on pages
+  int ns, shift;                   // (of Tiles)
   alignas(16) uint32_t scale[kSlots][8];  // of each 16 keys, two bf16: ks, and log2 vs above it
   float qs[256];                   // per M row: what its scores are multiplied by (< 0: the row is a NaN)
   float pair[2][2][256];           // what a row's two threads tell each other
@@ -236,19 +238,20 @@ struct Int {
 };
 __device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
 
-// The key tiles of a CTA: those of the sinks, then those of the window.
+// The keys of a CTA, in boxes: those of the sinks, ns of them, then those of the
+// windows, `shift` on; n tiles of 128.
 struct Tiles {
-  int ns, w0, n;  // sink tiles, first window tile, all
-  __device__ __forceinline__ int first_key(int j) const { return (j < ns ? j : w0 + j - ns) * 128; }
+  int ns, shift, n;
+  __device__ __forceinline__ int key(int v) const { return v < ns ? v : v + shift; }
 };
 
-__device__ __noinline__ void file_poison(TileShared* sh, int kb, uint32_t* odd_keys, unsigned long long* err) {
+__device__ __noinline__ void file_poison(TileShared* sh, int v, uint32_t* odd_keys, unsigned long long* err) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) {
     int b = 0;
     for (; b < kPoison; ++b) {
-      const int was = atomicCAS(&sh->poison_tile[b], -1, kb);
-      if (was == -1 || was == kb) break;
+      const int was = atomicCAS(&sh->poison_tile[b], -1, v);
+      if (was == -1 || was == v) break;
     }
     if (b == kPoison) flag_error(err);
     for (int w = 0; w < 4; ++w) {
@@ -354,11 +357,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   Tiles T;
   {
     const int keys = min(pmax + 1, P.keys);  // (a position may lie past the table)
-    const int sinks = min(P.sinks, keys);
-    T.ns = (sinks + 127) >> 7;
-    T.w0 = max(T.ns, wlo >> 7);
-    const int end = P.window > 0 ? (keys + 127) >> 7 : 0;
-    T.n = pmax < 0 ? 0 : T.ns + max(0, end - T.w0);
+    const int sinks = (min(P.sinks, keys) + P.box - 1) & -P.box, w0 = wlo & -P.box;
+    const bool apart = P.window > 0 && w0 > sinks;
+    T.ns = apart ? sinks : 0;
+    T.shift = apart ? w0 - sinks : 0;
+    const int end = P.window > 0 ? keys - T.shift : sinks;
+    T.n = pmax < 0 ? 0 : (end + 127) >> 7;
   }
   const int per = P.splits > 1 ? (T.n + P.splits - 1) / P.splits : T.n;
   const int j0 = split * per, nt = max(0, min(T.n, j0 + per) - j0);
@@ -386,17 +390,16 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   auto seen = [&](int key) { return key <= pmax && (key >= wlo || key < P.sinks); };
   // every row of the CTA sees keys a .. b; none does any of them
   auto all_seen = [&](int a, int b) { return b <= pmin && (a >= wlo_all || b < P.sinks); };
-  auto none_seen = [&](int a, int b) { return a > pmax || (b < wlo && a >= P.sinks); };
   // some row of the CTA does not see all of tile j
   auto tile_masked = [&](int j) {
-    const int kb = T.first_key(j);
-    return !all_seen(kb, kb + 127);
+    const int v = 128 * j, n = min(max(T.ns - v, 0), 128);
+    return (n > 0 && !all_seen(v, v + n - 1)) || (n < 128 && !all_seen(v + n + T.shift, v + 127 + T.shift));
   };
   // Page id, then cache row, of the first key of 16-key block (lane & 7) of
   // tile j; kUnseen where there is nothing to see, kNoPage where the page is
   // none.
   constexpr uint32_t kUnseen = 0xFFFFFFFFu, kNoPage = 0xFFFFFFFEu;
-  auto block_key = [&](int j) { return T.first_key(j) + 16 * (lane & 7); };
+  auto block_key = [&](int j) { return T.key(128 * j + 16 * (lane & 7)); };
   auto fetch_page = [&](int j) -> int {
     const int k0 = block_key(j);
     if (!(k0 <= pmax && (k0 + 15 >= wlo || k0 < P.sinks))) return -1;
@@ -429,9 +432,15 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       const int ek = scale_exp(scales & 0xFF), ev = scale_exp(scales >> 8);
       sh.scale[slot][lane] = pack_bf16x2(exp2i(ek), static_cast<float>(ev));
     }
+    if (lane < 2) {
+      const int v = 128 * (j0 + i) + 64 * lane;
+      sh.first[slot][lane] = bad != 0u || (v < T.ns && v + 63 >= T.ns) ? -1 : T.key(v);
+    }
     if (lane == 0) {
       sh.check[slot] = bad != 0u;
       if (bad) flag_error(P.err);
+      sh.ns = T.ns;
+      sh.shift = T.shift;
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.info[slot]);
@@ -446,9 +455,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       // the tile (some is its lane's answer), the tile with its odd keys
       uint32_t* odd_keys = sh.odd_keys[warp & 1];
       auto remember = [&](int key) { atomicOr(&odd_keys[key >> 5], 1u << (key & 31)); };
-      auto file = [&](int kb, bool some) {
+      auto file = [&](int v, bool some) {
         if (!__any_sync(0xffffffffu, some)) return;
-        file_poison(&sh, kb, odd_keys, P.err);
+        file_poison(&sh, v, odd_keys, P.err);
       };
       auto announce = [&](uint64_t* bar) {
         fence_proxy_async_smem();
@@ -466,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       // found once (these two warps get few of their schedulers' slots).
       auto mask_tile = [&](int j, uint32_t r, auto stride, auto zero_key, auto check_key) {
         constexpr int S = decltype(stride)::value;
-        const int kb = T.first_key(j), k0 = lt / (64 / S);
+        const int v = 128 * j, k0 = lt / (64 / S);
         bool some = false;
         auto zero = [&](int from, int to) {
 #pragma unroll 1
@@ -483,25 +492,32 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         const unsigned there = __ballot_sync(0xffffffffu, r != kNoPage);
         if (there != 0xffffffffu) {  // blocks of 16 keys on no page: key by key
 #pragma unroll 1
-          for (int key = 0; key < 128; ++key) {
-            if (!((there >> (key >> 4)) & 1u) || !seen(kb + key))
-              zero(key, key + 1);
-            else if (!all_seen(kb + key, kb + key))
-              check(key, key + 1);
+          for (int i = 0; i < 128; ++i) {
+            const int key = T.key(v + i);
+            if (!((there >> (i >> 4)) & 1u) || !seen(key))
+              zero(i, i + 1);
+            else if (!all_seen(key, key))
+              check(i, i + 1);
           }
         } else {
-          // within the tile: the sinks end at s1; the windows begin at a0, all
-          // of them have begun at a1, the first row ends at b0, the last at b1
-          auto in = [&](int key) { return min(max(key - kb, 0), 128); };
-          const int s1 = in(P.sinks), a0 = max(in(wlo), s1), a1 = max(in(wlo_all), s1);
-          const int b0 = in(pmin + 1), b1 = in(pmax + 1);
-          zero(s1, min(a0, b1));
-          zero(b1, 128);
-          check(b0, min(s1, b1));                    // sinks that lie ahead of some row
-          check(a0, min(a1, b1));                    // keys that some window has left
-          check(max(max(a0, b0), min(a1, b1)), b1);  // keys ahead of some row
+          const int n = min(max(T.ns - v, 0), 128);  // (keys of the sinks)
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part) {
+            // within the tile: the sinks end at s1; the windows begin at a0, all
+            // of them have begun at a1, the first row ends at b0, the last at b1
+            const int lo = part == 0 ? 0 : n, hi = part == 0 ? n : 128, kb = part == 0 ? v : v + T.shift;
+            if (lo >= hi) continue;
+            auto in = [&](int key) { return min(max(key - kb, lo), hi); };
+            const int s1 = in(P.sinks), a0 = max(in(wlo), s1), a1 = max(in(wlo_all), s1);
+            const int b0 = in(pmin + 1), b1 = in(pmax + 1);
+            zero(s1, min(a0, b1));
+            zero(b1, hi);
+            check(b0, min(s1, b1));                    // sinks that lie ahead of some row
+            check(a0, min(a1, b1));                    // keys that some window has left
+            check(max(max(a0, b0), min(a1, b1)), b1);  // keys ahead of some row
+          }
         }
-        file(kb, some);
+        file(v, some);
       };
       if constexpr (KVT == 0) {
         // V of masked tiles as it has landed
@@ -671,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       int page_n = nt > 1 ? fetch_page(j0 + 1) : -1;
       uint32_t rows = to_row(j0, fetch_page(j0)), word = scale_word(rows);
       // The boxes of a tile that hold keys of the cache: a bit for each at its
-      // first 16-key block, whose lane has its cache row.
+      // first 16-key block, whose lane gets its cache row.
       auto find_boxes = [&](uint32_t r, int& y) {
         const unsigned there = __ballot_sync(0xffffffffu, r < kNoPage) & 0xFFu;
         const int per = P.box >> 4;  // blocks of a box
@@ -679,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         // (its first block may be one that nothing sees: count back)
         const int first = in != 0u ? __ffs(in) - 1 : 0;
         y = static_cast<int>(__shfl_sync(0xffffffffu, r, (lane & 7) + first)) - 16 * first;
-        return __ballot_sync(0xffffffffu, lane < 8 && lane % per == 0 && in != 0u);
+        return __ballot_sync(0xffffffffu, lane < 8 && (lane & (per - 1)) == 0 && in != 0u);
       };
       // them at columns x .. (atoms of 128 bytes) on `full` with `arrivals`
       // arrivals
@@ -804,13 +820,14 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     bool ok = true;
 #pragma unroll 1
     for (int j = 0; j < nt; ++j) {
-      const int kb = T.first_key(j0 + j) + 64 * hf, slot = j % kSlots;
+      const int slot = j % kSlots;
       // the tile's masks and scales, then its scores.  (A slot's next tile is
       // published only after both softmaxes are done with this one: its K
       // waits for a ring buffer that S of a later tile frees.)
       ok = all_ok(ok && mbar_wait(&sh.info[slot], (j / kSlots) & 1, P.err) && mbar_wait(&sh.s_full[x], j & 1, P.err));
       tc_fence_after_sync();
-      const bool plain = kb + 63 <= hi_all && (kb >= lo_all || kb + 63 < P.sinks) && sh.check[slot] == 0;
+      const int kb = sh.first[slot][hf];
+      const bool plain = kb >= 0 && kb + 63 <= hi_all && (kb >= lo_all || kb + 63 < P.sinks);
       uint32_t sc[4];  // (block scales)
       if constexpr (KVT == 2) {
         const uint4 a = *reinterpret_cast<const uint4*>(&sh.scale[slot][4 * hf]);
@@ -851,8 +868,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         if (!plain) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const int k0 = kb + 32 * c;
-            uint32_t vis = low_bits(p + 1 - k0) & (~low_bits(p - P.window + 1 - k0) | low_bits(P.sinks - k0));
+            auto sees_of = [&](int k0) {
+              return low_bits(p + 1 - k0) & (~low_bits(p - P.window + 1 - k0) | low_bits(P.sinks - k0));
+            };
+            const int v0 = 128 * (j0 + j) + 64 * hf + 32 * c;
+            const uint32_t first = low_bits(sh.ns - v0);
+            uint32_t vis = (sees_of(v0) & first) | (sees_of(v0 + sh.shift) & ~first);
             if (sh.check[slot] != 0) vis &= sh.valid[slot][2 * hf + c];
 #pragma unroll
             for (int i = 0; i < 32; ++i) r[c][i] = (vis & (1u << i)) != 0u ? r[c][i] : 0xFF800000u;
@@ -957,7 +978,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
 #pragma unroll 1
         for (int b = 0; b < kPoison * 128 && sh.poison_tile[b >> 7] >= 0; ++b) {
           if (!((sh.poison[b >> 7][(b >> 5) & 3] >> (b & 31)) & 1u)) continue;
-          const int key = sh.poison_tile[b >> 7] + (b & 127);
+          const int key = T.key(sh.poison_tile[b >> 7] + (b & 127));
           if (key > p || !(key > p - P.window || key < P.sinks)) continue;
           const int blk = page_of(P, key);
           const int pid = P.block_table[static_cast<long long>(req) * P.bt_stride + blk];
