@@ -276,17 +276,18 @@ __device__ __forceinline__ void scaled_run(const AppendParams& P, int i, int h, 
   }
 }
 
-// Queries alone, row by row.  Launched to run beside the K/V kernel, which it
-// needs nothing of; CTA 0 waits for that one's end, so that this kernel's end
-// is both's.
+// Queries alone, row by row.
 __global__ void __launch_bounds__(kThreads, 5) query_kernel(const AppendParams P) {
+  griddep_launch_dependents();
   query_rows(P, blockIdx.x, P.q_ctas);
-  if (blockIdx.x == 0) griddep_wait();
 }
 
 // CTAs [0, kv_ctas) write K and V: with block scales CTA (c, h) the runs of
 // KV head h that begin in rows [c * chunk, (c + 1) * chunk), otherwise CTA c
-// those rows.  The others prepare queries, a row each.
+// those rows.  The others prepare queries, a row each.  Where the queries have
+// a launch of their own (`beside`), this one runs beside it and needs nothing
+// of it; its last CTA waits for that one's end, so that this kernel's end is
+// both's.
 // NT: B / kHalves with block scales, 0 without.
 template <int NT>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams P) {
@@ -308,6 +309,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams P) 
     } else {
       for (int i = i0; i < i1; ++i) plain_kv_row(P, i);
     }
+    if (P.beside && blockIdx.x == gridDim.x - 1) griddep_wait();
     return;
   }
   query_rows(P, cta - P.kv_ctas, P.rows);
@@ -315,12 +317,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams P) 
 
 template <int NT>
 cudaError_t launch_nt(AppendParams p, cudaStream_t stream) {
-  // From 1024 rows on K and V have a launch of their own, a CTA for each block
-  // of rows and KV head, and the queries another of CTAs that run through many
-  // rows: the registers of the first kind would keep the second from having
-  // its loads in flight, and a CTA for each of 16 384 rows and heads takes
-  // longer to start than to run.  Below, where a launch weighs more, one
-  // launch of a CTA per row (and KV head).
+  // From 1024 rows on the queries have a launch of their own, three CTAs an SM
+  // that run through many rows, and K and V another that fills the rest of each
+  // SM, a CTA for each block of rows and KV head (16 384 rows, 32 q and 4 KV
+  // heads: 113 us, 5.2 TB/s; K and V first 129 us, four or five query CTAs an
+  // SM 113 and 126 us).  One kernel's registers would keep queries from having
+  // their loads in flight, and a CTA for each of 16 384 rows and heads takes
+  // longer to start than to run (250 us).  Below, where a launch weighs more,
+  // one launch of a CTA per row (and KV head).
   const bool many = p.rows >= 1024;
   p.chunk = NT > 0 && many ? kHalves * NT : 1;
   const int chunks = (p.rows + p.chunk - 1) / p.chunk;
@@ -328,11 +332,14 @@ cudaError_t launch_nt(AppendParams p, cudaStream_t stream) {
   p.q_ctas = p.q_out == nullptr ? 0 : p.rows;
   if (!many)
     return launch_kernel(append_kernel<NT>, dim3(p.kv_ctas + p.q_ctas), dim3(kThreads), 0, stream, false, p);
-  const cudaError_t e = launch_kernel(append_kernel<NT>, dim3(p.kv_ctas), dim3(kThreads), 0, stream, false, p);
-  if (e != cudaSuccess || p.q_ctas == 0) return e;
-  const int most = sm_count() * 5;
-  if (p.q_ctas > most) p.q_ctas = most;
-  return launch_kernel(query_kernel, dim3(p.q_ctas), dim3(kThreads), 0, stream, true, p);
+  p.beside = p.q_ctas != 0;
+  if (p.q_ctas != 0) {
+    const int most = sm_count() * 3;
+    if (p.q_ctas > most) p.q_ctas = most;
+    const cudaError_t e = launch_kernel(query_kernel, dim3(p.q_ctas), dim3(kThreads), 0, stream, false, p);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_kernel(append_kernel<NT>, dim3(p.kv_ctas), dim3(kThreads), 0, stream, p.beside != 0, p);
 }
 
 }  // namespace
