@@ -374,9 +374,8 @@ def _cache_fits(gcfg, kv):
         raise ValueError(f"kv has dtype {kv.dtype}, its configuration kv_dtype {gcfg.kv_dtype}")
 
 
-def _covers(t, need, name):
-    if t is not None and t.numel() < need:
-        raise ValueError(f"{name} has {t.numel()} entries, the call needs {need}")
+def _too_small(t, need, name):
+    raise ValueError(f"{name} has {t.numel()} entries, the call needs {need}")
 
 
 def _same_device(*tensors):
@@ -421,12 +420,15 @@ def kv_append(cfg, gcfg, m: QsaMainPrep, positions, cos_sin, scales: QsaKvScales
     _scales_fit(gcfg, scales)
     _cache_fits(gcfg, t["kv"])
     hq, hkv = gcfg.num_q_heads, gcfg.num_kv_heads
-    _covers(t["main_qkv"], rows * (hq + hkv) * 256, "main_qkv")
-    _covers(t["slot_mapping"], rows, "slot_mapping")
-    _covers(t.get("main_q_out"), rows * hq * 128, "main_q_out")
-    _covers(t.get("main_gate_out"), rows * hq * 128, "main_gate_out")
-    _covers(positions, rows * 3, "positions")
-    _covers(cos_sin, cfg.max_position * cfg.rotary_dim, "cos_sin")
+    for x, need, name in (
+            (t["main_qkv"], rows * (hq + hkv) * 256, "main_qkv"),
+            (t["slot_mapping"], rows, "slot_mapping"),
+            (t.get("main_q_out"), rows * hq * 128, "main_q_out"),
+            (t.get("main_gate_out"), rows * hq * 128, "main_gate_out"),
+            (positions, rows * 3, "positions"),
+            (cos_sin, cfg.max_position * cfg.rotary_dim, "cos_sin")):
+        if x is not None and x.numel() < need:
+            _too_small(x, need, name)
     dev = _same_device(positions, cos_sin, t["kv"], t["main_qkv"], t["slot_mapping"],
                        None if scales is None else scales._tensors)
     with _on(dev):
@@ -444,11 +446,10 @@ def sparse_gqa_scaled(gcfg, scales: QsaKvScales, q, kv, block_table, packed, tok
     _cache_fits(gcfg, kv)
     rows = q.shape[0]
     need = rows * gcfg.num_q_heads * 128
-    _covers(q, need, "q")
-    _covers(out, need, "out")
-    _covers(gate, need, "gate")
-    _covers(packed, rows * packed.shape[1], "packed")
-    _covers(token_to_req, rows, "token_to_req")
+    for x, n, name in ((q, need, "q"), (out, need, "out"), (gate, need, "gate"),
+                       (packed, rows * packed.shape[1], "packed"), (token_to_req, rows, "token_to_req")):
+        if x is not None and x.numel() < n:
+            _too_small(x, n, name)
     dev = _same_device(q, kv, scales._tensors, block_table, packed, token_to_req, gate, out, ws)
     with _on(dev):
         st = load().qsa_sparse_gqa_scaled(
@@ -501,7 +502,8 @@ def window_gqa(gcfg, args: QsaWindowArgs, ws=None, stream=None):
     (qsa_window_gqa); ws: uint8, window_workspace_bytes() long."""
     _scales_fit(gcfg, args._scales)
     _cache_fits(gcfg, args._tensors[1])
-    _covers(args._tensors[0], args.rows * gcfg.num_q_heads * 128, "q")
+    if args._tensors[0].numel() < args.rows * gcfg.num_q_heads * 128:
+        _too_small(args._tensors[0], args.rows * gcfg.num_q_heads * 128, "q")
     with _on(args._device):
         st = load().qsa_window_gqa(ctypes.byref(gcfg), ctypes.byref(args), _ptr(ws, torch.uint8),
                                    0 if ws is None else ws.numel(),
