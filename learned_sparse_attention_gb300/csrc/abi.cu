@@ -1,6 +1,7 @@
 // C ABI of the QSA layer step (declared in include/qsa.h): host-side
 // validation, workspace layout, TMA descriptor encoding and kernel launch
 // order.  Nothing here allocates device memory.
+#include <cmath>
 #include <mutex>
 
 #include "qsa.h"
@@ -668,17 +669,37 @@ long long window_tokens(const qsa_window_args* a) {
   return n < a->max_context ? n : a->max_context;
 }
 
-// Tiles or single rows, and how many splits of them.
+// Tiles or single rows, and how many splits of them: whichever the sizes make
+// the faster one, by estimates of their times in us.
+//   rows   6, + 48 (e4m3: 37) for each million of row tokens and KV heads, +
+//          2 for each further wave of two CTAs an SM, + 2 for a merge;
+//   tiles  for each wave of one CTA an SM 9 + 1.5 a tile of 128 keys, however
+//          many rows share it, + 6 for a merge.
+// Measured, both ways (tiles / rows, us): window 4096, 8 heads a KV head, 4 KV
+// heads, 64 requests of 1 row 115 / 48 (block scales), of 2 rows 108 / 107, of
+// 3 rows 110 / 157; 32 of 4 rows 56 / 109; one of 8 rows 19 / 16, of 24 rows
+// 25 / 25, of 48 rows 26 / 53; 16 of 8 rows and one head a KV head 36 / 104;
+// window 256, 4 of 16 rows 14 / 9, 64 of 4 rows 28 / 26.  Over 43 such sizes
+// the estimates' choice took 1.00 of the faster one's time on average, 1.07 at
+// worst.
 struct WindowPlan {
   bool tile;
   int splits;
 };
 WindowPlan window_plan(const qsa_gqa_cfg* g, const qsa_window_args* a) {
-  const int group = g->num_q_heads / g->num_kv_heads;
+  const int group = g->num_q_heads / g->num_kv_heads, sms = sm_count();
   const long long n = window_tokens(a);
-  if (static_cast<long long>(a->rows) * group >= 24ll * a->reqs)
-    return {true, window_tile_splits(a->rows, a->reqs, g->num_kv_heads, group, n, sm_count())};
-  return {false, row_gqa_splits(a->rows, g->num_kv_heads, n, g->kv_dtype, sm_count())};
+  auto waves = [](double ctas, int at_once) { return std::ceil(ctas / at_once); };
+  const int row_splits = row_gqa_splits(a->rows, g->num_kv_heads, n, g->kv_dtype, sms);
+  const double pairs = static_cast<double>(a->rows) * g->num_kv_heads;
+  const double row_us = 6.0 + pairs * n * (g->kv_dtype == QSA_DTYPE_BF16 ? 48e-6 : 37e-6) +
+                        2.0 * (waves(pairs * row_splits, 2 * sms) - 1.0) + (row_splits > 1 ? 2.0 : 0.0);
+  const int tile_splits = window_tile_splits(a->rows, a->reqs, g->num_kv_heads, group, n, sms);
+  const double ctas = static_cast<double>(window_tile_groups(a->rows, a->reqs, group)) * g->num_kv_heads * tile_splits;
+  const double tiles = std::ceil((n + 127) / 128.0 / tile_splits);
+  const double tile_us = waves(ctas, sms) * (9.0 + 1.5 * tiles) + (tile_splits > 1 ? 6.0 : 0.0);
+  if (tile_us < row_us) return {true, tile_splits};
+  return {false, row_splits};
 }
 
 qsa_status do_window(const qsa_gqa_cfg* g, const qsa_window_args* a, void* ws, size_t ws_bytes,

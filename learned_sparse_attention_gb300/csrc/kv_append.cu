@@ -21,6 +21,8 @@
 // (16 bytes a lane).  With block scales a CTA holds a run's keys and values
 // of one KV head in registers between the maximum and the rounding (2, 4 or 8
 // tokens a half-warp), so they are read once.
+// Measured, 32 query and 4 KV heads, blocks of 32: 16 384 rows with queries
+// 112 us (5.2 TB/s of reads and writes), 64 rows 3.7 us, 128 rows 5.5 us.
 #include "kv_scale.cuh"
 #include "qsa_device.cuh"
 #include "qsa_kernels.h"

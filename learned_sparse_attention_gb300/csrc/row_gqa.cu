@@ -28,6 +28,11 @@
 // give it 2 + 2: dims (K) and tokens (V) are taken in that order, by q's
 // fragments and by K's rows (tau, below).  Splits leave fp32 partials that a
 // second kernel joins in a fixed order.
+// Measured: 64 rows of 32 query and 4 KV heads over block scales, the last
+// 4100 tokens 47.8 us (5.7 TB/s; e4m3 decoded as two e4m3 terms 72 us), 2051
+// selected ones 34.3 us (4.0 TB/s; runs of 1 KB come at ~5.3 TB/s, the rest is
+// the chain of loads before the first copy and the last CTAs); 8 rows of 64
+// and 8 heads, 4103 selected tokens in 4 splits 19.2 us.
 #include "kv_scale.cuh"
 #include "qsa_device.cuh"
 #include "qsa_kernels.h"

@@ -93,6 +93,9 @@ class Batch:
         assert (out[self.n:] == 7.0).all()  # rows of no request
 
 
+# (In these tests ~1000 rows and more of a request are many enough for the
+# kernel of tiles, ~100 and fewer for that of single rows.)
+
 def sample_of(n, k=24, seed=0):
     if n <= k:
         return None
@@ -191,9 +194,10 @@ def test_window_decode(kind, window, sinks):
 
 @pytest.mark.parametrize("hq,hkv", [(1, 1), (3, 1), (10, 2), (12, 2), (14, 2), (16, 1), (40, 8)])
 @pytest.mark.parametrize("kind", ["bf16", "block"])
-def test_window_groups(hq, hkv, kind):
-    b = Batch([200, 65], [1, 60], hq=hq, hkv=hkv, kind=kind, page=48, seed=hq, pad=1)
-    b.check_window(b.window(50, 7), 50, 7)
+@pytest.mark.parametrize("rows", [60, 1060])
+def test_window_groups(hq, hkv, kind, rows):
+    b = Batch([200, rows + 5], [1, rows], hq=hq, hkv=hkv, kind=kind, page=48, seed=hq, pad=1)
+    b.check_window(b.window(50, 7), 50, 7, None if rows == 60 else sample_of(b.n))
     assert Q.check_errors() == 0
 
 
@@ -205,6 +209,8 @@ def test_window_groups(hq, hkv, kind):
     ([2000, 900], [64, 1], 700, 130),  # a chunk and a decode row
     ([333] * 9, [4] * 9, 100, 1),      # verify steps
     ([1100], [1030], 5000, 0),         # plain causal
+    ([2000, 900], [640, 1], 700, 130),
+    ([333] * 9, [120] * 9, 100, 1),
 ])
 def test_window_prefill(kind, page, block, contexts, rows, window, sinks):
     b = Batch(contexts, rows, hq=8, hkv=2, kind=kind, page=page, block=block, seed=page + window, pad=5, gate=page != 64)
@@ -213,18 +219,19 @@ def test_window_prefill(kind, page, block, contexts, rows, window, sinks):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "block"])
-def test_window_requests_without_rows(kind):
-    b = Batch([40, 30, 20, 10], [0, 20, 0, 10], kind=kind, seed=2)
-    b.check_window(b.window(16, 2), 16, 2)
+@pytest.mark.parametrize("contexts,rows", [([40, 30, 20, 10], [0, 20, 0, 10]), ([40, 900, 20, 700], [0, 800, 0, 700])])
+def test_window_requests_without_rows(kind, contexts, rows):
+    b = Batch(contexts, rows, kind=kind, seed=2)
+    b.check_window(b.window(16, 2), 16, 2, sample_of(b.n, 48))
     assert Q.check_errors() == 0
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "block"])
-@pytest.mark.parametrize("rows", [1, 3, 90])
+@pytest.mark.parametrize("rows", [1, 3, 90, 900])
 def test_window_unseen_pages_and_garbage(kind, rows):
     """Pages that slid out of every window are -1 in the table, tokens behind
     the last position and before the window hold NaN (bf16: infinities too)."""
-    b = Batch([1000, 501], [rows, rows], kind=kind, page=32, block=32, seed=rows, hq=4, hkv=1)
+    b = Batch([1000, 501] if rows < 500 else [1500, 1301], [rows, rows], kind=kind, page=32, block=32, seed=rows, hq=4, hkv=1)
     window, sinks = 150, 3
     bad = 0x7F if kind != "bf16" else float("nan")
     for r, c in enumerate(b.contexts):
@@ -240,11 +247,12 @@ def test_window_unseen_pages_and_garbage(kind, rows):
     assert Q.check_errors() == 0
 
 
-@pytest.mark.parametrize("rows", [1, 70])
+@pytest.mark.parametrize("rows", [1, 70, 1000])
 def test_window_poisoned_token_reaches_only_rows_that_see_it(rows):
-    b = Batch([400], [rows], kind="bf16", page=16, seed=5, hq=2, hkv=1, gate=False)
+    context = 400 if rows < 300 else 1400
+    b = Batch([context], [rows], kind="bf16", page=16, seed=5, hq=2, hkv=1, gate=False)
     window = 40
-    tok = 400 - rows - window + 10 if rows > 1 else 400 - window - 2   # leaves the window during the call, or just has
+    tok = context - rows - window + 10 if rows > 1 else context - window - 2   # leaves the window during the call, or just has
     blk, off = b.table[0, tok // 16], tok % 16
     b.kv[blk, 0, off, D + 5] = float("inf")
     b.kv[blk, 0, off, D + 9] = float("nan")
@@ -262,9 +270,9 @@ def test_window_poisoned_token_reaches_only_rows_that_see_it(rows):
             assert_row(out[i], f64(b.q[i]), K, V, None, f"row {i}")
 
 
-@pytest.mark.parametrize("rows", [1, 70])
+@pytest.mark.parametrize("rows", [1, 70, 1000])
 def test_window_bad_page_is_left_out_and_counted(rows):
-    b = Batch([300], [rows], kind="bf16", page=16, seed=6, hq=2, hkv=1, gate=False)
+    b = Batch([300 if rows < 300 else 1200], [rows], kind="bf16", page=16, seed=6, hq=2, hkv=1, gate=False)
     b.table[0, 16] = b.blocks + 5    # tokens 256 .. 271
     out = b.window(64, 0)
     assert Q.check_errors() > 0
@@ -275,13 +283,14 @@ def test_window_bad_page_is_left_out_and_counted(rows):
         assert_row(out[i], f64(b.q[i]), K, V, None, f"row {i}")
 
 
-def test_window_rows_before_the_start():
+@pytest.mark.parametrize("rows", [40, 1000])
+def test_window_rows_before_the_start(rows):
     """A negative position sees nothing."""
-    b = Batch([20, 20], [2, 40], kind="bf16", seed=7)
-    b.pos[2:] = np.arange(-20, 20)
+    b = Batch([20, rows // 2], [2, rows], kind="bf16", seed=7)
+    b.pos[2:] = np.arange(-(rows // 2), rows // 2)
     out = b.window(8, 1)
-    assert (out[2:22] == 0).all()
-    b.check_window(out, 8, 1)
+    assert (out[2:2 + rows // 2] == 0).all()
+    b.check_window(out, 8, 1, None if rows == 40 else sample_of(b.n, 100))
 
 
 @pytest.mark.parametrize("kind", ["bf16", "block"])
@@ -295,19 +304,20 @@ def test_window_long_rows_are_split(kind, contexts, rows):
     assert Q.check_errors() == 0
 
 
-def test_window_strong_scores():
+@pytest.mark.parametrize("rows", [100, 800])
+def test_window_strong_scores(rows):
     """Scores that rise and fall along the row move the running maximum."""
-    b = Batch([900], [100], kind="bf16", page=64, seed=9, hq=8, hkv=1, spread=8.0)
+    b = Batch([900], [rows], kind="bf16", page=64, seed=9, hq=8, hkv=1, spread=8.0)
     ramp = torch.linspace(0.1, 6.0, 64).bfloat16()
     b.kv[..., :D] *= ramp[:, None]
-    b.check_window(b.window(600, 4), 600, 4, sample_of(100))
+    b.check_window(b.window(600, 4), 600, 4, sample_of(rows, 48))
 
 
 def test_window_captured_and_on_two_streams():
     """Two graphs that share one workspace, replayed in order, and a call on
     another stream."""
     b = Batch([3000, 2500], [1, 1], kind="block", page=64, block=32, seed=10, hq=8, hkv=1)
-    c = Batch([600], [200], kind="block", page=64, block=32, seed=11, hq=8, hkv=1)
+    c = Batch([1600], [1200], kind="block", page=64, block=32, seed=11, hq=8, hkv=1)
     out_b, out_c = b.window(2048, 4), c.window(256, 4)
     sizes, calls = [], []
     for x, w in ((b, 2048), (c, 256)):
@@ -337,30 +347,32 @@ def test_window_captured_and_on_two_streams():
 
 
 @pytest.mark.parametrize("kind", ["bf16", "block"])
-@pytest.mark.parametrize("rows", [1, 70])
+@pytest.mark.parametrize("rows", [1, 70, 1000])
 def test_window_positions_past_the_table(kind, rows):
     """Only the table's tokens are looked at, however far a position is."""
     b = Batch([320], [rows], kind=kind, page=32, seed=13, hq=2, hkv=1, gate=False)
     b.pos[:] = 2 ** 31 - 1 - np.arange(rows)[::-1]
     out = b.window(2 ** 31 - 1, 2 ** 31 - 1)
     assert Q.check_errors() > 0
-    for i in range(rows):
+    some = sample_of(rows) or range(rows)
+    for i in some:
         K, V = b.values(0, np.arange(320))
         assert_row(out[i], f64(b.q[i]), K, V, None, f"row {i}")
     assert (b.window(1000, 0) == 0).all()
     assert Q.check_errors() > 0
     out = b.window(0, 40)
     assert Q.check_errors() == 0
-    for i in range(rows):
+    for i in some:
         K, V = b.values(0, np.arange(40))
         assert_row(out[i], f64(b.q[i]), K, V, None, f"row {i}")
 
 
 @pytest.mark.parametrize("kind", ["bf16", "block"])
-def test_window_odd_values_beside_rows_before_the_start(kind):
+@pytest.mark.parametrize("rows", [40, 140])
+def test_window_odd_values_beside_rows_before_the_start(kind, rows):
     """Values that are not finite in many tiles reach every row that sees them
     and no row at a negative position."""
-    b = Batch([6000], [40], kind=kind, page=32, block=32, seed=14, hq=8, hkv=1, gate=False)
+    b = Batch([6000], [rows], kind=kind, page=32, block=32, seed=14, hq=8, hkv=1, gate=False)
     b.pos[5:20] = -np.arange(1, 16)
     odd = np.arange(0, 6000, 130)
     b.kv[torch.from_numpy(b.table[0, odd // 32].astype(np.int64)), 0, torch.from_numpy(odd % 32), D + 5] = \
@@ -368,21 +380,22 @@ def test_window_odd_values_beside_rows_before_the_start(kind):
     out = b.window(100000, 0)
     assert Q.check_errors() == 0
     assert (out[5:20] == 0).all()
-    rest = np.r_[0:5, 20:40]
+    rest = np.r_[0:5, 20:rows]
     assert np.isnan(out[rest][:, :, 5]).all()
     clean = np.arange(D) != 5
     b.kv[torch.from_numpy(b.table[0, odd // 32].astype(np.int64)), 0, torch.from_numpy(odd % 32), D + 5] = 0
-    for i in (0, 4, 20, 39):
+    for i in (0, 4, 20, rows - 1):
         K, V = b.values(0, O.window_tokens(int(b.pos[i]), 100000, 0))
         out[i][:, ~clean] = attend_row(f64(b.q[i]), K, V)[0][:, ~clean]
         assert_row(out[i], f64(b.q[i]), K, V, None, f"row {i}")
 
 
 @pytest.mark.parametrize("kind", ["e4m3", "block"])
-@pytest.mark.parametrize("page", [16, 64])
-def test_window_nan_codes_reach_only_rows_that_see_them(kind, page):
-    b = Batch([400], [70], kind=kind, page=page, block=16, seed=15, hq=2, hkv=1, gate=False)
-    toks = [345, 371, 399]   # left by the window, ahead of some rows, the last one's own
+@pytest.mark.parametrize("page,rows", [(16, 70), (16, 1000), (64, 1000)])
+def test_window_nan_codes_reach_only_rows_that_see_them(kind, page, rows):
+    context = 400 if rows < 300 else 1400
+    b = Batch([context], [rows], kind=kind, page=page, block=16, seed=15, hq=2, hkv=1, gate=False)
+    toks = [context - 55, context - 29, context - 1]   # left by the window, ahead of some rows, the last one's own
     for tok in toks:
         b.kv[b.table[0, tok // page], 0, tok % page, D + 9] = 0xFF
     out = b.window(40, 0)
@@ -394,10 +407,10 @@ def test_window_nan_codes_reach_only_rows_that_see_them(kind, page):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "block"])
-@pytest.mark.parametrize("rows", [1, 60])
+@pytest.mark.parametrize("rows", [1, 1000])
 def test_window_far_into_a_large_cache(kind, rows):
     """Pages whose bytes lie past 2^32."""
-    b = Batch([300], [rows], kind=kind, page=64, block=64, seed=16, hq=4, hkv=1)
+    b = Batch([1300], [rows], kind=kind, page=64, block=64, seed=16, hq=4, hkv=1)
     row_bytes = 512 if kind == "bf16" else 256
     ahead = 2 ** 32 // (64 * row_bytes) + 1
     out_near = b.window(120, 3)
@@ -467,7 +480,7 @@ def test_sparse_captured_and_replayed():
 
 # ------------------------------------------------------------------ together
 
-@pytest.mark.parametrize("rows", [[1, 1, 1], [5, 130, 1]])
+@pytest.mark.parametrize("rows", [[1, 1, 1], [5, 130, 1], [5, 400, 1]])
 def test_append_then_both_attentions(rows):
     """A step as a model runs it: keys and values into the cache with block
     scales, then the sparse layer's and the window layer's attention of the
