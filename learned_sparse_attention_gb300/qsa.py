@@ -261,7 +261,17 @@ def main_prep(t: dict, eps: float = 1e-6) -> QsaMainPrep:
     m.kv = _ptr(t["kv"], _IDX)
     m.slot_mapping = _ptr(t["slot_mapping"], torch.int64, "slot_mapping")
     m._tensors = dict(t)
+    m._entries = _main_entries(t)
     return m
+
+
+def _main_entries(t):
+    """What kv_append asks of main_prep's tensors at every call: their device
+    and numbers of entries."""
+    names = ("main_qkv", "slot_mapping", "main_q_out", "main_gate_out", "kv")
+    n = [1 << 62 if t.get(k) is None else t[k].numel() for k in names]
+    dev = {t[k].get_device() for k in names if t.get(k) is not None}
+    return (dev.pop() if len(dev) == 1 else None, *n)
 
 
 def main_prepare(cfg, gcfg, m: QsaMainPrep, positions, cos_sin, stream=None):
@@ -356,28 +366,6 @@ def kv_scales(scales, scale_block: int) -> QsaKvScales:
     return s
 
 
-def _scales_fit(gcfg, scales):
-    """A scales tensor that is smaller than the cache's would be read past its end."""
-    if scales is None or scales.scale_block <= 0:
-        return
-    need = gcfg.num_blocks * gcfg.num_kv_heads * (gcfg.page_size // scales.scale_block) * 2
-    if scales._tensors.numel() < need:
-        raise ValueError(f"scales has {scales._tensors.numel()} entries, the cache needs {need}")
-
-
-def _cache_fits(gcfg, kv):
-    """Likewise the cache itself, and a cache of the other element type."""
-    need = gcfg.num_blocks * gcfg.num_kv_heads * gcfg.page_size * 256
-    if kv.numel() < need:
-        raise ValueError(f"kv has {kv.numel()} entries, its configuration needs {need}")
-    if (kv.dtype == torch.bfloat16) != (gcfg.kv_dtype == DTYPE_BF16):
-        raise ValueError(f"kv has dtype {kv.dtype}, its configuration kv_dtype {gcfg.kv_dtype}")
-
-
-def _too_small(t, need, name):
-    raise ValueError(f"{name} has {t.numel()} entries, the call needs {need}")
-
-
 def _same_device(*tensors):
     """The device all tensors are on (None ones left out)."""
     dev = None
@@ -393,72 +381,100 @@ def _same_device(*tensors):
     return dev
 
 
-def _on(device):
+def _refuse(t, dtype, need, name, dev):
+    if t.numel() < need:
+        raise ValueError(f"{name} has {t.numel()} entries, the call needs {need}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, the call takes {dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"tensors on different devices: {name} is on {t.device}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _pointers(dev, specs):
+    """The addresses of (tensor or None, dtype, least entries, name) on device
+    dev.  (One pass, few calls: the small operators take as long as the checks.)"""
+    out = []
+    for t, dtype, need, name in specs:
+        if t is None:
+            out.append(None)
+            continue
+        if t.numel() < need or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+            _refuse(t, dtype, need, name, dev)
+        out.append(t.data_ptr())
+    if dev < 0:
+        raise ValueError("the tensors must be CUDA tensors")
+    return out
+
+
+def _cache_specs(gcfg, scales, kv):
+    """The cache and its scales, which smaller tensors would be read past the end of."""
+    blocks = gcfg.num_blocks * gcfg.num_kv_heads
+    page = gcfg.page_size
+    sc = (None, None, 0, None)
+    if scales is not None and scales.scale_block > 0:
+        sc = (scales._tensors, torch.uint8, blocks * (page // scales.scale_block) * 2, "scales")
+    return ((kv, torch.bfloat16 if gcfg.kv_dtype == DTYPE_BF16 else torch.uint8, blocks * page * 256, "kv"), sc)
+
+
+def _on(index):
     """Makes the tensors' device current for a call; nothing to do where it is."""
-    if device.type != "cuda" or device.index == torch._C._cuda_getDevice():
-        return _HERE
-    return torch.cuda.device(device)
+    return _HERE if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
 
 
 _HERE = contextlib.nullcontext()
 
 
-def _raw_stream(device, stream=None):
+def _raw_stream(index, stream=None):
     """The given stream's handle, or that of the device's current stream
     (without the Stream object that torch.cuda.current_stream() makes: a few
     microseconds, as much as the small calls take)."""
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def kv_append(cfg, gcfg, m: QsaMainPrep, positions, cos_sin, scales: QsaKvScales | None = None,
               stream=None):
     """Keys and values into the paged cache, normalised and rotated on the way,
     with q and gate beside them where `m` has them (qsa_kv_append)."""
-    t, rows = m._tensors, positions.shape[0]
-    _scales_fit(gcfg, scales)
-    _cache_fits(gcfg, t["kv"])
+    t, rows, dev = m._tensors, positions.size(0), positions.get_device()
     hq, hkv = gcfg.num_q_heads, gcfg.num_kv_heads
-    for x, need, name in (
-            (t["main_qkv"], rows * (hq + hkv) * 256, "main_qkv"),
-            (t["slot_mapping"], rows, "slot_mapping"),
-            (t.get("main_q_out"), rows * hq * 128, "main_q_out"),
-            (t.get("main_gate_out"), rows * hq * 128, "main_gate_out"),
-            (positions, rows * 3, "positions"),
-            (cos_sin, cfg.max_position * cfg.rotary_dim, "cos_sin")):
-        if x is not None and x.numel() < need:
-            _too_small(x, need, name)
-    dev = _same_device(positions, cos_sin, t["kv"], t["main_qkv"], t["slot_mapping"],
-                       None if scales is None else scales._tensors)
+    specs = ((positions, torch.int64, rows * 3, "positions"),
+             (cos_sin, torch.float32, cfg.max_position * cfg.rotary_dim, "cos_sin"))
+    cache, sc = _cache_specs(gcfg, scales, t["kv"])
+    at, qkv, slots, q, gate, kv = m._entries
+    if (at != dev or qkv < rows * (hq + hkv) * 256 or slots < rows or q < rows * hq * 128 or
+            gate < rows * hq * 128 or kv < cache[2] or t["kv"].dtype is not cache[1]):
+        bf16 = torch.bfloat16  # (which of them)
+        specs += ((t["main_qkv"], bf16, rows * (hq + hkv) * 256, "main_qkv"),
+                  (t["slot_mapping"], torch.int64, rows, "slot_mapping"),
+                  (t.get("main_q_out"), bf16, rows * hq * 128, "main_q_out"),
+                  (t.get("main_gate_out"), bf16, rows * hq * 128, "main_gate_out"), cache)
+    ptrs = _pointers(dev, (*specs, sc))
     with _on(dev):
         st = load().qsa_kv_append(
             ctypes.byref(cfg), ctypes.byref(gcfg), ctypes.byref(m),
-            None if scales is None else ctypes.byref(scales), _ptr(positions, torch.int64),
-            _ptr(cos_sin, torch.float32), rows, _raw_stream(dev, stream))
+            None if scales is None else ctypes.byref(scales), ptrs[0], ptrs[1], rows,
+            _raw_stream(dev, stream))
     _check("qsa_kv_append", st)
 
 
 def sparse_gqa_scaled(gcfg, scales: QsaKvScales, q, kv, block_table, packed, token_to_req, gate,
                       out, ws, stream=None):
     """Stage 4 over a cache with block scales (qsa_sparse_gqa_scaled)."""
-    _scales_fit(gcfg, scales)
-    _cache_fits(gcfg, kv)
-    rows = q.shape[0]
+    rows, dev = q.size(0), q.get_device()
+    reqs, width = block_table.size(0), packed.size(1)
     need = rows * gcfg.num_q_heads * 128
-    for x, n, name in ((q, need, "q"), (out, need, "out"), (gate, need, "gate"),
-                       (packed, rows * packed.shape[1], "packed"), (token_to_req, rows, "token_to_req")):
-        if x is not None and x.numel() < n:
-            _too_small(x, n, name)
-    dev = _same_device(q, kv, scales._tensors, block_table, packed, token_to_req, gate, out, ws)
+    bf16, i32 = torch.bfloat16, torch.int32
+    p = _pointers(dev, (
+        (q, bf16, need, "q"), (block_table, i32, 0, "block_table"), (packed, i32, rows * width, "packed"),
+        (token_to_req, i32, rows, "token_to_req"), (gate, bf16, need, "gate"), (out, bf16, need, "out"),
+        (ws, torch.uint8, 0, "ws"), *_cache_specs(gcfg, scales, kv)))
     with _on(dev):
         st = load().qsa_sparse_gqa_scaled(
-            ctypes.byref(gcfg), ctypes.byref(scales), _ptr(q, torch.bfloat16),
-            _ptr(kv, torch.uint8), _ptr(block_table, torch.int32), block_table.shape[1],
-            _ptr(packed, torch.int32), packed.shape[1], _ptr(token_to_req, torch.int32),
-            _ptr(gate, torch.bfloat16), _ptr(out, torch.bfloat16), rows,
-            block_table.shape[0], _ptr(ws, torch.uint8), 0 if ws is None else ws.numel(),
-            _raw_stream(dev, stream))
+            ctypes.byref(gcfg), None if scales is None else ctypes.byref(scales), p[0], p[7], p[1], block_table.size(1), p[2], width,
+            p[3], p[4], p[5], rows, reqs, p[6], 0 if ws is None else ws.numel(), _raw_stream(dev, stream))
     _check("qsa_sparse_gqa_scaled", st)
 
 
@@ -468,8 +484,8 @@ def window_args(q, kv, block_table, token_to_req, query_start_loc, logical_posit
     and its table, the rows' requests and positions, the window and the number
     of first tokens that stay visible."""
     a = QsaWindowArgs()
-    a._device = _same_device(q, kv, block_table, token_to_req, query_start_loc, logical_positions,
-                             out, gate, None if scales is None else scales._tensors)
+    _same_device(q, kv, block_table, token_to_req, query_start_loc, logical_positions, out, gate,
+                 None if scales is None else scales._tensors)
     a.rows, a.reqs = q.shape[0], query_start_loc.shape[0] - 1
     if out.shape != q.shape or (gate is not None and gate.shape != q.shape):
         raise ValueError("out and gate must have q's shape")
@@ -500,14 +516,13 @@ def window_workspace_bytes(gcfg, args: QsaWindowArgs) -> int:
 def window_gqa(gcfg, args: QsaWindowArgs, ws=None, stream=None):
     """Attention over the last `window` tokens and the first `sinks`
     (qsa_window_gqa); ws: uint8, window_workspace_bytes() long."""
-    _scales_fit(gcfg, args._scales)
-    _cache_fits(gcfg, args._tensors[1])
-    if args._tensors[0].numel() < args.rows * gcfg.num_q_heads * 128:
-        _too_small(args._tensors[0], args.rows * gcfg.num_q_heads * 128, "q")
-    with _on(args._device):
-        st = load().qsa_window_gqa(ctypes.byref(gcfg), ctypes.byref(args), _ptr(ws, torch.uint8),
-                                   0 if ws is None else ws.numel(),
-                                   _raw_stream(args._device, stream))
+    q, kv = args._tensors[0], args._tensors[1]
+    dev = q.get_device()
+    p = _pointers(dev, ((q, torch.bfloat16, args.rows * gcfg.num_q_heads * 128, "q"), (ws, torch.uint8, 0, "ws"),
+                        *_cache_specs(gcfg, args._scales, kv)))
+    with _on(dev):
+        st = load().qsa_window_gqa(ctypes.byref(gcfg), ctypes.byref(args), p[1], 0 if ws is None else ws.numel(),
+                                   _raw_stream(dev, stream))
     _check("qsa_window_gqa", st)
 
 

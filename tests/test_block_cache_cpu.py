@@ -181,8 +181,9 @@ def test_binding_refuses_host_tensors_and_small_scales(lib):
         Q.kv_scales(torch.zeros(8, dtype=torch.uint8), 16)
     s = _scales(block=32)
     s._tensors = torch.zeros(39, dtype=torch.uint8)
-    with pytest.raises(ValueError):
-        Q._scales_fit(_gcfg(), s)       # 10 blocks x 2 heads x 2 scale blocks x 2 = 80
+    kv = torch.zeros((10, 2, 64, 256), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="scales"):
+        Q._pointers(-1, Q._cache_specs(_gcfg(), s, kv))       # 10 blocks x 2 heads x 2 scale blocks x 2 = 80
 
 
 def test_binding_refuses_tensors_that_are_too_small():
@@ -201,7 +202,7 @@ def test_binding_refuses_tensors_that_are_too_small():
         pos, cs = kw.pop("positions", torch.zeros((4, 1, 3), dtype=torch.int64)), kw.pop("cos_sin", torch.zeros(10, 64))
         t.update(kw)
         m = Q.QsaMainPrep()
-        m._tensors = t
+        m._tensors, m._entries = t, Q._main_entries(t)
         Q.kv_append(cfg, g, m, pos, cs, scales=sc)
 
     for name, small in dict(main_qkv=bf(3, 6 * 128), main_q_out=bf(3, 2, 128), main_gate_out=bf(4, 1, 128), kv=kv[:2],
