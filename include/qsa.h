@@ -474,6 +474,10 @@ qsa_status qsa_sparse_gqa_scaled(const qsa_gqa_cfg* gcfg, const qsa_kv_scales* s
  *                 sees may be stale or -1, and tokens that no row sees may
  *                 hold anything.  A visible token past the table or on a
  *                 page outside the cache is left out of the sum and counted
+ *                 (and a value that is not finite reaches the rows that see
+ *                 it; if among 256 (row, head) pairs of a request more than 32
+ *                 stretches of 128 tokens that only some of them see hold such
+ *                 values, the others are left out and counted)
  *  ws             qsa_window_workspace_bytes() bytes, 256-byte aligned (NULL
  *                 where that is 0); its contents need not be kept or cleared
  */
