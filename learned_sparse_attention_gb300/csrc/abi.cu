@@ -674,13 +674,14 @@ long long window_tokens(const qsa_window_args* a) {
 //   rows   6, + 48 (e4m3: 37) for each million of row tokens and KV heads, +
 //          2 for each further wave of two CTAs an SM, + 2 for a merge;
 //   tiles  for each wave of one CTA an SM 9 + 1.5 a tile of 128 keys, however
-//          many rows share it, + 6 for a merge.
+//          many rows share it (e4m3 where a request's rows fit one row tile:
+//          1.1), + 6 for a merge.
 // Measured, both ways (tiles / rows, us): window 4096, 8 heads a KV head, 4 KV
-// heads, 64 requests of 1 row 115 / 48 (block scales), of 2 rows 108 / 107, of
-// 3 rows 110 / 157; 32 of 4 rows 56 / 109; one of 8 rows 19 / 16, of 24 rows
+// heads, 64 requests of 1 row 89 / 48 and of 3 rows 91 / 130 (block scales), of
+// 2 rows 108 / 107 and of 3 rows 110 / 157 (bf16); 32 of 4 rows 56 / 109; one of 8 rows 19 / 16, of 24 rows
 // 25 / 25, of 48 rows 26 / 53; 16 of 8 rows and one head a KV head 36 / 104;
-// window 256, 4 of 16 rows 14 / 9, 64 of 4 rows 28 / 26.  Over 43 such sizes
-// the estimates' choice took 1.00 of the faster one's time on average, 1.07 at
+// window 256, 4 of 16 rows 14 / 9, 64 of 4 rows 28 / 26.  Over 53 such sizes
+// the estimates' choice took 1.00 of the faster one's time on average, 1.09 at
 // worst.
 struct WindowPlan {
   bool tile;
@@ -697,7 +698,9 @@ WindowPlan window_plan(const qsa_gqa_cfg* g, const qsa_window_args* a) {
   const int tile_splits = window_tile_splits(a->rows, a->reqs, g->num_kv_heads, group, n, sms);
   const double ctas = static_cast<double>(window_tile_groups(a->rows, a->reqs, group)) * g->num_kv_heads * tile_splits;
   const double tiles = std::ceil((n + 127) / 128.0 / tile_splits);
-  const double tile_us = waves(ctas, sms) * (9.0 + 1.5 * tiles) + (tile_splits > 1 ? 6.0 : 0.0);
+  const bool one = static_cast<long long>(a->rows) * group <= 128ll * a->reqs;  // (about)
+  const double per_tile = one && g->kv_dtype != QSA_DTYPE_BF16 ? 1.1 : 1.5;
+  const double tile_us = waves(ctas, sms) * (9.0 + per_tile * tiles) + (tile_splits > 1 ? 6.0 : 0.0);
   if (tile_us < row_us) return {true, tile_splits};
   return {false, row_splits};
 }

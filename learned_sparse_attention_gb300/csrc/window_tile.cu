@@ -4,9 +4,10 @@
 // Mathematics.  As in row_gqa.cu; here 128 (row, head) pairs of one request
 // and KV head are the M rows of S = Q K^T and O += P V, R = 128 / G rows with
 // their G heads, and a CTA runs two such tiles, A and B (rows r0 .. r0 + R - 1
-// and the R after them), over one stream of 128-key tiles.  Two threads share
-// an M row, 64 keys each; both keep the row's reference and a sum of their
-// own weights in registers.
+// and the R after them), over one stream of 128-key tiles.  Where the rows fit
+// tile A, B takes the same rows over every other key tile (e4m3 caches), and
+// A's warps join the two at the end.  Two threads share an M row, 64 keys each;
+// both keep the row's reference and a sum of their own weights in registers.
 //
 // Roles, 20 warps:
 //   0-7, 8-15 softmax of tile A, B: S from TMEM, masks on the tiles that need
@@ -41,8 +42,8 @@
 // groups and 128 keys), fixed costs for short windows (~10 000 cycles to the
 // first S, ~8 000 from the last weights to the end).  Measured, 32 query and 4
 // KV heads, window 4096, 4 sinks: 16 384 rows 804 us (1.37 PFLOP/s), 8192 rows
-// 407 us on bf16 and 443 us with block scales; 32 requests of 4 rows 56 us
-// (4.9 TB/s); 3 requests of ~1000 to 2011 rows, 24 query heads, window 1000:
+// 406 us on bf16 and 434 us with block scales; 32 requests of 4 rows 56 us on
+// bf16 (4.9 TB/s) and 47 us with block scales; 3 requests of ~1000 to 2011 rows, 24 query heads, window 1000:
 // 106 us.
 // Without the softmax the loads and products alone took 374 us for the 8192
 // rows.
@@ -64,7 +65,7 @@ constexpr int kSoftWarps = 16;
 constexpr int kThreads = (kSoftWarps + 4) * 32;
 constexpr int kTile = 128 * 256;  // bytes of 128 rows of 128 16-bit values, two 64-dim atoms
 constexpr int kAtom = 128 * 128;
-constexpr int kSlots = 4;        // tiles whose scales and page masks are kept
+constexpr int kSlots = 8;        // tiles whose scales and page masks are kept
 constexpr int kPoison = 32;      // tiles that can remember odd V elements
 // A row's reference is moved when a weight has grown by 2^8 (bf16) or 2^10.
 // bf16 weights: it is set so that the largest is 2^-7; that one has reached 2
@@ -85,7 +86,7 @@ struct Rings {
   static constexpr int NK = KVT == 0 ? 2 : 3, NV = 2, NR = KVT == 0 ? 0 : 2;
   static constexpr int kKey = KVT == 0 ? kTile : kAtom;
   static constexpr int kBytes = NK * kKey + NV * kTile + NR * kAtom;
-  static_assert(kSlots > NK, "a slot is rewritten only after its tile's softmax");
+  static_assert(kSlots > NK + 2, "a slot is rewritten only after its tile's softmax");
 };
 
 struct TileShared {
@@ -102,6 +103,7 @@ struct TileShared {
   alignas(16) uint32_t scale[kSlots][8];  // of each 16 keys, two bf16: ks, and log2 vs above it
   float qs[256];                   // per M row: what its scores are multiplied by (< 0: the row is a NaN)
   float pair[2][2][256];           // what a row's two threads tell each other
+  float join[2][128];              // tile B's sums and references, where it has the same rows as A
 };
 template <int KVT>
 constexpr int kSmem = 1024 + 2 * kTile + Rings<KVT>::kBytes + static_cast<int>(sizeof(TileShared));
@@ -339,12 +341,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   // ---- positions of the CTA's rows, and behind them the Q rows on their way:
   // sixteen M rows a warp, a half-warp per row
   const int own_pos = tid < nrows ? window_position(P, row0 + tid) : -1;
+  const bool two = nrows > R;  // tile B has rows of its own
   uint4 qv[8];
   if (warp < kSoftWarps) {
     const int im0 = 32 * (warp & 3) + 16 * ((warp >> 2) & 1) + (lane >> 4);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const int im = im0 + 2 * u, r = (warp >> 3) * R + row_of(im);
+      const int im = im0 + 2 * u, r = (two ? warp >> 3 : 0) * R + row_of(im);
       qv[u] = make_uint4(0u, 0u, 0u, 0u);
       if (im < R * G && r < nrows)
         qv[u] = *reinterpret_cast<const uint4*>(P.q + (static_cast<long long>(row0 + r) * P.hq + kvh * G + head_of(im)) * 128 + 8 * (lane & 15));
@@ -378,7 +381,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
   }
   const int per = P.splits > 1 ? (T.n + P.splits - 1) / P.splits : T.n;
   const int j0 = split * per, nt = max(0, min(T.n, j0 + per) - j0);
-  const bool two = nrows > R;
+  // Tile B without rows of its own takes every other key tile of A's: on e4m3
+  // caches, whose bytes do not bound it (32 requests of 4 rows, 4100 tokens:
+  // block scales 63 -> 51 us, bf16 58 -> 60 us).
+  const bool duo = KVT != 0 && !two && nt > 1;
 
   if (pmax >= P.keys && tid == 0 && (P.window > 0 || P.sinks > P.keys)) flag_error(P.err);
   if (nt == 0) {  // nothing to see here: zeros, or an empty split
@@ -643,12 +649,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       // O += P V of tile number i
       auto values = [&](int x, int i) {
         const uint32_t b = v0 + (((i % RG::NV) * kTile) >> 4);
-        if (!all_ok(mbar_wait(&sh.p_ready[x], i & 1, P.err))) return false;
+        const int own = duo ? i >> 1 : i;  // (of tile x)
+        if (!all_ok(mbar_wait(&sh.p_ready[x], own & 1, P.err))) return false;
         tc_fence_after_sync();
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * kk, b + ((kk * 2048) >> 4), id_o,
-                 i == 0 && kk == 0 ? 0u : 1u);
+                 own == 0 && kk == 0 ? 0u : 1u);
         return true;
       };
       auto wait_k = [&](int i) {
@@ -656,27 +663,40 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         tc_fence_after_sync();
         return ok;
       };
-      bool ok = all_ok(mbar_wait(&sh.q_ready[0], 0, P.err)) && wait_k(0);
+      auto start = [&](int x, int i) {
+        scores(x, i);
+        mma_commit(&sh.s_full[x]);
+      };
+      auto wait_v = [&](int i) { return all_ok(mbar_wait(&sh.vfull[i % RG::NV], (i / RG::NV) & 1, P.err)); };
+      auto wait_q = [&](int x) {
+        const bool ok = all_ok(mbar_wait(&sh.q_ready[x], 0, P.err));
+        tc_fence_after_sync();
+        return ok;
+      };
+      bool ok = wait_q(0) && wait_k(0);
       if (ok) {
-        scores(0, 0);
-        mma_commit(&sh.s_full[0]);
+        start(0, 0);
         if (two) {
-          ok = all_ok(mbar_wait(&sh.q_ready[1], 0, P.err));
-          tc_fence_after_sync();
-          scores(1, 0);
-          mma_commit(&sh.s_full[1]);
+          ok = wait_q(1);
+          start(1, 0);
         }
         mma_commit(&sh.kempty[0]);
+        if (duo) {
+          ok = wait_q(1) && wait_k(1);
+          start(1, 1);
+          mma_commit(&sh.kempty[1]);
+        }
       }
-      for (int i = 0; i < nt && ok; ++i) {
+      // (x a constant where it can be: with one loop for all, 8192 rows took 412
+      // instead of 405 us)
+      for (int i = 0; i < nt && ok && !duo; ++i) {
         const bool more = i + 1 < nt;
-        ok = all_ok(mbar_wait(&sh.vfull[i % RG::NV], (i / RG::NV) & 1, P.err)) && values(0, i);
+        ok = wait_v(i) && values(0, i);
         if (!ok) break;
         if (more) {
           ok = wait_k(i + 1);
           if (!ok) break;
-          scores(0, i + 1);
-          mma_commit(&sh.s_full[0]);
+          start(0, i + 1);
         } else {
           mma_commit(&sh.o_full[0]);
         }
@@ -686,14 +706,25 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         }
         mma_commit(&sh.vempty[i % RG::NV]);
         if (more) {
-          if (two) {
-            scores(1, i + 1);
-            mma_commit(&sh.s_full[1]);
-          }
+          if (two) start(1, i + 1);
           mma_commit(&sh.kempty[(i + 1) % RG::NK]);
+        } else {
+          mma_commit(&sh.o_full[1]);
         }
       }
-      mma_commit(&sh.o_full[1]);
+      for (int i = 0; i < nt && ok && duo; ++i) {
+        ok = wait_v(i) && values(i & 1, i);
+        if (!ok) break;
+        mma_commit(&sh.vempty[i % RG::NV]);
+        if (i + 2 < nt) {
+          ok = wait_k(i + 2);
+          if (!ok) break;
+          start(i & 1, i + 2);
+          mma_commit(&sh.kempty[(i + 2) % RG::NK]);
+        } else {
+          mma_commit(&sh.o_full[i & 1]);
+        }
+      }
     } else if (warp == kSoftWarps + 1) {
       // ---------------------------------------------------------- TMA
       int page_n = nt > 1 ? fetch_page(j0 + 1) : -1;
@@ -752,16 +783,17 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         }
       }
     }
-  } else if (warp < 8 || two) {
+  } else if (warp < 8 || two || duo) {
     // ------------------------------------------------------------ softmax
     regs_up<kSoftmaxRegs>();
     // M row im of tile x; this thread's 64 keys (at the end: dims) of it
     const int x = warp >> 3, hf = (warp >> 2) & 1, im = 32 * (warp & 3) + lane, m = 128 * x + im;
     const int pair = 1 + 4 * x + (warp & 3);  // the barrier of the row's two warps
-    const bool live = im < R * G && x * R + row_of(im) < nrows;
+    const int r0 = two ? row0 + x * R : row0;  // first row
+    const bool live = im < R * G && r0 + row_of(im) < row0 + nrows;
     // its position; a row before the start computes what it likes and is
     // zero at the end
-    auto position = [&] { return live ? window_position(P, row0 + x * R + row_of(im)) : -1; };
+    auto position = [&] { return live ? window_position(P, r0 + row_of(im)) : -1; };
     const int pos = position(), p = max(pos, 0);
     // ---- Q of the two warps' 32 M rows, sixteen each, a half-warp per row
     {
@@ -815,9 +847,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.q_ready[x]);
     // (the gate's half row into L2 while there is time)
-    if (live && P.gate != nullptr && P.splits == 1)
+    if (live && (x == 0 || two) && P.gate != nullptr && P.splits == 1)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(
-          P.gate + (static_cast<long long>(row0 + x * R + row_of(im)) * P.hq + kvh * G + head_of(im)) * 128 + 64 * hf));
+          P.gate + (static_cast<long long>(r0 + row_of(im)) * P.hq + kvh * G + head_of(im)) * 128 + 64 * hf));
     pair_sync(pair);
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + 128 * x + lanes, to = tmem + 256 + 128 * x + 64 * hf + lanes;
@@ -830,13 +862,15 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     // (a wait that gives up ends the waiting, not the loop: the two warps
     // always meet)
     bool ok = true;
+    const int both = duo ? 1 : 0;  // (tile x's own key tiles: all, or every other)
+    int own = 0;
 #pragma unroll 1
-    for (int j = 0; j < nt; ++j) {
+    for (int j = both & x; j < nt; j += 1 + both, ++own) {
       const int slot = j % kSlots;
       // the tile's masks and scales, then its scores.  (A slot's next tile is
       // published only after both softmaxes are done with this one: its K
       // waits for a ring buffer that S of a later tile frees.)
-      ok = all_ok(ok && mbar_wait(&sh.info[slot], (j / kSlots) & 1, P.err) && mbar_wait(&sh.s_full[x], j & 1, P.err));
+      ok = all_ok(ok && mbar_wait(&sh.info[slot], (j / kSlots) & 1, P.err) && mbar_wait(&sh.s_full[x], own & 1, P.err));
       tc_fence_after_sync();
       const int kb = sh.first[slot][hf];
       const bool plain = kb >= 0 && kb + 63 <= hi_all && (kb >= lo_all || kb + 63 < P.sinks);
@@ -895,14 +929,14 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           float mx = -INFINITY;
 #pragma unroll
           for (int b = 0; b < 4; ++b) mx = fmaxf(mx, exponent(max16(&r[b >> 1][16 * (b & 1)]), b));
-          sh.pair[j & 1][hf][m] = mx;
+          sh.pair[own & 1][hf][m] = mx;
           pair_sync(pair);
-          mx = fmaxf(mx, sh.pair[j & 1][hf ^ 1][m]);
+          mx = fmaxf(mx, sh.pair[own & 1][hf ^ 1][m]);
           // moves the reference up, the sums with it
           const float mn = fmaxf(ref, mx + kRoom<KVT>);
           const float al = ex2_ftz(ref - (mn == -INFINITY ? 0.f : mn));
           l *= al;
-          if (j > 0) {  // (S of this tile is complete, so O of the last one is)
+          if (own > 0) {  // (S of this tile is complete, so O of the last one is)
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               uint32_t o[16];
@@ -965,16 +999,36 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       mbar_arrive(&sh.p_ready[x]);
     }
     // ---- output
-    sh.pair[nt & 1][hf][m] = l;
+    sh.pair[own & 1][hf][m] = l;
     pair_sync(pair);
-    l += sh.pair[nt & 1][hf ^ 1][m];
+    l += sh.pair[own & 1][hf ^ 1][m];
     ok = all_ok(ok && mbar_wait(&sh.o_full[x], 0, P.err) && mbar_wait(&sh.loads_done, 0, P.err));
+    float other = 0.f;  // what tile B's O is multiplied by
+    float self = 1.f;
+    if (duo) {
+      if (x == 1) {
+        sh.join[0][im] = l;  // (twice the same)
+        sh.join[1][im] = ref;
+        asm volatile("bar.arrive 9, 512;" ::: "memory");
+      } else {
+        ok = all_ok(ok && mbar_wait(&sh.o_full[1], 0, P.err));
+        asm volatile("bar.sync 9, 512;" ::: "memory");
+        const float lb = sh.join[0][im], rb = sh.join[1][im], top = fmaxf(ref, rb);
+        self = ref == -INFINITY ? 0.f : ex2_ftz(ref - top);
+        other = rb == -INFINITY ? 0.f : ex2_ftz(rb - top);
+        l = l * self + lb * other;
+        ref = top;
+      }
+    }
     tc_fence_after_sync();
-    const long long head = static_cast<long long>(row0 + x * R + row_of(im)) * P.hq + kvh * G + head_of(im);
+    if (x == 0 || two) {  // (tile B's part has joined A's)
+    const long long head = static_cast<long long>(r0 + row_of(im)) * P.hq + kvh * G + head_of(im);
     const long long ph = static_cast<long long>(split) * P.rows * P.hq + head;
     // (a NaN sum is not an empty row)
     const bool sees = position() >= 0, empty = !sees || l == 0.f;
     const float inv = (KVT == 1 ? P.v_scale : 1.0f) / l;
+    self *= inv;
+    other *= inv;
     // the warp's 32 rows and 64 dims cross to coalesced stores through their
     // own place in the Q tile, which no MMA reads any more
     uint8_t* tile = sQ + x * kTile;
@@ -985,7 +1039,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       tmem_wait_ld32(o);
       float f[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) f[i] = empty ? 0.f : __uint_as_float(o[i]) * inv;
+      for (int i = 0; i < 32; ++i) f[i] = empty ? 0.f : __uint_as_float(o[i]) * self;
+      if (duo) {
+        tmem_ld32_issue(to + 128 + 32 * c, o);
+        tmem_wait_ld32(o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = empty ? 0.f : fmaf(__uint_as_float(o[i]), other, f[i]);
+      }
       if (sees && ok) {  // what the row sees of the remembered elements
 #pragma unroll 1
         for (int b = 0; b < kPoison * 128 && sh.poison_tile[b >> 7] >= 0; ++b) {
@@ -1024,19 +1084,20 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       const int c8 = 8 * hf + (lane & 7), im0 = 32 * (warp & 3) + (lane >> 3);
       uint4 gate[8];
       auto at = [&](int i2) {
-        return (static_cast<long long>(row0 + x * R + row_of(i2)) * P.hq + kvh * G + head_of(i2)) * 128 + 8 * c8;
+        return (static_cast<long long>(r0 + row_of(i2)) * P.hq + kvh * G + head_of(i2)) * 128 + 8 * c8;
       };
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int i2 = im0 + 4 * u;
-        gate[u] = i2 < R * G && x * R + row_of(i2) < nrows ? load_gate(P, at(i2)) : make_uint4(0u, 0u, 0u, 0u);
+        gate[u] = i2 < R * G && r0 + row_of(i2) < row0 + nrows ? load_gate(P, at(i2)) : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int i2 = im0 + 4 * u;
-        if (i2 < R * G && x * R + row_of(i2) < nrows)
+        if (i2 < R * G && r0 + row_of(i2) < row0 + nrows)
           store_gated(P, at(i2), *reinterpret_cast<const uint4*>(tile + tile_byte(i2, c8)), gate[u]);
       }
+    }
     }
   }
   tc_fence_before_sync();

@@ -218,6 +218,19 @@ def test_window_prefill(kind, page, block, contexts, rows, window, sinks):
     assert Q.check_errors() == 0
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "block"])
+@pytest.mark.parametrize("contexts,rows,hq,hkv,window,sinks", [
+    ([1500 - 7 * i for i in range(40)], [4] * 40, 8, 2, 1400, 5),   # verify steps, whole windows
+    ([20000, 11003], [8, 5], 8, 1, 30000, 0),                       # the same, split
+    ([900, 700, 801], [100, 128, 99], 2, 2, 790, 0),                # heads of their own
+    ([3000] * 20, [16] * 20, 8, 2, 257, 40),                        # few key tiles, an odd number of them
+])
+def test_window_requests_of_one_row_tile(kind, contexts, rows, hq, hkv, window, sinks):
+    b = Batch(contexts, rows, hq=hq, hkv=hkv, kind=kind, page=64, block=32, seed=len(rows), pad=2)
+    b.check_window(b.window(window, sinks), window, sinks, sample_of(b.n))
+    assert Q.check_errors() == 0
+
+
 @pytest.mark.parametrize("kind", ["bf16", "block"])
 @pytest.mark.parametrize("contexts,rows", [([40, 30, 20, 10], [0, 20, 0, 10]), ([40, 900, 20, 700], [0, 800, 0, 700])])
 def test_window_requests_without_rows(kind, contexts, rows):
