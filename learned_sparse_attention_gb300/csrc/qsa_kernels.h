@@ -162,6 +162,7 @@ struct RowGqaParams {
   float* part_lse;         // [splits, rows, Hq]
   unsigned long long* err;
 };
+constexpr int kMaxRowSplits = 128;
 // Splits of rows of up to max_tokens tokens on a device with `sms`
 // multiprocessors.
 int row_gqa_splits(int rows, int hkv, long long max_tokens, int kv_dtype, int sms);

@@ -470,35 +470,67 @@ __global__ void __launch_bounds__(kThreads, 2) row_gqa_kernel(const RowGqaParams
   }
 }
 
-// Joins the splits of each (row, head), 8 dims a thread, in split order.
+// Joins the splits of each (row, head), 8 dims a thread, in split order.  A
+// half-warp's lanes read the log-sum-exps of 16 splits at a time and the
+// partials of 8 are on their way together (33 splits of one row, one after
+// another, took 11 us of 19).
 __global__ void __launch_bounds__(256) row_merge_kernel(const RowGqaParams P) {
   griddep_wait();  // every split's partials are written
   const long long idx = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   const long long head = idx >> 4;
   if (head >= static_cast<long long>(P.rows) * P.hq) return;
-  const int row = static_cast<int>(head / P.hq), d0 = (static_cast<int>(idx) & 15) * 8;
+  const int lane16 = static_cast<int>(idx) & 15, row = static_cast<int>(head / P.hq), d0 = lane16 * 8;
   if (P.packed == nullptr && !row_live(P, row, P.token_to_req[row])) return;
+  const unsigned half = 0xFFFFu << (threadIdx.x & 16);  // (as one from here on)
   const uint4 gate = load_gate(P, head * 128 + d0);
   const long long stride = static_cast<long long>(P.rows) * P.hq;
-  float M = -INFINITY;
+  constexpr int kMost = kMaxRowSplits / 16;
+  float w[kMost];
+  float M = -INFINITY, W = 0.f;
   bool nan = false;
-  for (int s = 0; s < P.splits; ++s) {
-    const float v = __ldcg(P.part_lse + s * stride + head);
-    nan |= v != v;
-    M = fmaxf(M, v);
+#pragma unroll
+  for (int k = 0; k < kMost; ++k) {
+    const int s = 16 * k + lane16;
+    w[k] = s < P.splits ? __ldcg(P.part_lse + s * stride + head) : -INFINITY;
+    nan |= w[k] != w[k];
+    M = fmaxf(M, w[k]);
   }
-  float W = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < P.splits; ++s) {
-    const float lse = __ldcg(P.part_lse + s * stride + head);
-    if (lse == -INFINITY) continue;
-    const float w = ex2_ftz(lse - M);
-    W += w;
-    const float4* po = reinterpret_cast<const float4*>(P.part_o + (s * stride + head) * 128 + d0);
-    const float4 a = __ldcg(po), b = __ldcg(po + 1);
-    acc[0] = fmaf(w, a.x, acc[0]); acc[1] = fmaf(w, a.y, acc[1]);
-    acc[2] = fmaf(w, a.z, acc[2]); acc[3] = fmaf(w, a.w, acc[3]);
-    acc[4] = fmaf(w, b.x, acc[4]); acc[5] = fmaf(w, b.y, acc[5]);
-    acc[6] = fmaf(w, b.z, acc[6]); acc[7] = fmaf(w, b.w, acc[7]);
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(half, M, o));
+  nan = __any_sync(half, nan);
+#pragma unroll
+  for (int k = 0; k < kMost; ++k) {
+    w[k] = w[k] == -INFINITY ? 0.f : ex2_ftz(w[k] - M);
+    W += w[k];
+  }
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) W += __shfl_xor_sync(half, W, o);
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < kMost; ++k) {
+    if (16 * k >= P.splits) break;
+#pragma unroll 1
+    for (int i = 0; i < 16 && 16 * k + i < P.splits; i += 8) {
+      float4 a[8], b[8];
+      float ws[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        ws[u] = __shfl_sync(half, w[k], i + u, 16);
+        a[u] = b[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (ws[u] > 0.f) {  // (a split that saw nothing may not have written)
+          const float4* po = reinterpret_cast<const float4*>(P.part_o + ((16 * k + i + u) * stride + head) * 128 + d0);
+          a[u] = __ldcg(po);
+          b[u] = __ldcg(po + 1);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        acc[0] = fmaf(ws[u], a[u].x, acc[0]); acc[1] = fmaf(ws[u], a[u].y, acc[1]);
+        acc[2] = fmaf(ws[u], a[u].z, acc[2]); acc[3] = fmaf(ws[u], a[u].w, acc[3]);
+        acc[4] = fmaf(ws[u], b[u].x, acc[4]); acc[5] = fmaf(ws[u], b[u].y, acc[5]);
+        acc[6] = fmaf(ws[u], b[u].z, acc[6]); acc[7] = fmaf(ws[u], b[u].w, acc[7]);
+      }
+    }
   }
   const float inv = nan ? __int_as_float(0x7fffffff) : W == 0.f ? 0.f : 1.0f / W;
 #pragma unroll
@@ -526,18 +558,22 @@ cudaError_t launch_kind(const RowGqaParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-// As many splits as keep the CTAs in one wave at two per SM (shared memory):
-// a second wave, or a row cut finer than that, costs more than it evens out
-// (64 rows x 4 KV heads of 4100 tokens, e4m3: 1 split 50 us, 2 splits 60 us;
-// 8 rows x 8 of 4103: 4 splits 27 us, 5 splits 30 us).
+// As many splits as keep the CTAs in one wave at two per SM (shared memory): a
+// second wave, or a row cut finer than that, costs more than it evens out (64
+// rows x 4 KV heads of 4100 tokens, e4m3: 1 split 50 us, 2 splits 60 us; 8 rows
+// x 8 of 4103: 4 splits 27 us, 5 splits 30 us).  A warp has two slabs at the
+// least, and the join, which reads a partial for each split, keeps their square
+// to a twelfth of the tokens (one row and KV head of 4100 tokens, bf16: 8
+// splits 11.7 us, 16 10.7, 22 10.5, 33 11.6).
 int row_gqa_splits(int rows, int hkv, long long max_tokens, int kv_dtype, int sms) {
   const long long base = static_cast<long long>(rows) * hkv;
   if (base <= 0) return 1;
-  const int least = (kv_dtype == QSA_DTYPE_BF16 ? 16 : 32) * kWarps * 2;  // two slabs a warp
+  const int least = (kv_dtype == QSA_DTYPE_BF16 ? 16 : 32) * kWarps * 2;
   long long s = 2ll * sms / base;
   const long long most = (max_tokens + least - 1) / least;
   if (s > most) s = most;
-  if (s > 128) s = 128;
+  if (s > kMaxRowSplits) s = kMaxRowSplits;
+  while (s > 1 && 12 * s * s > max_tokens) --s;
   return s < 1 ? 1 : static_cast<int>(s);
 }
 
