@@ -426,9 +426,10 @@ typedef struct qsa_kv_scales {
  * Offsets after the run keep their codes: they belong to no token yet.
  *  - Slots < 0 write nothing for their row (padding); slots past the cache are
  *    masked and counted.
- *  - A run whose first slot repeats the slot before it or steps back inside
- *    that one's scale block is not written, and counted.  Runs of one call that are not
- *    neighbours must lie in different scale blocks: they would race.
+ *  - A run whose first slot lies in the scale block of the row before it (it
+ *    repeats or steps back), or of the last row before up to 31 rows of
+ *    padding, is not written, and counted.  Other runs of one call must lie in
+ *    different scale blocks: they would race.
  *  - A scale block belongs to one sequence: sequences that share a page share
  *    whole scale blocks that are full.
  */

@@ -678,11 +678,11 @@ long long window_tokens(const qsa_window_args* a) {
 //          1.1), + 6 for a merge.
 // Measured, both ways (tiles / rows, us): window 4096, 8 heads a KV head, 4 KV
 // heads, 64 requests of 1 row 89 / 48 and of 3 rows 91 / 130 (block scales), of
-// 2 rows 108 / 107 and of 3 rows 110 / 157 (bf16); 32 of 4 rows 56 / 109; one of 8 rows 19 / 16, of 24 rows
-// 25 / 25, of 48 rows 26 / 53; 16 of 8 rows and one head a KV head 36 / 104;
-// window 256, 4 of 16 rows 14 / 9, 64 of 4 rows 28 / 26.  Over 53 such sizes
-// the estimates' choice took 1.00 of the faster one's time on average, 1.09 at
-// worst.
+// 2 rows 108 / 107 and of 3 rows 110 / 157 (bf16); 32 of 4 rows 56 / 109; one of
+// 8 rows 18 / 15, of 24 rows 22 / 25, of 48 rows 26 / 53; 16 of 8 rows and one
+// head a KV head 36 / 104; window 256, 4 of 16 rows 14 / 9, 64 of 4 rows 28 / 26.
+// Over 53 such sizes the estimates' choice took 1.00 of the faster one's time on
+// average, 1.09 at worst.
 struct WindowPlan {
   bool tile;
   int splits;

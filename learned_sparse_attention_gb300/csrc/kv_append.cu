@@ -22,7 +22,7 @@
 // of one KV head in registers between the maximum and the rounding (2, 4 or 8
 // tokens a half-warp), so they are read once.
 // Measured, 32 query and 4 KV heads, blocks of 32: 16 384 rows with queries
-// 112 us (5.2 TB/s of reads and writes), 64 rows 3.7 us, 128 rows 5.5 us.
+// 112 us (5.2 TB/s of reads and writes), 64 rows 3.9 us, 128 rows 6.0 us.
 #include "kv_scale.cuh"
 #include "qsa_device.cuh"
 #include "qsa_kernels.h"
@@ -183,13 +183,11 @@ __device__ __forceinline__ void scaled_run(const AppendParams& P, int i, int h, 
   constexpr int B = kHalves * NT;
   const long long slot = P.slots[i];
   const long long blk = slot / P.page;
-  // a row that repeats its predecessor's place or steps back inside one
-  // block would race with that run
-  const bool back = i > 0 && P.slots[i - 1] >= slot && ((P.slots[i - 1] ^ slot) & ~(B - 1ll)) == 0;
-  if (blk >= P.num_blocks || back) {
+  if (blk >= P.num_blocks) {
     if (h == 0 && threadIdx.x == 0) flag_error(P.err);
     return;
   }
+  const long long past = lane < i ? P.slots[i - 1 - lane] : -1;
   // the run's length: every warp looks at all B rows
   int m = 0;
 #pragma unroll
@@ -215,6 +213,14 @@ __device__ __forceinline__ void scaled_run(const AppendParams& P, int i, int h, 
     kr[u] = *reinterpret_cast<const uint4*>(x);
     v[u] = *reinterpret_cast<const uint4*>(x + P.hkv * kD);
     load_pos(P, row, pos[u]);
+  }
+  // a run in the block of the last row before it (it repeats or steps back, or
+  // padding parts it from that row) would race with that row's run
+  const unsigned rows = __ballot_sync(0xffffffffu, past >= 0 && past < static_cast<long long>(P.num_blocks) * P.page);
+  const long long last = __shfl_sync(0xffffffffu, past, rows != 0u ? __ffs(rows) - 1 : 0);
+  if (rows != 0u && ((last ^ slot) & ~(B - 1ll)) == 0) {
+    if (h == 0 && threadIdx.x == 0) flag_error(P.err);
+    return;
   }
   float k[NT][8];
   float pk = 0.f, pv = 0.f;
@@ -284,9 +290,9 @@ __global__ void __launch_bounds__(kThreads, 5) query_kernel(const AppendParams P
   query_rows(P, blockIdx.x, P.q_ctas);
 }
 
-// CTAs [0, kv_ctas) write K and V: with block scales CTA (c, h) the runs of
-// KV head h that begin in rows [c * chunk, (c + 1) * chunk), otherwise CTA c
-// those rows.  The others prepare queries, a row each.  Where the queries have
+// CTAs [0, kv_ctas) write K and V: with block scales CTA (c, h, part) every
+// parts-th run of KV head h of those that begin in rows [c * chunk, (c + 1) *
+// chunk), otherwise CTA c those rows.  The others prepare queries, a row each.  Where the queries have
 // a launch of their own (`beside`), this one runs beside it and needs nothing
 // of it; its last CTA waits for that one's end, so that this kernel's end is
 // both's.
@@ -298,15 +304,21 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams P) 
   griddep_launch_dependents();
   if (cta < P.kv_ctas) {
     const int h = NT > 0 ? cta % P.hkv : 0;
-    const int i0 = (NT > 0 ? cta / P.hkv : cta) * P.chunk;
+    const int part = NT > 0 ? cta / P.hkv % P.parts : 0;
+    const int i0 = (NT > 0 ? cta / P.hkv / P.parts : cta) * P.chunk;
     const int i1 = min(i0 + P.chunk, P.rows);
     if constexpr (NT > 0) {
       float g[8];
       load_gain(P.k_norm_w, lane16, g);
+      int turn = part;                      // runs until this CTA's next one
       for (int b = i0; b < i1; b += 32) {  // 32 rows at a time: where runs begin
         const int i = b + (threadIdx.x & 31);
         unsigned first = __ballot_sync(0xffffffffu, i < i1 && P.slots[i] >= 0 && !goes_on<NT>(P, i - 1));
-        for (; first != 0u; first &= first - 1u) scaled_run<NT>(P, b + __ffs(first) - 1, h, g);
+        for (; first != 0u; first &= first - 1u) {
+          if (turn-- != 0) continue;
+          turn = P.parts - 1;
+          scaled_run<NT>(P, b + __ffs(first) - 1, h, g);
+        }
       }
     } else {
       for (int i = i0; i < i1; ++i) plain_kv_row(P, i);
@@ -326,11 +338,17 @@ cudaError_t launch_nt(AppendParams p, cudaStream_t stream) {
   // SM 113 and 126 us).  One kernel's registers would keep queries from having
   // their loads in flight, and a CTA for each of 16 384 rows and heads takes
   // longer to start than to run (250 us).  Below, where a launch weighs more,
-  // one launch of a CTA per row (and KV head).
+  // one launch of a CTA per row (and KV head).  Two launches / one, us: 512 rows
+  // of one sequence 9.1 / 9.2 and of 512 sequences 16.0 / 15.6, 1024 rows 11.5 /
+  // 15.7 and 25.6 / 28.7.
   const bool many = p.rows >= 1024;
   p.chunk = NT > 0 && many ? kHalves * NT : 1;
   const int chunks = (p.rows + p.chunk - 1) / p.chunk;
-  p.kv_ctas = NT > 0 ? chunks * p.hkv : chunks;
+  // (a chunk may be one run or, in a decode batch, a run a row: while there is
+  // room, several CTAs share its runs; 1024 sequences of a row 47 -> 25.6 us)
+  const int parts = many ? 6 * sm_count() / (chunks * p.hkv) : 1;
+  p.parts = parts < 1 ? 1 : parts > 16 ? 16 : parts;
+  p.kv_ctas = NT > 0 ? chunks * p.hkv * p.parts : chunks;
   p.q_ctas = p.q_out == nullptr ? 0 : p.rows;
   if (!many)
     return launch_kernel(append_kernel<NT>, dim3(p.kv_ctas + p.q_ctas), dim3(kThreads), 0, stream, false, p);

@@ -193,6 +193,7 @@ struct AppendParams {
   float eps, k_scale, v_scale;
   int chunk, kv_ctas, q_ctas;  // set by the launch: rows per K/V CTA, CTAs of each kind
   unsigned long long* err;
+  int parts;                // CTAs that share a chunk's runs
   int beside;               // the K/V kernel runs beside the queries'
 };
 cudaError_t launch_kv_append(AppendParams p, cudaStream_t stream);

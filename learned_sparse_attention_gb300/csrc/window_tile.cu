@@ -1022,82 +1022,82 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     }
     tc_fence_after_sync();
     if (x == 0 || two) {  // (tile B's part has joined A's)
-    const long long head = static_cast<long long>(r0 + row_of(im)) * P.hq + kvh * G + head_of(im);
-    const long long ph = static_cast<long long>(split) * P.rows * P.hq + head;
-    // (a NaN sum is not an empty row)
-    const bool sees = position() >= 0, empty = !sees || l == 0.f;
-    const float inv = (KVT == 1 ? P.v_scale : 1.0f) / l;
-    self *= inv;
-    other *= inv;
-    // the warp's 32 rows and 64 dims cross to coalesced stores through their
-    // own place in the Q tile, which no MMA reads any more
-    uint8_t* tile = sQ + x * kTile;
+      const long long head = static_cast<long long>(r0 + row_of(im)) * P.hq + kvh * G + head_of(im);
+      const long long ph = static_cast<long long>(split) * P.rows * P.hq + head;
+      // (a NaN sum is not an empty row)
+      const bool sees = position() >= 0, empty = !sees || l == 0.f;
+      const float inv = (KVT == 1 ? P.v_scale : 1.0f) / l;
+      self *= inv;
+      other *= inv;
+      // the warp's 32 rows and 64 dims cross to coalesced stores through their
+      // own place in the Q tile, which no MMA reads any more
+      uint8_t* tile = sQ + x * kTile;
 #pragma unroll 1
-    for (int c = 0; c < 2; ++c) {
-      uint32_t o[32];
-      tmem_ld32_issue(to + 32 * c, o);
-      tmem_wait_ld32(o);
-      float f[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) f[i] = empty ? 0.f : __uint_as_float(o[i]) * self;
-      if (duo) {
-        tmem_ld32_issue(to + 128 + 32 * c, o);
+      for (int c = 0; c < 2; ++c) {
+        uint32_t o[32];
+        tmem_ld32_issue(to + 32 * c, o);
         tmem_wait_ld32(o);
+        float f[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) f[i] = empty ? 0.f : fmaf(__uint_as_float(o[i]), other, f[i]);
-      }
-      if (sees && ok) {  // what the row sees of the remembered elements
+        for (int i = 0; i < 32; ++i) f[i] = empty ? 0.f : __uint_as_float(o[i]) * self;
+        if (duo) {
+          tmem_ld32_issue(to + 128 + 32 * c, o);
+          tmem_wait_ld32(o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) f[i] = empty ? 0.f : fmaf(__uint_as_float(o[i]), other, f[i]);
+        }
+        if (sees && ok) {  // what the row sees of the remembered elements
 #pragma unroll 1
-        for (int b = 0; b < kPoison * 128 && sh.poison_tile[b >> 7] >= 0; ++b) {
-          if (!((sh.poison[b >> 7][(b >> 5) & 3] >> (b & 31)) & 1u)) continue;
-          const int key = T.key(sh.poison_tile[b >> 7] + (b & 127));
-          if (key > p || !(key > p - P.window || key < P.sinks)) continue;
-          const int blk = page_of(P, key);
-          const int pid = P.block_table[static_cast<long long>(req) * P.bt_stride + blk];
-          const long long at = ((static_cast<long long>(pid) * P.hkv + kvh) * P.page + key - blk * P.page) * 256 + 128 + 64 * hf + 32 * c;
+          for (int b = 0; b < kPoison * 128 && sh.poison_tile[b >> 7] >= 0; ++b) {
+            if (!((sh.poison[b >> 7][(b >> 5) & 3] >> (b & 31)) & 1u)) continue;
+            const int key = T.key(sh.poison_tile[b >> 7] + (b & 127));
+            if (key > p || !(key > p - P.window || key < P.sinks)) continue;
+            const int blk = page_of(P, key);
+            const int pid = P.block_table[static_cast<long long>(req) * P.bt_stride + blk];
+            const long long at = ((static_cast<long long>(pid) * P.hkv + kvh) * P.page + key - blk * P.page) * 256 + 128 + 64 * hf + 32 * c;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float v = KVT == 0 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(P.kv)[at + i]) << 16)
-                            : (static_cast<const uint8_t*>(P.kv)[at + i] & 0x7F) == 0x7F ? __int_as_float(0x7fffffff) : 0.f;
-            if (!(fabsf(v) <= 3.39e38f)) f[i] += v;
+            for (int i = 0; i < 32; ++i) {
+              const float v = KVT == 0 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(P.kv)[at + i]) << 16)
+                              : (static_cast<const uint8_t*>(P.kv)[at + i] & 0x7F) == 0x7F ? __int_as_float(0x7fffffff) : 0.f;
+              if (!(fabsf(v) <= 3.39e38f)) f[i] += v;
+            }
           }
+        }
+        if (P.splits > 1) {
+          if (!live || !ok) continue;
+          float4* po = reinterpret_cast<float4*>(P.part_o + ph * 128 + 64 * hf + 32 * c);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) po[q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(tile + tile_byte(im, 8 * hf + 4 * c + q)) =
+                make_uint4(pack_bf16x2(f[8 * q], f[8 * q + 1]), pack_bf16x2(f[8 * q + 2], f[8 * q + 3]),
+                           pack_bf16x2(f[8 * q + 4], f[8 * q + 5]), pack_bf16x2(f[8 * q + 6], f[8 * q + 7]));
         }
       }
       if (P.splits > 1) {
-        if (!live || !ok) continue;
-        float4* po = reinterpret_cast<float4*>(P.part_o + ph * 128 + 64 * hf + 32 * c);
+        if (live && ok && hf == 0) P.part_lse[ph] = empty ? -INFINITY : ref + log2f(l);
+      } else if (ok) {
+        __syncwarp();
+        // four rows at a time, eight lanes each
+        const int c8 = 8 * hf + (lane & 7), im0 = 32 * (warp & 3) + (lane >> 3);
+        uint4 gate[8];
+        auto at = [&](int i2) {
+          return (static_cast<long long>(r0 + row_of(i2)) * P.hq + kvh * G + head_of(i2)) * 128 + 8 * c8;
+        };
 #pragma unroll
-        for (int q = 0; q < 8; ++q) po[q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
-      } else {
+        for (int u = 0; u < 8; ++u) {
+          const int i2 = im0 + 4 * u;
+          gate[u] = i2 < R * G && r0 + row_of(i2) < row0 + nrows ? load_gate(P, at(i2)) : make_uint4(0u, 0u, 0u, 0u);
+        }
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<uint4*>(tile + tile_byte(im, 8 * hf + 4 * c + q)) =
-              make_uint4(pack_bf16x2(f[8 * q], f[8 * q + 1]), pack_bf16x2(f[8 * q + 2], f[8 * q + 3]),
-                         pack_bf16x2(f[8 * q + 4], f[8 * q + 5]), pack_bf16x2(f[8 * q + 6], f[8 * q + 7]));
+        for (int u = 0; u < 8; ++u) {
+          const int i2 = im0 + 4 * u;
+          if (i2 < R * G && r0 + row_of(i2) < row0 + nrows)
+            store_gated(P, at(i2), *reinterpret_cast<const uint4*>(tile + tile_byte(i2, c8)), gate[u]);
+        }
       }
-    }
-    if (P.splits > 1) {
-      if (live && ok && hf == 0) P.part_lse[ph] = empty ? -INFINITY : ref + log2f(l);
-    } else if (ok) {
-      __syncwarp();
-      // four rows at a time, eight lanes each
-      const int c8 = 8 * hf + (lane & 7), im0 = 32 * (warp & 3) + (lane >> 3);
-      uint4 gate[8];
-      auto at = [&](int i2) {
-        return (static_cast<long long>(r0 + row_of(i2)) * P.hq + kvh * G + head_of(i2)) * 128 + 8 * c8;
-      };
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int i2 = im0 + 4 * u;
-        gate[u] = i2 < R * G && r0 + row_of(i2) < row0 + nrows ? load_gate(P, at(i2)) : make_uint4(0u, 0u, 0u, 0u);
-      }
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int i2 = im0 + 4 * u;
-        if (i2 < R * G && r0 + row_of(i2) < row0 + nrows)
-          store_gated(P, at(i2), *reinterpret_cast<const uint4*>(tile + tile_byte(i2, c8)), gate[u]);
-      }
-    }
     }
   }
   tc_fence_before_sync();

@@ -658,14 +658,16 @@ def dequantise_block_kv(codes, scales, scale_block: int) -> np.ndarray:
 def append_runs(slots, scale_block: int) -> list:
     """[(first row, rows)] of the runs of consecutive rows whose slots ascend
     inside one scale block; rows without a slot are in none, and neither are
-    rows that repeat or step back inside their predecessor's block."""
+    runs that begin in the block of the last row before them, 31 rows without
+    a slot between at the most."""
     runs, i, n = [], 0, len(slots)
     while i < n:
         s = int(slots[i])
         j = i + 1
         while j < n and s >= 0 and int(slots[j]) > int(slots[j - 1]) and int(slots[j]) // scale_block == s // scale_block:
             j += 1
-        back = i > 0 and int(slots[i - 1]) >= s and int(slots[i - 1]) // scale_block == s // scale_block
+        past = [int(x) for x in slots[max(0, i - 32):i] if x >= 0]
+        back = bool(past) and past[-1] // scale_block == s // scale_block
         if s >= 0 and not back:
             runs.append((i, j - i))
         i = j

@@ -238,7 +238,8 @@ def test_scale_exponent():
 def test_append_runs():
     assert O.append_runs([64, 65, 66], 32) == [(0, 3)]
     assert O.append_runs([94, 95, 96, 97], 32) == [(0, 2), (2, 2)]
-    assert O.append_runs([3, -1, 4, 4, 5], 16) == [(0, 1), (2, 1)]
+    assert O.append_runs([3, -1, 4, 4, 5], 16) == [(0, 1)] and O.append_runs([3, -1, 20], 16) == [(0, 1), (2, 1)]
+    assert O.append_runs([3] + [-1] * 31 + [4], 16) == [(0, 1)]
     assert O.append_runs([9, 8], 16) == [(0, 1)] and O.append_runs([9, 40, 8], 16) == [(0, 1), (1, 1), (2, 1)]
     assert O.append_runs([1, 3, 9], 16) == [(0, 3)]
 

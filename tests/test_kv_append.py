@@ -204,10 +204,11 @@ def test_batches(rows_per_req):
 def test_padding_bad_and_repeated_slots():
     c = Case(12, seed=9)
     slots = np.array([70, 71, -1, 72, 6 * 64, 80, 80, 81, -1, 200, 199, 201])
-    # 72 begins a new run at offset 8: the block's scale only grows; 6 * 64 is
-    # past the cache; the second 80 and 199 are not written
+    # 72 and the first 80 begin runs in the block of the last row before them,
+    # 6 * 64 is past the cache, the second 80 repeats and 199 steps back: none is
+    # written, nor is what goes on with them
     codes, scales, _ = run_scaled(c, slots)
-    assert Q.check_errors() == 3
+    assert Q.check_errors() == 5
     want = slots.copy()
     want[4] = -1
     k, v = c.oracle_kv()
@@ -287,3 +288,37 @@ def test_on_another_stream(rows):
     torch.cuda.synchronize()
     assert torch.equal(got, t2["main_q_out"]) and torch.equal(codes, codes2) and torch.equal(scales, scales2)
     assert Q.check_errors() == 0
+
+
+@pytest.mark.parametrize("block", [16, 64])
+@pytest.mark.parametrize("hkv", [1, 3])
+def test_many_short_runs(block, hkv):
+    """1200 rows, most of them runs of their own: one to three rows each in
+    some scale block, in any order."""
+    rng = np.random.default_rng(block + hkv)
+    c = Case(1200, hq=hkv, hkv=hkv, blocks=1200 * block // 64 + 1, block=block, seed=15)
+    where = rng.permutation(c.blocks * 64 // block)
+    slots, at = [], 0
+    while len(slots) < 1200:  # (padding only between runs: inside one it would part it in two)
+        n, first = rng.integers(1, 4), rng.integers(0, block - 3)
+        slots += [where[at] * block + first + k if at % 30 else -1 for k in range(n)]
+        at += 1
+    slots = np.array(slots[:1200])
+    codes, scales, _ = run_scaled(c, slots)
+    check_scaled(c, slots, codes, scales)
+    assert Q.check_errors() == 0
+
+
+@pytest.mark.parametrize("rows", [70, 1100])
+def test_padding_inside_a_sequence_is_refused(rows):
+    """What follows padding in the block of the row before it is left out and
+    counted, in another block it is a run of its own."""
+    c = Case(rows, blocks=60, seed=16)
+    slots = contiguous_slots(c, 64, rows)
+    slots[10:14] = -1              # 74 .. 77: 78 .. 95 follow in the same block of 32
+    slots[30:33] = -1              # 94 .. 96: 97 follows in the next one
+    codes, scales, _ = run_scaled(c, slots)
+    assert Q.check_errors() == 1
+    want = slots.copy()
+    want[14:30] = -1
+    check_scaled(c, want, codes, scales)
