@@ -184,9 +184,14 @@ size_t row_ws_bytes(const qsa_gqa_cfg* g, int rows, int splits) {
          align256(static_cast<size_t>(splits) * rows * g->num_q_heads * sizeof(float));
 }
 
+// The same of the single-row kernel, which needs none where a cluster joins.
+size_t rows_ws_bytes(const qsa_gqa_cfg* g, int rows, int splits) {
+  return row_gqa_cluster(rows, g->num_kv_heads, splits, sm_count()) ? 0 : row_ws_bytes(g, rows, splits);
+}
+
 size_t gqa_ws_bytes(const qsa_gqa_cfg* g, int rows, int packed_width) {
   if (g->kv_dtype == QSA_DTYPE_E4M3_BLOCK)
-    return row_ws_bytes(g, rows, row_gqa_splits(rows, g->num_kv_heads, packed_width - 1, g->kv_dtype, sm_count()));
+    return rows_ws_bytes(g, rows, row_gqa_splits(rows, g->num_kv_heads, packed_width - 1, g->kv_dtype, sm_count()));
   return gqa_layout(g, rows, packed_width).total;
 }
 
@@ -618,9 +623,10 @@ qsa_status fill_row_gqa(RowGqaParams* p, const qsa_gqa_cfg* g, const qsa_kv_scal
 
 // The split of the rows and its partials in ws, and, the checks being done,
 // the device's error word.
-qsa_status place_splits(RowGqaParams* p, const qsa_gqa_cfg* g, int splits, void* ws, size_t ws_bytes) {
+qsa_status place_splits(RowGqaParams* p, const qsa_gqa_cfg* g, int splits, bool tile, void* ws, size_t ws_bytes) {
   p->splits = splits;
-  const size_t need = row_ws_bytes(g, p->rows, splits);
+  p->cluster = !tile && row_gqa_cluster(p->rows, p->hkv, splits, sm_count());
+  const size_t need = p->cluster ? 0 : row_ws_bytes(g, p->rows, splits);
   if (need != 0 && (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < need))
     return QSA_ERR_WORKSPACE;
   p->err = error_word();
@@ -648,7 +654,7 @@ qsa_status do_sparse_scaled(const qsa_gqa_cfg* g, const qsa_kv_scales* scales, c
   if (st != QSA_OK) return st;
   p.packed = packed;
   p.packed_width = packed_width;
-  st = place_splits(&p, g, row_gqa_splits(rows, p.hkv, packed_width - 1, p.kv_dtype, sm_count()), ws, ws_bytes);
+  st = place_splits(&p, g, row_gqa_splits(rows, p.hkv, packed_width - 1, p.kv_dtype, sm_count()), /*tile=*/false, ws, ws_bytes);
   if (st != QSA_OK) return st;
   return cuda_status(launch_row_gqa(p, stream));
 }
@@ -721,7 +727,7 @@ qsa_status do_window(const qsa_gqa_cfg* g, const qsa_window_args* a, void* ws, s
   const long long keys = static_cast<long long>(a->bt_stride) * p.page;
   p.keys = static_cast<int>(keys < kMaxKeys ? keys : kMaxKeys);
   const WindowPlan plan = window_plan(g, a);
-  st = place_splits(&p, g, plan.splits, ws, ws_bytes);
+  st = place_splits(&p, g, plan.splits, plan.tile, ws, ws_bytes);
   if (st != QSA_OK) return st;
   if (!plan.tile) return cuda_status(launch_row_gqa(p, stream));
   // boxes that pages are multiples of.  Larger ones take less of the TMA
@@ -1012,7 +1018,8 @@ qsa_status qsa_window_gqa(const qsa_gqa_cfg* gcfg, const qsa_window_args* args, 
 
 size_t qsa_window_workspace_bytes(const qsa_gqa_cfg* gcfg, const qsa_window_args* args) {
   if (check_window(gcfg, args) != QSA_OK || args->rows == 0) return 0;
-  return row_ws_bytes(gcfg, args->rows, window_plan(gcfg, args).splits);
+  const WindowPlan plan = window_plan(gcfg, args);
+  return plan.tile ? row_ws_bytes(gcfg, args->rows, plan.splits) : rows_ws_bytes(gcfg, args->rows, plan.splits);
 }
 
 qsa_status qsa_mtp_steps(const qsa_cfg* cfg, const qsa_gqa_cfg* gcfg, const qsa_step_args* steps,

@@ -158,6 +158,7 @@ struct RowGqaParams {
   int keys;                // window only: tokens of a row of the table, at most kMaxKeys
   int box;                 // keys of a TMA box of the window tiles: 16, 32 or 64
   int splits;
+  int cluster;             // rows alone: the splits of a row and KV head are a cluster and join in it
   float* part_o;           // [splits, rows, Hq, 128] (splits > 1)
   float* part_lse;         // [splits, rows, Hq]
   unsigned long long* err;
@@ -166,6 +167,8 @@ constexpr int kMaxRowSplits = 128;
 // Splits of rows of up to max_tokens tokens on a device with `sms`
 // multiprocessors.
 int row_gqa_splits(int rows, int hkv, long long max_tokens, int kv_dtype, int sms);
+// Whether they join in a cluster, with no partials in memory.
+bool row_gqa_cluster(int rows, int hkv, int splits, int sms);
 cudaError_t launch_row_gqa(const RowGqaParams& p, cudaStream_t stream);
 // Joins the splits that p's launch left in part_o and part_lse.
 cudaError_t launch_row_merge(const RowGqaParams& p, cudaStream_t stream);

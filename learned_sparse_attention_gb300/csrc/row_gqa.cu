@@ -26,13 +26,15 @@
 // (S = Q K^T) or dims (O = P V) on N, so a lane's scores are the P fragment it
 // needs next.  Of e4m3 rows a lane holds 4 consecutive bytes where bf16 rows
 // give it 2 + 2: dims (K) and tokens (V) are taken in that order, by q's
-// fragments and by K's rows (tau, below).  Splits leave fp32 partials that a
-// second kernel joins in a fixed order.
+// fragments and by K's rows (tau, below).  Splits join in a fixed order: in a
+// cluster, or as fp32 partials that a second kernel reads.
 // Measured: 64 rows of 32 query and 4 KV heads over block scales, the last
 // 4100 tokens 47.8 us (5.7 TB/s; e4m3 decoded as two e4m3 terms 72 us), 2051
 // selected ones 34.3 us (4.0 TB/s; runs of 1 KB come at ~5.3 TB/s, the rest is
 // the chain of loads before the first copy and the last CTAs); 8 rows of 64
-// and 8 heads, 4103 selected tokens in 4 splits 19.2 us.
+// and 8 heads, 4103 selected tokens in 4 splits 18.3 us.
+#include <cooperative_groups.h>
+
 #include "kv_scale.cuh"
 #include "qsa_device.cuh"
 #include "qsa_kernels.h"
@@ -95,8 +97,10 @@ __global__ void __launch_bounds__(kThreads, 2) row_gqa_kernel(const RowGqaParams
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   // KV-head-major order: rows of one request that share tokens meet in L2
-  const int kvh = static_cast<int>(blockIdx.x) / P.rows, row = static_cast<int>(blockIdx.x) % P.rows;
-  const int split = blockIdx.y;
+  // (with clusters, the splits of a row and KV head are one)
+  const int pair = P.cluster ? static_cast<int>(blockIdx.x) / P.splits : static_cast<int>(blockIdx.x);
+  const int kvh = pair / P.rows, row = pair % P.rows;
+  const int split = P.cluster ? static_cast<int>(blockIdx.x) % P.splits : static_cast<int>(blockIdx.y);
   const int G = P.group;
   const int req = P.token_to_req[row];
   griddep_launch_dependents();
@@ -436,6 +440,9 @@ __global__ void __launch_bounds__(kThreads, 2) row_gqa_kernel(const RowGqaParams
       *reinterpret_cast<float2*>(co + at * LD + 8 * nb + 2 * t) = make_float2(o[nb][2 * hb], o[nb][2 * hb + 1]);
   }
   __syncthreads();
+  float* fm = co + kWarps * HN * LD;  // with clusters: the CTA's own part, [head] and [head][dim]
+  float* fl = fm + HN;
+  float* fo = fl + HN;
   const int d0 = (threadIdx.x & 15) * 8;
 #pragma unroll
   for (int hb = 0; hb < HB; ++hb) {
@@ -453,6 +460,16 @@ __global__ void __launch_bounds__(kThreads, 2) row_gqa_kernel(const RowGqaParams
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] = fmaf(co[(w * HN + h) * LD + d0 + e], wt, acc[e]);
     }
+    if (P.cluster) {
+      if (d0 == 0) {
+        fm[h] = M;
+        fl[h] = L;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; e += 4)
+        *reinterpret_cast<float4*>(fo + h * 128 + d0 + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+      continue;
+    }
     // (a NaN sum is not an empty row)
     const float inv = L == 0.f ? 0.f : (KVT == 1 ? P.v_scale : 1.0f) / L;
 #pragma unroll
@@ -468,6 +485,34 @@ __global__ void __launch_bounds__(kThreads, 2) row_gqa_kernel(const RowGqaParams
     po[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
     if (d0 == 0) P.part_lse[ph] = L == 0.f ? -INFINITY : M + log2f(L);
   }
+  if (!P.cluster) return;
+  // ---- join the cluster's parts, 8 dims of a head a thread, over all its CTAs
+  cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+  cluster.sync();
+  for (int it = split + P.splits * static_cast<int>(threadIdx.x); it < 16 * G; it += P.splits * kThreads) {
+    const int h = it >> 4, d = (it & 15) * 8;
+    const long long at = (static_cast<long long>(row) * P.hq + kvh * G + h) * 128 + d;
+    const uint4 gate = load_gate(P, at);
+    float M = -INFINITY;
+    for (int q = 0; q < P.splits; ++q) M = fmaxf(M, cluster.map_shared_rank(fm, q)[h]);
+    float L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int q = 0; q < P.splits; ++q) {
+      const float mq = cluster.map_shared_rank(fm, q)[h];
+      const float wt = mq == -INFINITY ? 0.f : ex2_ftz(mq - M);
+      L = fmaf(cluster.map_shared_rank(fl, q)[h], wt, L);
+      const float4* o4 = reinterpret_cast<const float4*>(cluster.map_shared_rank(fo, q) + h * 128 + d);
+      const float4 a = o4[0], b = o4[1];
+      acc[0] = fmaf(a.x, wt, acc[0]); acc[1] = fmaf(a.y, wt, acc[1]);
+      acc[2] = fmaf(a.z, wt, acc[2]); acc[3] = fmaf(a.w, wt, acc[3]);
+      acc[4] = fmaf(b.x, wt, acc[4]); acc[5] = fmaf(b.y, wt, acc[5]);
+      acc[6] = fmaf(b.z, wt, acc[6]); acc[7] = fmaf(b.w, wt, acc[7]);
+    }
+    const float inv = L == 0.f ? 0.f : (KVT == 1 ? P.v_scale : 1.0f) / L;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] *= inv;
+    store_gated8(P, at, acc, gate);
+  }
+  cluster.sync();  // (a CTA's part is read until here)
 }
 
 // Joins the splits of each (row, head), 8 dims a thread, in split order.  A
@@ -541,7 +586,7 @@ __global__ void __launch_bounds__(256) row_merge_kernel(const RowGqaParams P) {
 template <int KVT, int HB>
 cudaError_t launch_kind(const RowGqaParams& p, cudaStream_t stream) {
   using RP = RowPlan<KVT>;
-  constexpr int kMerge = kWarps * 8 * HB * (128 + 4 + 2) * 4;
+  constexpr int kMerge = (kWarps * 8 * HB * (128 + 4 + 2) + 8 * HB * (128 + 2)) * 4;
   constexpr int kSmem = RP::kSmem > kMerge ? RP::kSmem : kMerge;
   static bool attr_set[64] = {};
   int dev = 0;
@@ -552,6 +597,9 @@ cudaError_t launch_kind(const RowGqaParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
+  if (p.cluster)
+    return launch_kernel_cluster(row_gqa_kernel<KVT, HB>, dim3(p.rows * p.hkv * p.splits), dim3(kThreads), kSmem,
+                                 stream, false, p.splits, p);
   return launch_kernel(row_gqa_kernel<KVT, HB>, dim3(p.rows * p.hkv, p.splits), dim3(kThreads), kSmem,
                        stream, false, p);
 }
@@ -577,6 +625,15 @@ int row_gqa_splits(int rows, int hkv, long long max_tokens, int kv_dtype, int sm
   return s < 1 ? 1 : static_cast<int>(s);
 }
 
+// Up to eight splits of a row and KV head are a cluster and join through its
+// shared memory, without the partials' way through memory and a second launch
+// (8 rows x 8 KV heads in 4 splits 19.1 -> 18.3 us, one row in 5 splits 7.2 ->
+// 6.6); not where the launch nearly fills the SMs, whose groups may then hold
+// fewer clusters than single CTAs.
+bool row_gqa_cluster(int rows, int hkv, int splits, int sms) {
+  return splits > 1 && splits <= 8 && static_cast<long long>(rows) * hkv * splits <= 2 * sms * 85 / 100;
+}
+
 cudaError_t launch_row_gqa(const RowGqaParams& p, cudaStream_t stream) {
   if (p.rows == 0) return cudaSuccess;
   const bool wide = p.group > 8;
@@ -586,7 +643,7 @@ cudaError_t launch_row_gqa(const RowGqaParams& p, cudaStream_t stream) {
     case QSA_DTYPE_E4M3: e = wide ? launch_kind<1, 2>(p, stream) : launch_kind<1, 1>(p, stream); break;
     default: e = wide ? launch_kind<2, 2>(p, stream) : launch_kind<2, 1>(p, stream); break;
   }
-  if (e != cudaSuccess || p.splits == 1) return e;
+  if (e != cudaSuccess || p.splits == 1 || p.cluster) return e;
   return launch_row_merge(p, stream);
 }
 

@@ -231,6 +231,29 @@ def test_window_requests_of_one_row_tile(kind, contexts, rows, hq, hkv, window, 
     assert Q.check_errors() == 0
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "block"])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (6, 2), (8, 1), (32, 2)])
+@pytest.mark.parametrize("n", [300, 700, 1000, 2000])
+def test_window_single_rows_in_few_splits(kind, hq, hkv, n):
+    """Two to eight splits; rows shorter than one of them, before the start and
+    of no request among them."""
+    b = Batch([n, n // 2, 3, n - 1], [1, 1, 1, 1], hq=hq, hkv=hkv, kind=kind, page=64, block=32, seed=n + hq, pad=2)
+    b.pos[1] = -1
+    out = b.window(100000, 0)
+    assert (out[1] == 0).all()
+    b.check_window(out, 100000, 0)
+    assert Q.check_errors() == 0
+
+
+@pytest.mark.parametrize("hq,hkv", [(3, 1), (16, 1), (8, 2)])
+@pytest.mark.parametrize("n", [500, 1300, 2000])
+def test_sparse_in_few_splits(hq, hkv, n):
+    b = Batch([3000, 2500, 2200], [1, 1, 1], hq=hq, hkv=hkv, page=64, block=64, seed=n + hq)
+    packed = packed_rows(b, n + 1, n, [n, 0, n // 3])
+    check_sparse(b, packed, run_sparse(b, packed))
+    assert Q.check_errors() == 0
+
+
 @pytest.mark.parametrize("kind", ["bf16", "block"])
 @pytest.mark.parametrize("contexts,rows", [([40, 30, 20, 10], [0, 20, 0, 10]), ([40, 900, 20, 700], [0, 800, 0, 700])])
 def test_window_requests_without_rows(kind, contexts, rows):
