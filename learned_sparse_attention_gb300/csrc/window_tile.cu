@@ -376,7 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     const bool apart = P.window > 0 && w0 > sinks;
     T.ns = apart ? sinks : 0;
     T.shift = apart ? w0 - sinks : 0;
-    const int end = P.window > 0 ? keys - T.shift : sinks;
+    // (windows that begin past the table hold none of its keys, the sinks stay)
+    const int end = P.window > 0 ? max(keys - T.shift, T.ns) : sinks;
     T.n = pmax < 0 ? 0 : (end + 127) >> 7;
   }
   const int per = P.splits > 1 ? (T.n + P.splits - 1) / P.splits : T.n;
