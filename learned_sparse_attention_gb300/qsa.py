@@ -268,10 +268,12 @@ def main_prep(t: dict, eps: float = 1e-6) -> QsaMainPrep:
 def _main_entries(t):
     """What kv_append asks of main_prep's tensors at every call: their device
     and numbers of entries."""
-    names = ("main_qkv", "slot_mapping", "main_q_out", "main_gate_out", "kv")
+    names = ("main_qkv", "slot_mapping", "main_q_out", "main_gate_out", "kv", "main_k_norm_w", "main_q_norm_w")
+    if t.get("main_q_out") is None:
+        names = names[:-1]  # (K and V alone: not read)
     n = [1 << 62 if t.get(k) is None else t[k].numel() for k in names]
     dev = {t[k].get_device() for k in names if t.get(k) is not None}
-    return (dev.pop() if len(dev) == 1 else None, *n)
+    return (dev.pop() if len(dev) == 1 else None, *n[:5], min(n[5:]))
 
 
 def main_prepare(cfg, gcfg, m: QsaMainPrep, positions, cos_sin, stream=None):
@@ -443,14 +445,17 @@ def kv_append(cfg, gcfg, m: QsaMainPrep, positions, cos_sin, scales: QsaKvScales
     specs = ((positions, torch.int64, rows * 3, "positions"),
              (cos_sin, torch.float32, cfg.max_position * cfg.rotary_dim, "cos_sin"))
     cache, sc = _cache_specs(gcfg, scales, t["kv"])
-    at, qkv, slots, q, gate, kv = m._entries
+    at, qkv, slots, q, gate, kv, norm = m._entries
     if (at != dev or qkv < rows * (hq + hkv) * 256 or slots < rows or q < rows * hq * 128 or
-            gate < rows * hq * 128 or kv < cache[2] or t["kv"].dtype is not cache[1]):
+            gate < rows * hq * 128 or kv < cache[2] or norm < 128 or t["kv"].dtype is not cache[1]):
         bf16 = torch.bfloat16  # (which of them)
         specs += ((t["main_qkv"], bf16, rows * (hq + hkv) * 256, "main_qkv"),
                   (t["slot_mapping"], torch.int64, rows, "slot_mapping"),
                   (t.get("main_q_out"), bf16, rows * hq * 128, "main_q_out"),
-                  (t.get("main_gate_out"), bf16, rows * hq * 128, "main_gate_out"), cache)
+                  (t.get("main_gate_out"), bf16, rows * hq * 128, "main_gate_out"), cache,
+                  (t.get("main_k_norm_w"), bf16, 128, "main_k_norm_w"))
+        if t.get("main_q_out") is not None:
+            specs += ((t.get("main_q_norm_w"), bf16, 128, "main_q_norm_w"),)
     ptrs = _pointers(dev, (*specs, sc))
     with _on(dev):
         st = load().qsa_kv_append(
