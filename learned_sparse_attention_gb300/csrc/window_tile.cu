@@ -276,6 +276,17 @@ __device__ __noinline__ void file_poison(TileShared* sh, int v, uint32_t* odd_ke
   __syncwarp();
 }
 
+// Whether one of the rows at these positions sees one of the keys a .. b.
+// (Rows far apart leave keys between their windows that nobody sees.)
+__device__ __noinline__ bool rows_see(const int32_t* positions, int rows, int window, int sinks, int a, int b) {
+#pragma unroll 1
+  for (int r = 0; r < rows; ++r) {
+    const int p = min(positions[r], kMaxKeys);  // (as window_position; below 0 it sees none)
+    if (p >= a && (a < sinks || (window > 0 && b > p - window))) return true;
+  }
+  return false;
+}
+
 // KVT 0 bf16, 1 e4m3 with static scales, 2 e4m3 with block scales.
 template <int KVT>
 __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_constant__ CUtensorMap tmap, const RowGqaParams P) {
@@ -455,9 +466,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       const int v = 128 * (j0 + i) + 64 * lane;
       sh.first[slot][lane] = bad != 0u || (v < T.ns && v + 63 >= T.ns) ? -1 : T.key(v);
     }
+    if (bad != 0u) {  // counted where a row sees one of them
+      const int k0 = block_key(j0 + i);
+      const bool missed = lane < 8 && rows == kNoPage && rows_see(P.logical + row0, nrows, P.window, P.sinks, k0, k0 + 15);
+      if (__any_sync(0xffffffffu, missed) && lane == 0) flag_error(P.err);
+    }
     if (lane == 0) {
       sh.check[slot] = bad != 0u;
-      if (bad) flag_error(P.err);
       sh.ns = T.ns;
       sh.shift = T.shift;
     }
@@ -503,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         auto check = [&](int from, int to) {
 #pragma unroll 1
           for (int key = from + ((k0 - from) & (S - 1)); key < to; key += S)
-            if (check_key(key)) {
+            if (check_key(key) && rows_see(P.logical + row0, nrows, P.window, P.sinks, T.key(v + key), T.key(v + key))) {
               remember(key);
               some = true;
             }

@@ -41,3 +41,81 @@ def test_sinks_of_rows_whose_windows_pass_the_table(kind, rows, first):
     out = b.window(1000, 40, max_context=first + rows)
     assert Q.check_errors() > 0
     check_rows(b, out, some(rows), 1000, 40, lost=np.arange(320, first + rows))
+
+
+def far_apart(kind, rows, seed, page=32):
+    """One request, half of its rows from position 1000 and half from 20000 on,
+    with windows of 1000: nobody sees tokens 1000 + rows // 2 .. 19000."""
+    b = Batch([20000 + rows - rows // 2], [rows], kind=kind, page=page, block=16, seed=seed, hq=2, hkv=1, gate=False)
+    half = rows // 2
+    b.pos[:] = np.r_[1000 + np.arange(half), 20000 + np.arange(rows - half)]
+    return b, (1000 + half + page - 1) // page, 19001 // page  # and the first and last + 1 of the unseen pages
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows", [70, 1001])
+def test_pages_between_rows_far_apart_may_be_gone(kind, rows):
+    b, p0, p1 = far_apart(kind, rows, 22)
+    b.table[0, p0:p1] = -1
+    out = b.window(1000, 3)
+    assert Q.check_errors() == 0
+    check_rows(b, out, some(rows) + [rows // 2 - 1, rows // 2], 1000, 3)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows", [70, 1001])
+def test_odd_values_that_no_row_sees_take_no_room(kind, rows):
+    """NaN in more than 32 stretches of 128 tokens between two groups of rows,
+    and one more that some rows see."""
+    b, p0, p1 = far_apart(kind, rows, 23)
+    bad = float("nan") if kind == "bf16" else 0x7F
+    b.kv[torch.from_numpy(b.table[0, p0:p1].astype(np.int64)), :, :, D:] = bad
+    tok = 19000 + rows // 4  # left by the window on the way through the later rows
+    b.kv[b.table[0, tok // 32], 0, tok % 32, D + 9] = bad
+    out = b.window(1000, 3)
+    assert Q.check_errors() == 0
+    sees = (b.pos - 1000 < tok) & (tok <= b.pos)
+    assert sees.any() and not sees.all()
+    assert np.isnan(out[sees][:, :, 9]).all()
+    assert np.isfinite(out[sees][:, :, np.arange(D) != 9]).all() and np.isfinite(out[~sees]).all()
+    check_rows(b, out, [i for i in some(rows) + [rows // 2 - 1] if not sees[i]], 1000, 3)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows", [60, 2000])
+def test_sinks_alone_need_no_other_pages(kind, rows):
+    b = Batch([rows], [rows], kind=kind, page=16, block=16, seed=24, hq=2, hkv=1, gate=False)
+    b.table[0, 13:] = -1  # tokens from 208 on: 200 are sinks, the rest unseen
+    out = b.window(0, 200)
+    assert Q.check_errors() == 0
+    check_rows(b, out, some(rows), 0, 200)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_bad_pages_in_tiles_are_left_out_and_counted(kind):
+    b = Batch([4300], [4000], kind=kind, page=16, block=16, seed=25, hq=2, hkv=1, gate=False)
+    b.table[0, 16], b.table[0, 100] = b.blocks + 5, -1
+    out = b.window(64, 0)
+    assert Q.check_errors() > 0
+    near = list(range(40)) + list(range(1595 - 300, 1685 - 300, 3))
+    check_rows(b, out, near + some(4000), 64, 0, lost=np.r_[256:272, 1600:1616])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_odd_values_in_tiles_reach_only_rows_that_see_them(kind):
+    """Tokens that enter and leave the windows during the call."""
+    b = Batch([4300], [4000], kind=kind, page=16, block=16, seed=26, hq=2, hkv=1, gate=False)
+    toks = [240, 299, 1000, 1001, 2047, 2048, 4299]
+    for t in toks:
+        b.kv[b.table[0, t // 16], 0, t % 16, D + 5] = float("inf") if kind == "bf16" else 0xFF
+        b.kv[b.table[0, t // 16], 0, t % 16, D + 9] = float("nan") if kind == "bf16" else 0x7F
+    out = b.window(64, 0)
+    assert Q.check_errors() == 0
+    sees = np.zeros(4000, dtype=bool)
+    for t in toks:
+        sees |= (b.pos - 64 < t) & (t <= b.pos)
+    clean = ~np.isin(np.arange(D), [5, 9])
+    assert np.isnan(out[sees][:, :, 9]).all() and not np.isfinite(out[sees][:, :, 5]).any()
+    assert np.isfinite(out[sees][:, :, clean]).all() and np.isfinite(out[~sees]).all()
+    edge = [i for t in toks for p in (t - 1, t + 63, t + 64) for i in [p - 300] if 0 <= i < 4000]
+    check_rows(b, out, [i for i in edge + some(4000) if not sees[i]], 64, 0)
