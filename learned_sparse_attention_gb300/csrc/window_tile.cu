@@ -24,10 +24,14 @@
 // could hide the other.
 // TMEM: S_A, S_B, O_A, O_B of 128 columns each.  P is the A operand from
 // TMEM; V is the N-major B operand of the ring tile as it is stored.
-// e4m3 caches: K's codes are multiplied as they are, by q split into two e4m3
-// terms hi + lo (after a power of two per row that puts its largest |q| into
-// [128, 256): exact but for elements below 2^-10 of it, off by at most 2^-18
-// of it there); P and V are f16.  K's block scales multiply the scores and
+// e4m3 caches: K's codes are multiplied as they are, by q split into two terms,
+// hi in e4m3 and lo in e5m2, after a power of two per row that puts its largest
+// |q| into [128, 256).  An element from 2^-6 up (2^-13 of the largest) is exact:
+// hi takes 4 of its 8 bits and leaves at most 8 units of its last place (2^-13
+// at the least), which 3 bits hold.  A smaller one leaves at most 2^-10 to lo,
+// which is off by 2^-14 there, 2^-21 of the largest (with lo in e4m3, whose
+// steps end at 2^-9: exact from 2^-9 of the largest, off by 2^-17).  P and V
+// are f16.  K's block scales multiply the scores and
 // V's enter the exponent, as in row_gqa.cu.
 //
 // A V element that is not finite in a tile that some rows do not see would
@@ -129,8 +133,8 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo,
       "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Same for e4m3 x e4m3
-__device__ __forceinline__ void mma_ss_e4m3(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+// Same for 8-bit inputs
+__device__ __forceinline__ void mma_ss_f8(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
                                             uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %5, 0;\n\t"
@@ -215,6 +219,12 @@ __device__ __forceinline__ void regs_up() {
 template <int N>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// Two floats -> two e5m2 bytes (to nearest even, saturating), `lo` in the low byte.
+__device__ __forceinline__ uint16_t f32x2_to_e5m2x2(float lo, float hi) {
+  uint16_t out;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(out) : "f"(hi), "f"(lo));
+  return out;
 }
 // Byte of 16-byte chunk c (8 dims) of row r in a swizzled two-atom tile.
 __device__ __forceinline__ constexpr int tile_byte(int r, int c) {
@@ -646,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     } else if (warp == kSoftWarps) {
       // ---------------------------------------------------------- MMA
       constexpr uint32_t fmt = KVT == 0 ? 1u : 0u;  // bf16 or f16
-      const uint32_t id_s = umma_idesc(fmt, 128, 128);  // (format 0 is e4m3 among 8-bit operands)
+      const uint32_t id_s = umma_idesc(fmt, 128, 128);  // (format 0 is e4m3 among 8-bit operands, 1 e5m2)
       const uint32_t id_o = id_s | (1u << 16);          // B is N-major
       const uint32_t q0 = desc_lo(smem_addr(sQ), 16), k0 = desc_lo(smem_addr(sK), 16);
       // N-major: the second 64 dims one atom on
@@ -658,8 +668,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
           const int off = (kk & 3) * 32, atom = (kk >> 2) * kAtom;
           if constexpr (KVT == 0)
             mma_ss(tmem + 128 * x, a + ((atom + off) >> 4), b + ((atom + off) >> 4), id_s, kk != 0 ? 1u : 0u);
-          else  // the hi terms, then the lo terms, over the same codes
-            mma_ss_e4m3(tmem + 128 * x, a + ((atom + off) >> 4), b + (off >> 4), id_s, kk != 0 ? 1u : 0u);
+          else  // the hi terms, then the lo terms (A in e5m2), over the same codes
+            mma_ss_f8(tmem + 128 * x, a + ((atom + off) >> 4), b + (off >> 4), kk < 4 ? id_s : id_s | (1u << 7), kk != 0 ? 1u : 0u);
         }
       };
       // O += P V of tile number i
@@ -846,8 +856,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
             e4m3x4_to_f16x2x2(hi[i], b0, b1);
             const float2 y0 = __half22float2(*reinterpret_cast<const __half2*>(&b0));
             const float2 y1 = __half22float2(*reinterpret_cast<const __half2*>(&b1));
-            lo[i] = static_cast<uint32_t>(f32x2_to_e4m3x2(f[4 * i] - y0.x, f[4 * i + 1] - y0.y)) |
-                    (static_cast<uint32_t>(f32x2_to_e4m3x2(f[4 * i + 2] - y1.x, f[4 * i + 3] - y1.y)) << 16);
+            lo[i] = static_cast<uint32_t>(f32x2_to_e5m2x2(f[4 * i] - y0.x, f[4 * i + 1] - y0.y)) |
+                    (static_cast<uint32_t>(f32x2_to_e5m2x2(f[4 * i + 2] - y1.x, f[4 * i + 3] - y1.y)) << 16);
           }
           qs = fmaxf(qs * (KVT == 1 ? P.k_scale : 1.0f) * exp2i(e), kLeast);
           if (peak >= 0x7F80u) qs = -1.0f;

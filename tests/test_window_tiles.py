@@ -8,7 +8,7 @@ import torch
 
 from learned_sparse_attention_gb300 import qsa as Q
 from oracle import qsa_oracle as O
-from tests.attention_bounds import assert_row
+from tests.attention_bounds import assert_row, attend_row
 from tests.oracle_io import f64
 from tests.test_window_gqa import Batch, D
 
@@ -119,3 +119,51 @@ def test_odd_values_in_tiles_reach_only_rows_that_see_them(kind):
     assert np.isfinite(out[sees][:, :, clean]).all() and np.isfinite(out[~sees]).all()
     edge = [i for t in toks for p in (t - 1, t + 63, t + 64) for i in [p - 300] if 0 <= i < 4000]
     check_rows(b, out, [i for i in edge + some(4000) if not sees[i]], 64, 0)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "block"])
+@pytest.mark.parametrize("rows", [8, 1000])
+def test_queries_with_one_loud_element(kind, rows):
+    """Elements down to 2^-11 of their head's largest keep all their bits: keys
+    that are blind to the loud one and weigh the others' last bits against each
+    other get scores that are fp32 sums of exact products.  (Rounded to steps
+    of 2^-19 of the largest, these elements would double the scores.)"""
+    b = Batch([1300], [rows], kind=kind, page=64, block=32, seed=27, hq=2, hkv=1, gate=False)
+    rng = np.random.default_rng(3)
+    q = np.where(np.arange(D) % 2 == 0, 0.5 + 2.0 ** -8, 0.5 + 3 * 2.0 ** -8)
+    q[17] = 1000.0
+    b.q = (torch.from_numpy(q) * torch.from_numpy(rng.choice([-1.0, 1.0], (rows, 2, 1)))).bfloat16()
+    key = np.where(np.arange(D) % 2 == 0, 1.0, -1.0)
+    key[17] = 0.0
+    c = rng.choice([-64.0, -32.0, 16.0, 48.0, 64.0], b.kv.shape[:3] + (1,))
+    b.kv[..., :D] = torch.from_numpy(c * key).to(torch.float8_e4m3fn).view(torch.uint8)
+    b.k_scale = 1.0
+    if kind == "block":
+        b.scales[..., 0] = 127
+    out = b.window(600, 2)
+    assert Q.check_errors() == 0
+    check_rows(b, out, some(rows), 600, 2)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "block"])
+@pytest.mark.parametrize("rows", [8, 1000])
+@pytest.mark.parametrize("ratio", [2.0 ** 14, 2.0 ** 18])
+def test_queries_of_a_wide_range(kind, rows, ratio):
+    """Smaller elements are off by at most 2^-21 of their head's largest, so a
+    score by 2^-21 max|q| sum|k| / sqrt(D) beyond its bound: every weight moves
+    by at most e^2d - 1 of itself, the output by that times sum w|v|."""
+    b = Batch([1300], [rows], kind=kind, page=64, block=32, seed=28, hq=2, hkv=1, gate=False)
+    b.q[:, :, 17] = ratio
+    b.kv[..., 17] = 0
+    if kind == "block":
+        b.scales[..., 0] = 119
+    out = b.window(600, 2)
+    assert Q.check_errors() == 0
+    for i in some(rows):
+        q = f64(b.q[i])
+        K, V = b.values(0, O.window_tokens(int(b.pos[i]), 600, 2))
+        want, bound = attend_row(q, K, V)
+        size = attend_row(q, K, np.abs(V))[0]  # sum w|v|
+        d = (np.abs(K[:, 0]).sum(1) / np.sqrt(D)).max() * np.abs(q).max(1) * 2.0 ** -21
+        more = np.expm1(2 * d)[:, None] * size * (1 + 2.0 ** -6)
+        assert (np.abs(out[i] - want) <= bound * (1 + np.expm1(2 * d)[:, None]) + more).all(), i
