@@ -105,7 +105,7 @@ struct TileShared {
   int first[kSlots][2];            // first key of each half, -1: of two stretches of keys, or not all on pages
   int ns, shift;                   // (of Tiles)
   alignas(16) uint32_t scale[kSlots][8];  // of each 16 keys, two bf16: ks, and log2 vs above it
-  float qs[256];                   // per M row: what its scores are multiplied by (< 0: the row is a NaN)
+  float qs[256];                   // per M row: what its scores are multiplied by (< 0: its scores are NaN)
   float pair[2][2][256];           // what a row's two threads tell each other
   float join[2][128];              // tile B's sums and references, where it has the same rows as A
 };
@@ -860,7 +860,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
                     (static_cast<uint32_t>(f32x2_to_e5m2x2(f[4 * i + 2] - y1.x, f[4 * i + 3] - y1.y)) << 16);
           }
           qs = fmaxf(qs * (KVT == 1 ? P.k_scale : 1.0f) * exp2i(e), kLeast);
-          if (peak >= 0x7F80u) qs = -1.0f;
+          if (peak >= 0x7F80u) {  // not finite: NaN codes, which make every score that is seen a NaN
+            qs = -1.0f;
+            hi[0] = hi[1] = 0x7F7F7F7Fu;
+          }
           // the hi terms' atom, then the lo terms'
           uint8_t* dst = tile + im * 128 + (((lane16 >> 1) ^ (im & 7)) << 4) + (lane16 & 1) * 8;
           *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
@@ -884,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
     const int hi_all = __reduce_min_sync(0xffffffffu, pos >= 0 ? p : INT_MAX);
     const int lo_all = __reduce_max_sync(0xffffffffu, pos >= 0 ? p - P.window + 1 : INT_MIN);
     // (a row that sees nothing never asks for a reference)
-    float ref = pos >= 0 && sh.qs[m] > 0.f ? -INFINITY : 0.f, l = sh.qs[m] < 0.f ? __int_as_float(0x7fffffff) : 0.f;
+    float ref = pos >= 0 && sh.qs[m] > 0.f ? -INFINITY : 0.f, l = 0.f;
     // (a wait that gives up ends the waiting, not the loop: the two warps
     // always meet)
     bool ok = true;

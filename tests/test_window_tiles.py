@@ -167,3 +167,21 @@ def test_queries_of_a_wide_range(kind, rows, ratio):
         d = (np.abs(K[:, 0]).sum(1) / np.sqrt(D)).max() * np.abs(q).max(1) * 2.0 ** -21
         more = np.expm1(2 * d)[:, None] * size * (1 + 2.0 ** -6)
         assert (np.abs(out[i] - want) <= bound * (1 + np.expm1(2 * d)[:, None]) + more).all(), i
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows", [60, 6000])
+def test_odd_queries_that_see_nothing_are_zero(kind, rows):
+    """A query that is not finite makes what it sees a NaN, and nothing of a
+    window that lies on pages outside the cache."""
+    b = Batch([rows + 240], [rows], kind=kind, page=16, block=16, seed=29, hq=2, hkv=1, gate=False)
+    b.table[0, 16:18] = b.blocks, -1       # tokens 256 .. 287, the window of position 287
+    i = 287 - 240
+    b.q[i, 0, 3], b.q[i, 1, 100] = float("nan"), float("inf")
+    b.q[i - 1, 0, 3], b.q[7, 1, 5] = float("nan"), float("-inf")
+    out = b.window(32, 0)
+    assert Q.check_errors() > 0
+    assert (out[i] == 0).all()
+    assert np.isnan(out[i - 1, 0]).all() and np.isnan(out[7, 1]).all()
+    assert np.isfinite(out[i - 1, 1]).all() and np.isfinite(out[7, 0]).all()
+    check_rows(b, out, [r for r in some(rows) if r not in (i, i - 1, 7)], 32, 0, lost=np.arange(256, 288))
