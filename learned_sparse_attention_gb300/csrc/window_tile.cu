@@ -81,6 +81,7 @@ constexpr int kPoison = 32;      // tiles that can remember odd V elements
 template <int KVT>
 constexpr float kRoom = KVT == 0 ? 7.0f : 0.0f;
 constexpr uint32_t kTwo = 0x40004000u;
+constexpr float kFar = 1048576.f;  // 2^20: fp32 steps of 2^-3
 constexpr float kLeast = 1.2e-38f;  // a score's factor is never 0: masked scores are -inf
 
 // The rings.  e4m3 caches: K tiles stay codes, half the size, and V's codes
@@ -930,7 +931,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       // is it moved and the tile done again.  (S is in place until P is
       // stored, and P is stored only after the two warps have met: the second
       // half's lies over the first half's S.)
-      bool moved = __any_sync(0xffffffffu, ref == -INFINITY);
+      // A reference beyond 2^20 is looked at in every tile.
+      bool moved = __any_sync(0xffffffffu, !(fabsf(ref) <= kFar));
       uint32_t pk[32];
       float sum;
 #pragma unroll 1
@@ -954,6 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
             for (int i = 0; i < 32; ++i) r[c][i] = (vis & (1u << i)) != 0u ? r[c][i] : 0xFF800000u;
           }
         }
+        bool far = false;
         if (moved) {
           float mx = -INFINITY;
 #pragma unroll
@@ -976,6 +979,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
             }
           }
           ref = mn;
+          // Further out an unrounded product less the rounded reference leaves a
+          // weight's range: exponents are rounded first, as the reference was.
+          far = __any_sync(0xffffffffu, fabsf(ref) > kFar && ref != -INFINITY);
+          if (far) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) r[i >> 5][i & 31] = __float_as_uint(exponent(__uint_as_float(r[i >> 5][i & 31]), i >> 4));
+          }
         }
         const float neg_ref = ref == -INFINITY ? 0.f : -ref;
         unsigned long long sum2 = 0ull;  // (two sums, of even and odd keys)
@@ -985,10 +995,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           const uint32_t* rr = &r[b >> 1][16 * (b & 1)];
-          float f = qs, base = neg_ref, inv_vs = 1.0f;
+          float f = far ? 1.0f : qs, base = neg_ref, inv_vs = 1.0f;
           if constexpr (KVT == 2) {
-            f = fmaxf(f * bf16_lo(sc[b]), kLeast);
-            base += bf16_hi(sc[b]);
+            if (!far) {
+              f = fmaxf(f * bf16_lo(sc[b]), kLeast);
+              base += bf16_hi(sc[b]);
+            }
             inv_vs = ex2_ftz(-bf16_hi(sc[b]));
           }
           const unsigned long long f2 = f32x2_pack(f, f), base2 = f32x2_pack(base, base);

@@ -185,3 +185,34 @@ def test_odd_queries_that_see_nothing_are_zero(kind, rows):
     assert np.isnan(out[i - 1, 0]).all() and np.isnan(out[7, 1]).all()
     assert np.isfinite(out[i - 1, 1]).all() and np.isfinite(out[7, 0]).all()
     check_rows(b, out, [r for r in some(rows) if r not in (i, i - 1, 7)], 32, 0, lost=np.arange(256, 288))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows", [5, 1000])
+@pytest.mark.parametrize("size", [2.0 ** 24, 2.0 ** 34, 2.0 ** 60])
+def test_scores_beyond_fp32_steps_of_one(kind, rows, size):
+    """Scores so large that neighbouring fp32 values are further apart than a
+    weight's range pick the best token, not an infinity or a NaN."""
+    b = Batch([1300], [rows], kind=kind, page=64, block=32, seed=30, hq=2, hkv=1, gate=False)
+    b.q *= size / 2.0 ** 15
+    if kind == "bf16":
+        b.kv[..., :D] *= 2.0 ** 15
+    elif kind == "e4m3":
+        b.k_scale = 2.0 ** 10
+    else:
+        b.scales[..., 0] = 127 + 10
+    out = b.window(300, 2)
+    assert Q.check_errors() == 0 and np.isfinite(out).all()
+    checked = 0
+    for i in some(rows):
+        K, V = b.values(0, O.window_tokens(int(b.pos[i]), 300, 2))
+        for h in range(2):
+            z = K[:, 0] @ f64(b.q[i])[h] / np.sqrt(D)
+            top = np.argsort(z)[-2:]
+            # a score's error is at most 2^-24 * 130 of sum |q k| / sqrt(D)
+            off = 130 * 2.0 ** -24 * (np.abs(K[:, 0]) @ np.abs(f64(b.q[i])[h])).max() / np.sqrt(D)
+            if z[top[1]] - z[top[0]] > 2 * off + 100:
+                v = V[top[1], 0]
+                assert (np.abs(out[i, h] - v) <= 2.0 ** -8 * np.abs(v) + 1e-30).all(), (i, h)
+                checked += 1
+    assert checked > len(some(rows))
