@@ -441,7 +441,9 @@ qsa_status qsa_kv_append(const qsa_cfg* cfg, const qsa_gqa_cfg* gcfg, const qsa_
  * qsa_sparse_gqa_scaled -- qsa_sparse_gqa over a cache with block scales
  * (gcfg->kv_dtype QSA_DTYPE_E4M3_BLOCK).  Arguments and results are those of
  * qsa_sparse_gqa; each score takes its token's K scale and each value its
- * token's V scale.  ws: qsa_workspace_bytes() bytes for this gcfg.
+ * token's V scale.  ws: qsa_workspace_bytes() bytes for this gcfg, rows and
+ * packed_width (= token_topk + compress_ratio), which are enough for fewer
+ * rows and narrower selections too.
  *  reqs   rows of block_table; a row whose token_to_req is outside [0, reqs)
  *         is counted and gets zeros
  */
@@ -501,8 +503,11 @@ typedef struct qsa_window_args {
 qsa_status qsa_window_gqa(const qsa_gqa_cfg* gcfg, const qsa_window_args* args, void* ws,
                           size_t ws_bytes, void* stream);
 
-/* Scratch bytes of qsa_window_gqa for these sizes (the pointers are not read;
- * 0: none needed, or invalid sizes). */
+/* Scratch bytes of qsa_window_gqa for these sizes and for every call of this
+ * gcfg, of any reqs, whose rows, window, sinks and max_context are no larger:
+ * some of those need more than the largest does, and a buffer of this size
+ * serves them all (the pointers are not read; 0: none needed, or invalid
+ * sizes). */
 size_t qsa_window_workspace_bytes(const qsa_gqa_cfg* gcfg, const qsa_window_args* args);
 
 /* Scratch bytes needed by qsa_layer_step (and enough for every stage call)

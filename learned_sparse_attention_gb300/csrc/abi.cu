@@ -189,9 +189,36 @@ size_t rows_ws_bytes(const qsa_gqa_cfg* g, int rows, int splits) {
   return row_gqa_cluster(rows, g->num_kv_heads, splits, sm_count()) ? 0 : row_ws_bytes(g, rows, splits);
 }
 
+// Fewer rows are split further, and more of them are joined without scratch, so
+// that a call's own need rises and falls with its sizes.  The two below are the
+// most that calls of up to `rows` rows and `tokens` tokens a row need (of
+// single rows, then of tiles): both needs only grow with the tokens, and no
+// split is left where the rows alone fill the device.
+size_t rows_ws_bound(const qsa_gqa_cfg* g, int rows, long long tokens) {
+  const int full = 2 * sm_count() / g->num_kv_heads;
+  size_t most = 0;
+  for (int r = 1; r <= rows && r <= full; ++r) {
+    const size_t n = rows_ws_bytes(g, r, row_gqa_splits(r, g->num_kv_heads, tokens, g->kv_dtype, sm_count()));
+    if (n > most) most = n;
+  }
+  return most;
+}
+size_t tiles_ws_bound(const qsa_gqa_cfg* g, int rows, long long tokens) {
+  const int group = g->num_q_heads / g->num_kv_heads;
+  size_t most = 0;
+  // (by full row groups of one request: more requests make more groups)
+  const int per = window_tile_rows(group), full = sm_count() / g->num_kv_heads;
+  for (int k = 1; k <= full; ++k) {
+    const int r = rows / per >= k ? k * per : rows;
+    const size_t n = row_ws_bytes(g, r, window_tile_splits(r, 1, g->num_kv_heads, group, tokens, sm_count()));
+    if (n > most) most = n;
+    if (r == rows) break;
+  }
+  return most;
+}
+
 size_t gqa_ws_bytes(const qsa_gqa_cfg* g, int rows, int packed_width) {
-  if (g->kv_dtype == QSA_DTYPE_E4M3_BLOCK)
-    return rows_ws_bytes(g, rows, row_gqa_splits(rows, g->num_kv_heads, packed_width - 1, g->kv_dtype, sm_count()));
+  if (g->kv_dtype == QSA_DTYPE_E4M3_BLOCK) return rows_ws_bound(g, rows, packed_width - 1);
   return gqa_layout(g, rows, packed_width).total;
 }
 
@@ -1018,8 +1045,9 @@ qsa_status qsa_window_gqa(const qsa_gqa_cfg* gcfg, const qsa_window_args* args, 
 
 size_t qsa_window_workspace_bytes(const qsa_gqa_cfg* gcfg, const qsa_window_args* args) {
   if (check_window(gcfg, args) != QSA_OK || args->rows == 0) return 0;
-  const WindowPlan plan = window_plan(gcfg, args);
-  return plan.tile ? row_ws_bytes(gcfg, args->rows, plan.splits) : rows_ws_bytes(gcfg, args->rows, plan.splits);
+  const size_t rows = rows_ws_bound(gcfg, args->rows, window_tokens(args));
+  const size_t tiles = tiles_ws_bound(gcfg, args->rows, window_tokens(args));
+  return rows > tiles ? rows : tiles;
 }
 
 qsa_status qsa_mtp_steps(const qsa_cfg* cfg, const qsa_gqa_cfg* gcfg, const qsa_step_args* steps,

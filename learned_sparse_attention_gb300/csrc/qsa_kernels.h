@@ -173,6 +173,7 @@ cudaError_t launch_row_gqa(const RowGqaParams& p, cudaStream_t stream);
 // Joins the splits that p's launch left in part_o and part_lse.
 cudaError_t launch_row_merge(const RowGqaParams& p, cudaStream_t stream);
 // Window attention by tiles of 128 (row, head) pairs of one request.
+int window_tile_rows(int group);                              // rows of a CTA
 long long window_tile_groups(int rows, int reqs, int group);  // CTAs of a KV head and split
 int window_tile_splits(int rows, int reqs, int hkv, int group, long long max_tokens, int sms);
 // tmap: the cache as [blocks * Hkv * page, 256] with a box of 128 bytes x

@@ -1163,12 +1163,11 @@ cudaError_t launch_kind(const RowGqaParams& p, const CUtensorMap& tmap, const di
 
 }  // namespace
 
-// Rows of a CTA.
-static int tile_rows(int group) { return 2 * (128 / group); }
+int window_tile_rows(int group) { return 2 * (128 / group); }
 
 // (at the least: a request's last group may be a part of one)
 long long window_tile_groups(int rows, int reqs, int group) {
-  const int per = tile_rows(group);
+  const int per = window_tile_rows(group);
   const long long groups = (static_cast<long long>(rows) + per - 1) / per;
   return groups < reqs ? (reqs < rows ? reqs : rows) : groups;
 }
@@ -1187,7 +1186,7 @@ int window_tile_splits(int rows, int reqs, int hkv, int group, long long max_tok
 
 cudaError_t launch_window_tile(const RowGqaParams& p, const CUtensorMap& tmap, cudaStream_t stream) {
   if (p.rows == 0) return cudaSuccess;
-  long long groups = static_cast<long long>(p.rows) / tile_rows(p.group) + p.reqs;
+  long long groups = static_cast<long long>(p.rows) / window_tile_rows(p.group) + p.reqs;
   if (groups > p.rows) groups = p.rows;
   const dim3 grid(static_cast<unsigned>(groups), p.hkv, p.splits);
   cudaError_t e;

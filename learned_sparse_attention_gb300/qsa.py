@@ -515,6 +515,8 @@ def window_args(q, kv, block_table, token_to_req, query_start_loc, logical_posit
 
 
 def window_workspace_bytes(gcfg, args: QsaWindowArgs) -> int:
+    """Scratch bytes of window_gqa for calls up to these sizes
+    (qsa_window_workspace_bytes)."""
     return int(load().qsa_window_workspace_bytes(ctypes.byref(gcfg), ctypes.byref(args)))
 
 

@@ -216,3 +216,51 @@ def test_scores_beyond_fp32_steps_of_one(kind, rows, size):
                 assert (np.abs(out[i, h] - v) <= 2.0 ** -8 * np.abs(v) + 1e-30).all(), (i, h)
                 checked += 1
     assert checked > len(some(rows))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("hq,hkv", [(8, 1), (8, 2)])
+def test_workspace_of_the_largest_call_serves_smaller_ones(kind, hq, hkv):
+    """Single rows with one split, joined in a cluster and joined by a second
+    launch, tiles with and without splits, in one buffer."""
+    b = Batch([4100], [256], hq=hq, hkv=hkv, kind=kind, page=64, block=32, seed=34)
+    b.table = b.table.repeat(256, 0)  # (requests that share their pages)
+    d = b.to_gpu()
+
+    def args(rows, reqs, context):
+        qsl = torch.arange(reqs + 1, dtype=torch.int32, device="cuda") * (rows // reqs)
+        t2r = torch.arange(rows, dtype=torch.int32, device="cuda") // (rows // reqs)
+        pos = context - rows // reqs + torch.arange(rows, dtype=torch.int32, device="cuda") % (rows // reqs)
+        return Q.window_args(d["q"][:rows], d["kv"], d["table"], t2r, qsl, pos, torch.empty_like(d["q"][:rows]), 100000, 0,
+                             context, gate=d["gate"][:rows], scales=b.sc)
+
+    most = Q.window_workspace_bytes(b.gcfg(), args(256, 256, 4100))
+    shared = torch.full((most,), 0xFF, dtype=torch.uint8, device="cuda")
+    for rows, reqs in [(256, 256), (256, 1), (64, 64), (64, 2), (48, 1), (16, 16), (8, 8), (5, 5), (4, 1), (1, 1)]:
+        for context in (4100, 1100, 300):
+            a = args(rows, reqs, context)
+            Q.window_gqa(b.gcfg(), a, shared)
+            own = Q.window_workspace_bytes(b.gcfg(), a)
+            assert own <= most
+            out = a._tensors[7].clone()
+            Q.window_gqa(b.gcfg(), a, torch.empty(own, dtype=torch.uint8, device="cuda") if own else None)
+            assert torch.equal(out, a._tensors[7]) and not torch.isnan(out.float()).any()
+    assert Q.check_errors() == 0
+
+
+def test_selection_workspace_of_the_largest_call_serves_smaller_ones():
+    b = Batch([4200], [256], hq=8, hkv=1, kind="block", page=64, block=32, seed=35)
+    b.table, b.t2r = b.table.repeat(256, 0), np.arange(256, dtype=np.int32)
+    d = b.to_gpu()
+    cfg = Q.make_cfg(8, 4, 4096, Q.DTYPE_BF16, 4, 1)
+    ws = torch.full((Q.workspace_bytes(cfg, b.gcfg(), 256, 256, 0),), 0xFF, dtype=torch.uint8, device="cuda")
+    for width in (4100, 1028, 260):
+        packed = torch.arange(width, dtype=torch.int32, device="cuda").repeat(256, 1)
+        packed[:, -1] = width - 1
+        for rows in (256, 100, 64, 16, 8, 5, 1):
+            Q.sparse_gqa_scaled(b.gcfg(), b.sc, d["q"][:rows], d["kv"], d["table"], packed[:rows], d["t2r"][:rows],
+                                d["gate"][:rows], d["out"][:rows], ws)
+            for i in {0, rows - 1}:
+                K, V = b.values(i, np.arange(width - 1))
+                assert_row(f64(d["out"][i]), f64(b.q[i]), K, V, f64(b.gate[i]), f"row {i} of {rows}")
+    assert Q.check_errors() == 0
