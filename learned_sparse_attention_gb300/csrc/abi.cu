@@ -705,17 +705,19 @@ long long window_tokens(const qsa_window_args* a) {
 // Tiles or single rows, and how many splits of them: whichever the sizes make
 // the faster one, by estimates of their times in us.
 //   rows   6, + 48 (e4m3: 37) for each million of row tokens and KV heads, +
-//          2 for each further wave of two CTAs an SM, + 2 for a merge;
+//          2 for each further wave of two CTAs an SM, + 2 for a second launch
+//          that joins splits;
 //   tiles  for each wave of one CTA an SM 9 + 1.5 a tile of 128 keys, however
 //          many rows share it (e4m3 where a request's rows fit one row tile:
-//          1.1), + 6 for a merge.
-// Measured, both ways (tiles / rows, us): window 4096, 8 heads a KV head, 4 KV
-// heads, 64 requests of 1 row 89 / 48 and of 3 rows 91 / 130 (block scales), of
-// 2 rows 108 / 107 and of 3 rows 110 / 157 (bf16); 32 of 4 rows 56 / 109; one of
-// 8 rows 18 / 15, of 24 rows 22 / 25, of 48 rows 26 / 53; 16 of 8 rows and one
-// head a KV head 36 / 104; window 256, 4 of 16 rows 14 / 9, 64 of 4 rows 28 / 26.
-// Over 53 such sizes the estimates' choice took 1.00 of the faster one's time on
-// average, 1.09 at worst.
+//          1.1), + 6 where splits are joined.
+// Measured, both ways, L2 flushed before each call (tiles / rows, us, a graph's
+// launch included): window 4096, 8 heads a KV head, 4 KV heads, 64 requests of 1
+// row 100 / 67 and of 3 rows 102 / 136 (block scales), of 2 rows 126 / 122 and of
+// 3 rows 126 / 165 (bf16); 32 of 4 rows 72 / 111; one of 8 rows 25 / 21, of 24
+// rows 29 / 31, of 48 rows 33 / 60; 16 of 8 rows and one head a KV head 48 / 110;
+// window 256, 4 of 16 rows 20 / 16, 64 of 4 rows 37 / 36.  Over 52 such sizes the
+// estimates' choice took 1.005 of the faster one's time on average, 1.14 at
+// worst (24 rows, block scales, 33 / 29); with inputs in L2 1.003 and 1.09.
 struct WindowPlan {
   bool tile;
   int splits;
@@ -727,7 +729,8 @@ WindowPlan window_plan(const qsa_gqa_cfg* g, const qsa_window_args* a) {
   const int row_splits = row_gqa_splits(a->rows, g->num_kv_heads, n, g->kv_dtype, sms);
   const double pairs = static_cast<double>(a->rows) * g->num_kv_heads;
   const double row_us = 6.0 + pairs * n * (g->kv_dtype == QSA_DTYPE_BF16 ? 48e-6 : 37e-6) +
-                        2.0 * (waves(pairs * row_splits, 2 * sms) - 1.0) + (row_splits > 1 ? 2.0 : 0.0);
+                        2.0 * (waves(pairs * row_splits, 2 * sms) - 1.0) +
+                        (row_splits > 1 && !row_gqa_cluster(a->rows, g->num_kv_heads, row_splits, sms) ? 2.0 : 0.0);
   const int tile_splits = window_tile_splits(a->rows, a->reqs, g->num_kv_heads, group, n, sms);
   const double ctas = static_cast<double>(window_tile_groups(a->rows, a->reqs, group)) * g->num_kv_heads * tile_splits;
   const double tiles = std::ceil((n + 127) / 128.0 / tile_splits);

@@ -607,12 +607,13 @@ cudaError_t launch_kind(const RowGqaParams& p, cudaStream_t stream) {
 }  // namespace
 
 // As many splits as keep the CTAs in one wave at two per SM (shared memory): a
-// second wave, or a row cut finer than that, costs more than it evens out (64
-// rows x 4 KV heads of 4100 tokens, e4m3: 1 split 50 us, 2 splits 60 us; 8 rows
-// x 8 of 4103: 4 splits 27 us, 5 splits 30 us).  A warp has two slabs at the
-// least, and the join, which reads a partial for each split, keeps their square
-// to a twelfth of the tokens (one row and KV head of 4100 tokens, bf16: 8
-// splits 11.7 us, 16 10.7, 22 10.5, 33 11.6).
+// second wave, or a row cut finer than that, costs more than it evens out (L2
+// flushed before each call: 64 rows x 4 KV heads of 4100 tokens, e4m3, 1 split
+// 65 us, 2 splits 73; 8 rows x 8 of 4103, 3 splits 34 us, 4 splits 32, 5 splits
+// 40).  A warp has two slabs at the least, and the join, which reads a partial
+// for each split, keeps their square to a twelfth of the tokens (one row and KV
+// head of 4100 tokens, bf16: 4 splits 21.8 us, 8 to 22 splits 17.5, 33 splits
+// 19.6).
 int row_gqa_splits(int rows, int hkv, long long max_tokens, int kv_dtype, int sms) {
   const long long base = static_cast<long long>(rows) * hkv;
   if (base <= 0) return 1;
@@ -627,9 +628,9 @@ int row_gqa_splits(int rows, int hkv, long long max_tokens, int kv_dtype, int sm
 
 // Up to eight splits of a row and KV head are a cluster and join through its
 // shared memory, without the partials' way through memory and a second launch
-// (8 rows x 8 KV heads in 4 splits 19.1 -> 18.3 us, one row in 5 splits 7.2 ->
-// 6.6); not where the launch nearly fills the SMs, whose groups may then hold
-// fewer clusters than single CTAs.
+// (8 rows x 8 KV heads in 4 splits 33.9 -> 31.9 us, two rows x 4 KV heads in 8
+// splits 19.6 -> 17.6, L2 flushed before each call); not where the launch nearly
+// fills the SMs, whose groups may then hold fewer clusters than single CTAs.
 bool row_gqa_cluster(int rows, int hkv, int splits, int sms) {
   return splits > 1 && splits <= 8 && static_cast<long long>(rows) * hkv * splits <= 2 * sms * 85 / 100;
 }
