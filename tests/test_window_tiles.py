@@ -264,3 +264,57 @@ def test_selection_workspace_of_the_largest_call_serves_smaller_ones():
                 K, V = b.values(i, np.arange(width - 1))
                 assert_row(f64(d["out"][i]), f64(b.q[i]), K, V, f64(b.gate[i]), f"row {i} of {rows}")
     assert Q.check_errors() == 0
+
+
+@pytest.mark.parametrize("rows", [8, 1000])
+def test_scale_bytes_at_and_past_their_ends(rows):
+    """V scales over all of 2^-40 .. 2^40 and bytes outside, which are read as
+    the nearest of them; K scales from the ordinary down."""
+    b = Batch([1300], [rows], kind="block", page=64, block=16, seed=31, hq=8, hkv=2)
+    rng = np.random.default_rng(2)
+    b.scales[..., 0] = torch.from_numpy(rng.choice([0, 87, 100, 118, 122], b.scales.shape[:-1]).astype(np.uint8))
+    b.scales[..., 1] = torch.from_numpy(rng.choice([0, 87, 100, 127, 140, 167, 255], b.scales.shape[:-1]).astype(np.uint8))
+    out = b.window(600, 2)
+    assert Q.check_errors() == 0
+    check_rows(b, out, some(rows), 600, 2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("splits", [False, True])
+def test_tiles_captured_and_replayed(kind, splits):
+    """A chunk (of a short context: one split; of a long one: several) as a
+    graph, replayed on new rows with another's leavings in the workspace."""
+    contexts = [9000] if splits else [700, 650]
+    rows = [200] if splits else [700, 500]
+    make = lambda seed: Batch(contexts, rows, hq=8, hkv=2, kind=kind, page=64, block=32, seed=seed)  # noqa: E731
+    b = make(32)
+    b.window(20000, 0)
+    d = b.d
+    a = Q.window_args(d["q"], d["kv"], d["table"], d["t2r"], d["qsl"], d["pos"], d["out"], 20000, 0, max(contexts),
+                      gate=d["gate"], scales=b.sc)
+    n = Q.window_workspace_bytes(b.gcfg(), a)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Q.window_gqa(b.gcfg(), a, ws)
+    c = make(33)
+    c.to_gpu()
+    for k in ("q", "kv", "table", "gate", "scales"):
+        if d[k] is not None:
+            d[k].copy_(c.d[k])
+    ws.fill_(0xFF)
+    d["out"].fill_(7.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    check_rows(c, f64(d["out"]), some(c.n, 12), 20000, 0)
+    assert Q.check_errors() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_prompt_that_sees_all_before_it(kind):
+    """Plain causal attention: windows back to token 0, from a row of one token
+    to one of thousands, and a second request that goes on from 900."""
+    b = Batch([3500, 1600], [3500, 700], hq=8, hkv=2, kind=kind, page=64, block=32, seed=36)
+    out = b.window(2 ** 31 - 1, 0)
+    assert Q.check_errors() == 0
+    check_rows(b, out, some(b.n, 20) + [1, 127, 128, 3499, 3500], 2 ** 31 - 1, 0)
