@@ -396,7 +396,9 @@ qsa_status qsa_mtp_steps(const qsa_cfg* cfg, const qsa_gqa_cfg* gcfg, const qsa_
  * The scales of a QSA_DTYPE_E4M3_BLOCK cache.  A token's K of one KV head is
  * code * 2^(b - 127), b the K byte of its block of scale_block tokens, and V
  * likewise.  Bytes stand for 2^-40 .. 2^40 (87 .. 167); others are read as
- * the nearest of them.
+ * the nearest of them.  The readers hold a softmax weight and its V scale as one
+ * f16: a token whose product of the two is below 2^-24 of its row's largest adds
+ * nothing to the output.
  *  scales       [num_blocks, Hkv, page_size / scale_block, 2] bytes: K, V;
  *               4-byte aligned
  *  scale_block  tokens per scale: 16, 32 or 64, a divisor of page_size

@@ -21,8 +21,9 @@
 // (16 bytes a lane).  With block scales a CTA holds a run's keys and values
 // of one KV head in registers between the maximum and the rounding (2, 4 or 8
 // tokens a half-warp), so they are read once.
-// Measured, 32 query and 4 KV heads, blocks of 32: 16 384 rows with queries
-// 112 us (5.2 TB/s of reads and writes), 64 rows 3.9 us, 128 rows 6.0 us.
+// Measured, 32 query and 4 KV heads, blocks of 32, ten calls on ten sets of
+// inputs: 16 384 rows with queries 114 us (5.1 TB/s of reads and writes), 64 rows
+// 4.0 us, 128 rows 6.4 us.
 #include "kv_scale.cuh"
 #include "qsa_device.cuh"
 #include "qsa_kernels.h"
@@ -338,14 +339,15 @@ cudaError_t launch_nt(AppendParams p, cudaStream_t stream) {
   // SM 113 and 126 us).  One kernel's registers would keep queries from having
   // their loads in flight, and a CTA for each of 16 384 rows and heads takes
   // longer to start than to run (250 us).  Below, where a launch weighs more,
-  // one launch of a CTA per row (and KV head).  Two launches / one, us: 512 rows
-  // of one sequence 9.1 / 9.2 and of 512 sequences 16.0 / 15.6, 1024 rows 11.5 /
-  // 15.7 and 25.6 / 28.7.
+  // one launch of a CTA per row (and KV head).  Two launches / one, us (inputs in
+  // L2): 512 rows of one sequence 9.1 / 9.2 and of 512 sequences 16.0 / 15.6,
+  // 1024 rows 11.5 / 15.7 and 25.6 / 28.7.
   const bool many = p.rows >= 1024;
   p.chunk = NT > 0 && many ? kHalves * NT : 1;
   const int chunks = (p.rows + p.chunk - 1) / p.chunk;
   // (a chunk may be one run or, in a decode batch, a run a row: while there is
-  // room, several CTAs share its runs; 1024 sequences of a row 47 -> 25.6 us)
+  // room, several CTAs share its runs; 1024 sequences of a row 47 -> 25.6 us with
+  // inputs in L2, 32.5 without)
   const int parts = many ? 6 * sm_count() / (chunks * p.hkv) : 1;
   p.parts = parts < 1 ? 1 : parts > 16 ? 16 : parts;
   p.kv_ctas = NT > 0 ? chunks * p.hkv * p.parts : chunks;

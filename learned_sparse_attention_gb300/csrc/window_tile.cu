@@ -40,15 +40,18 @@
 // request's start see nothing and set no masks: their sums are not used.
 // Every wait is bounded (mbar_wait); a timeout sets the error word.
 //
+// Roundings: as in row_gqa.cu (the A operand in TMEM has V's type).
+//
 // Bound: the tensor cores in the loop (a tile's S of 128 x 128 x 128 and its
 // product with V take ~1270 cycles, and a row group's tile waits ~1600 for its
 // weights while the other group's products take ~1060: 2900 cycles for two
 // groups and 128 keys), fixed costs for short windows (~10 000 cycles to the
-// first S, ~8 000 from the last weights to the end).  Measured, 32 query and 4
-// KV heads, window 4096, 4 sinks: 16 384 rows 804 us (1.37 PFLOP/s), 8192 rows
-// 406 us on bf16 and 434 us with block scales; 32 requests of 4 rows 56 us on
-// bf16 (4.9 TB/s) and 47 us with block scales; 3 requests of ~1000 to 2011 rows, 24 query heads, window 1000:
-// 106 us.
+// first S, ~8 000 from the last weights to the end) and, at one CTA an SM, the
+// last wave.  Measured, 32 query and 4 KV heads, window 4096, 4 sinks, ten calls
+// on ten sets of inputs: 16 384 rows 813 us (1.35 PFLOP/s), 8192 rows 409 us on
+// bf16 and 435 us with block scales; 32 requests of 4 rows 57 us on bf16 (4.8
+// TB/s) and 49 us with block scales; 3 requests of ~1200 to 2011 rows, 24 query
+// heads, window 1000: 109 us (484 CTAs, 3.2 waves that take four).
 // Without the softmax the loads and products alone took 374 us for the 8192
 // rows.
 #include <cuda_fp16.h>
