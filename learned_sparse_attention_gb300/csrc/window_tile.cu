@@ -97,6 +97,15 @@ struct Rings {
   static_assert(kSlots > NK + 2, "a slot is rewritten only after its tile's softmax");
 };
 
+// A CTA's rows and the places of its keys, for the rare questions what they see.
+struct Rows {
+  const int32_t* positions;
+  int n, window, sinks;
+  int ns, shift;  // (of Tiles)
+  bool apart;     // there may be keys between their windows that nobody sees
+  unsigned long long* err;
+};
+
 struct TileShared {
   uint64_t kfull[3], kempty[3], vfull[2], vempty[2], vgo[2], rfull[2], rempty[2];
   uint64_t info[kSlots], s_full[2], p_ready[2], q_ready[2], o_full[2], loads_done;
@@ -108,6 +117,7 @@ struct TileShared {
   int check[kSlots];               // some key is not
   int first[kSlots][2];            // first key of each half, -1: of two stretches of keys, or not all on pages
   int ns, shift;                   // (of Tiles)
+  Rows rows[3];                    // of the warps that load, one each
   alignas(16) uint32_t scale[kSlots][8];  // of each 16 keys, two bf16: ks, and log2 vs above it
   float qs[256];                   // per M row: what its scores are multiplied by (< 0: its scores are NaN)
   float pair[2][2][256];           // what a row's two threads tell each other
@@ -273,32 +283,69 @@ struct Tiles {
   __device__ __forceinline__ int key(int v) const { return v < ns ? v : v + shift; }
 };
 
-__device__ __noinline__ void file_poison(TileShared* sh, int v, uint32_t* odd_keys, unsigned long long* err) {
+// Whether one of the rows sees one of the keys a .. b (a warp's question).
+__device__ __forceinline__ bool rows_see(const Rows* rows, int a, int b) {
+  bool yes = false;
+#pragma unroll 1
+  for (int r = threadIdx.x & 31; r < rows->n; r += 32) {
+    const int p = min(rows->positions[r], kMaxKeys);  // (as window_position; below 0 it sees none)
+    yes |= p >= a && (a < rows->sinks || (rows->window > 0 && b > p - rows->window));
+  }
+  return __any_sync(0xffffffffu, yes);
+}
+
+// Counts an error where one of them sees a key of the 16-key blocks `blocks` of
+// the tile from v on.
+__device__ __noinline__ void count_blocks(const Rows* rows, int v, unsigned blocks) {
+  bool seen = !rows->apart;
+#pragma unroll 1
+  for (; blocks != 0u && !seen; blocks &= blocks - 1u) {
+    const int k0 = Tiles{rows->ns, rows->shift, 0}.key(v + 16 * (__ffs(blocks) - 1));
+    seen = rows_see(rows, k0, k0 + 15);
+  }
+  if (seen && (threadIdx.x & 31) == 0) flag_error(rows->err);
+}
+
+// Files the odd keys that a warp has found in the tile from v on, but for those
+// that nobody sees.
+__device__ __noinline__ void file_poison(TileShared* sh, int which, int v) {
+  const Rows* rows = &sh->rows[which];
+  uint32_t* odd_keys = sh->odd_keys[which & 1];
+  const Tiles T{rows->ns, rows->shift, 0};
+  __syncwarp();
+  uint32_t odd[4], any = 0u;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    odd[w] = odd_keys[w];
+    const int k = v + 32 * w;
+    if (rows->apart && odd[w] != 0u) {
+      uint32_t look = rows_see(rows, T.key(k), T.key(k + 31)) ? odd[w] : 0u;
+      odd[w] = 0u;
+#pragma unroll 1
+      for (; look != 0u; look &= look - 1u) {
+        const int key = T.key(k + __ffs(look) - 1);
+        if (rows_see(rows, key, key)) odd[w] |= look & -look;
+      }
+    }
+    any |= odd[w];
+  }
   __syncwarp();
   if ((threadIdx.x & 31) == 0) {
-    int b = 0;
-    for (; b < kPoison; ++b) {
-      const int was = atomicCAS(&sh->poison_tile[b], -1, v);
-      if (was == -1 || was == v) break;
+    int b = kPoison;
+    if (any != 0u) {
+      for (b = 0; b < kPoison; ++b) {
+        const int was = atomicCAS(&sh->poison_tile[b], -1, v);
+        if (was == -1 || was == v) break;
+      }
+      if (b == kPoison) flag_error(rows->err);
     }
-    if (b == kPoison) flag_error(err);
+#pragma unroll
     for (int w = 0; w < 4; ++w) {
-      if (b < kPoison) atomicOr(&sh->poison[b][w], odd_keys[w]);
+      if (b < kPoison) atomicOr(&sh->poison[b][w], odd[w]);
       odd_keys[w] = 0u;
     }
   }
   __syncwarp();
-}
-
-// Whether one of the rows at these positions sees one of the keys a .. b.
-// (Rows far apart leave keys between their windows that nobody sees.)
-__device__ __noinline__ bool rows_see(const int32_t* positions, int rows, int window, int sinks, int a, int b) {
-#pragma unroll 1
-  for (int r = 0; r < rows; ++r) {
-    const int p = min(positions[r], kMaxKeys);  // (as window_position; below 0 it sees none)
-    if (p >= a && (a < sinks || (window > 0 && b > p - window))) return true;
-  }
-  return false;
 }
 
 // KVT 0 bf16, 1 e4m3 with static scales, 2 e4m3 with block scales.
@@ -480,11 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
       const int v = 128 * (j0 + i) + 64 * lane;
       sh.first[slot][lane] = bad != 0u || (v < T.ns && v + 63 >= T.ns) ? -1 : T.key(v);
     }
-    if (bad != 0u) {  // counted where a row sees one of them
-      const int k0 = block_key(j0 + i);
-      const bool missed = lane < 8 && rows == kNoPage && rows_see(P.logical + row0, nrows, P.window, P.sinks, k0, k0 + 15);
-      if (__any_sync(0xffffffffu, missed) && lane == 0) flag_error(P.err);
-    }
+    // (counted where a row sees one of them)
+    if (bad != 0u) count_blocks(&sh.rows[0], 128 * (j0 + i), bad);
     if (lane == 0) {
       sh.check[slot] = bad != 0u;
       sh.ns = T.ns;
@@ -496,16 +540,22 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
 
   if (warp >= kSoftWarps) {
     regs_down<kOtherRegs>();
+    if (warp > kSoftWarps) {
+      // (windows that all meet leave no key out: the first and the last cover them)
+      if (lane == 0)
+        sh.rows[warp - (kSoftWarps + 1)] = {P.logical + row0, nrows, P.window, P.sinks, T.ns, T.shift, pmax - pmin >= P.window, P.err};
+      __syncwarp();
+    }
     if (warp >= kSoftWarps + 2) {
       // ---------------------------------------------------------- by hand
       const int lt = tid - (kSoftWarps + 2) * 32;  // 0 .. 63
       // an odd element at key `key` of a tile, and, once the warp is through
       // the tile (some is its lane's answer), the tile with its odd keys
-      uint32_t* odd_keys = sh.odd_keys[warp & 1];
+      uint32_t* odd_keys = sh.odd_keys[(warp - (kSoftWarps + 1)) & 1];
       auto remember = [&](int key) { atomicOr(&odd_keys[key >> 5], 1u << (key & 31)); };
       auto file = [&](int v, bool some) {
         if (!__any_sync(0xffffffffu, some)) return;
-        file_poison(&sh, v, odd_keys, P.err);
+        file_poison(&sh, warp - (kSoftWarps + 1), v);
       };
       auto announce = [&](uint64_t* bar) {
         fence_proxy_async_smem();
@@ -532,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tile_kernel(const __grid_c
         auto check = [&](int from, int to) {
 #pragma unroll 1
           for (int key = from + ((k0 - from) & (S - 1)); key < to; key += S)
-            if (check_key(key) && rows_see(P.logical + row0, nrows, P.window, P.sinks, T.key(v + key), T.key(v + key))) {
+            if (check_key(key)) {
               remember(key);
               some = true;
             }
