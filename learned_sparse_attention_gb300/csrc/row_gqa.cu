@@ -553,8 +553,8 @@ __global__ void __launch_bounds__(256) row_merge_kernel(const RowGqaParams P) {
   nan = __any_sync(half, nan);
 #pragma unroll
   for (int k = 0; k < kMost; ++k) {
-    w[k] = w[k] == -INFINITY ? 0.f : ex2_ftz(w[k] - M);
-    W += w[k];
+    w[k] = w[k] == -INFINITY ? -1.f : ex2_ftz(w[k] - M);  // (-1: saw nothing)
+    W += fmaxf(w[k], 0.f);
   }
 #pragma unroll
   for (int o = 8; o >= 1; o >>= 1) W += __shfl_xor_sync(half, W, o);
@@ -570,7 +570,9 @@ __global__ void __launch_bounds__(256) row_merge_kernel(const RowGqaParams P) {
       for (int u = 0; u < 8; ++u) {
         ws[u] = __shfl_sync(half, w[k], i + u, 16);
         a[u] = b[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (ws[u] > 0.f) {  // (a split that saw nothing may not have written)
+        // (a split that saw nothing may not have written; one whose weight
+        // vanishes still hands on what is not finite)
+        if (ws[u] >= 0.f) {
           const float4* po = reinterpret_cast<const float4*>(P.part_o + ((16 * k + i + u) * stride + head) * 128 + d0);
           a[u] = __ldcg(po);
           b[u] = __ldcg(po + 1);

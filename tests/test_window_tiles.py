@@ -318,3 +318,27 @@ def test_a_prompt_that_sees_all_before_it(kind):
     out = b.window(2 ** 31 - 1, 0)
     assert Q.check_errors() == 0
     check_rows(b, out, some(b.n, 20) + [1, 127, 128, 3499, 3500], 2 ** 31 - 1, 0)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,context", [(1, 700), (1, 1300), (1, 6000), (3, 6000), (40, 6000), (600, 6000)])
+def test_odd_values_of_negligible_weight_reach_who_sees_them(kind, rows, context):
+    """Half of the tokens weigh less than 2^-126 of the other half's, with an
+    odd value among them: single rows and tiles, joined over splits or not."""
+    b = Batch([context], [rows], kind=kind, page=64, block=32, seed=37, hq=8, hkv=1, gate=False)
+    sign = torch.from_numpy(np.random.default_rng(5).choice([-1.0, 1.0], D))
+    b.q[:] = 2 * sign.bfloat16()
+    half = (context - rows) // 2
+    code = {"bf16": 4.0, "e4m3": 128.0, "block": 4.0}[kind]
+    if kind == "block":
+        b.scales[..., 0] = 127
+    for t in range(context):
+        row = (-code if t < half else code) * sign
+        k = row.bfloat16() if kind == "bf16" else row.to(torch.float8_e4m3fn).view(torch.uint8)
+        b.kv[b.table[0, t // 64], 0, t % 64, :D] = k
+    tok = half // 3
+    b.kv[b.table[0, tok // 64], 0, tok % 64, D + 9] = float("nan") if kind == "bf16" else 0x7F
+    out = b.window(100000, 0)
+    assert Q.check_errors() == 0
+    assert np.isnan(out[:, :, 9]).all()
+    assert np.isfinite(out[:, :, np.arange(D) != 9]).all()
