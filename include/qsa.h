@@ -569,7 +569,8 @@ size_t qsa_window_workspace_bytes(const qsa_gqa_cfg* gcfg, const qsa_window_args
  *  slopes         [Hq] fp32, finite and below 2^64 in size, or NULL
  *  doc_start      [rows] int32: first token of the row's document (NULL: 0)
  *  prefix_end     [rows] int32: the row sees the tokens below it although they
- *                 may lie ahead of it (NULL: 0); they have to be in the cache
+ *                 may lie ahead of it (NULL: 0); they have to be in the cache.
+ *                 Values below 0 are 0 in both
  *  ws             qsa_biased_workspace_bytes() bytes, 256-byte aligned (NULL
  *                 where that is 0); its contents need not be kept or cleared
  */

@@ -31,11 +31,13 @@ __device__ __forceinline__ int window_position(const RowGqaParams& P, int row) {
 // position p.
 struct Span {
   int p, lo, hi;
-  __device__ __forceinline__ bool sees() const { return lo <= hi; }
+  __host__ __device__ __forceinline__ bool sees() const { return lo <= hi; }
 };
-__device__ __forceinline__ Span span_at(int p, int window, int doc, int prefix) {
+__host__ __device__ __forceinline__ Span span_at(int p, int window, int doc, int prefix) {
   if (p < 0) return {-1, 0, -1};
-  return {p, max(max(doc, 0), p - window + 1), max(p, min(prefix, kMaxKeys) - 1)};
+  // (clamped from both sides: prefixes may have any value, and what follows adds
+  // up to a tile's keys to the last token)
+  return {p, max(max(doc, 0), p - window + 1), max(p, min(max(prefix, 1), kMaxKeys) - 1)};
 }
 __device__ __forceinline__ Span biased_span(const RowGqaParams& P, int row) {
   return span_at(window_position(P, row), P.window, P.doc_start != nullptr ? P.doc_start[row] : 0,
