@@ -57,6 +57,13 @@ __device__ __forceinline__ void ring_commit_row(const CompressParams& P, int row
   ring_commit_store(P, ring_commit_prepare(P, row, lane16), lane16);
 }
 
+// How many rows a request has that begins at row `start` and ends before `end`;
+// -1 where they do not lie within [0, rows).  (Compared, not subtracted: starts
+// may be anything.)
+__host__ __device__ __forceinline__ int rows_of_request(int start, int end, int rows) {
+  return start >= 0 && end >= start && end <= rows ? end - start : -1;
+}
+
 // Row group g of the logits kernel, found by the whole block: the rows of
 // each request in chunks of R, numbered in request order.  Returns
 // (row0, nrows, request, 0), or row0 = -1 when g is past the last group.
@@ -77,8 +84,8 @@ __device__ __forceinline__ int4 find_group(const int32_t* qsl, int reqs, int row
     int n = 0, start = 0;
     if (q < reqs) {
       start = qsl[q];
-      n = qsl[q + 1] - start;
-      if (n < 0 || start < 0 || start + n > rows) {  // rows outside [0, rows): skipped
+      n = rows_of_request(start, qsl[q + 1], rows);
+      if (n < 0) {  // skipped
         if (g == 0) flag_error(err);
         n = 0;
       }

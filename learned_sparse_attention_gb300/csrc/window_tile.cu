@@ -341,8 +341,8 @@ __device__ __forceinline__ int4 find_group_32(const int32_t* qsl, int reqs, int 
   int n = 0, start = 0;
   if (lane < reqs) {
     start = qsl[lane];
-    n = qsl[lane + 1] - start;
-    if (n < 0 || start < 0 || start + n > rows) {  // rows outside [0, rows): skipped
+    n = rows_of_request(start, qsl[lane + 1], rows);
+    if (n < 0) {  // skipped
       if (g == 0 && threadIdx.x < 32) flag_error(err);
       n = 0;
     }

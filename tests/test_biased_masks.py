@@ -64,3 +64,20 @@ def test_highest_ends(kind, rows, high):
     assert (out[odd[:rows].nonzero()[0]] == 0).all()
     b.check(out, [i for i in some(rows, 8) if not odd[i]])
     Q.check_errors()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("reqs", [6, 40])
+def test_starts_that_step_back_across_the_integers(kind, reqs):
+    """Requests whose starts are outside the call are counted and have no rows,
+    those beside them theirs; in window calls too."""
+    b = Biased([1500] + [16] * (reqs - 2) + [900], [1300] + [0] * (reqs - 2) + [700], hq=8, hkv=1, page=16, kind=kind, seed=3, pad=2)
+    b.setup(cap=20.0)
+    b.qsl[2], b.qsl[3] = HIGH, -10  # 1300 .. HIGH, HIGH .. -10, -10 .. 1300
+    out = b.run()
+    assert Q.check_errors() > 0
+    b.check(out, some(b.n, 20))
+    b.d["out"].fill_(7.0)
+    out = b.window(500, 4)
+    assert Q.check_errors() > 0
+    b.check_window(out, 500, 4, some(b.n, 20))
