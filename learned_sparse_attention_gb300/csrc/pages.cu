@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kCopy) free_kernel(const Pool P, const int32_t
 // ---------------------------------------------------------------- compact
 struct Moves {
   int32_t* count;   // pages that move
-  int32_t* to;      // [num_blocks]: where a page from `live` on goes (-1: free)
+  int32_t* to;      // [num_blocks]: where a page is afterwards (-1: free now), from a 16-byte border on
   int32_t* movers;  // [num_blocks / 2 + 1], and where they go
   int32_t* holes;
 };
@@ -524,11 +524,20 @@ __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const Pool P, const
     const int4 v4 = base == 0 ? first : load_refs(P, p);
     const int v[4] = {v4.x, v4.y, v4.z, v4.w};
     long long mine = 0;
-    int kind[4];
+    int kind[4], to[4];  // 1: a hole, 2: a mover
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      kind[k] = p + k >= P.num_blocks ? 0 : p + k < live ? (v[k] <= 0 ? 1 : 0) : v[k] > 0 ? 2 : 3;
+      const bool low = p + k < live;
+      kind[k] = p + k >= P.num_blocks ? 0 : low && v[k] <= 0 ? 1 : !low && v[k] > 0 ? 2 : 0;
       mine += kind[k] == 1 ? 1ll : kind[k] == 2 ? 1ll << 32 : 0ll;
+      to[k] = low && v[k] > 0 ? static_cast<int>(p + k) : -1;  // (movers' below)
+    }
+    if (p + 3 < P.num_blocks) {
+      *reinterpret_cast<int4*>(M.to + p) = make_int4(to[0], to[1], to[2], to[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (p + k < P.num_blocks) M.to[p + k] = to[k];
     }
     long long total;
     long long rank = found + cluster_scan(mine, &total, warps, slot, turn);
@@ -540,13 +549,11 @@ __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const Pool P, const
       } else if (kind[k] == 2) {
         M.movers[rank >> 32] = static_cast<int>(p + k);
         rank += 1ll << 32;
-      } else if (kind[k] == 3) {
-        M.to[p + k] = -1;
       }
     }
     found += total;
   }
-  cluster.sync();  // both lists are complete
+  cluster.sync();  // both lists are complete, and M.to but for movers
   const int moves = static_cast<int>(found >> 32);
   for (int k = cluster.block_rank() * kPlan + threadIdx.x; k < moves; k += kPlan * cluster.num_blocks()) M.to[M.movers[k]] = M.holes[k];
   if (cluster.block_rank() == 0 && threadIdx.x == 0) {
@@ -556,10 +563,9 @@ __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const Pool P, const
 }
 
 template <int N>
-__global__ void __launch_bounds__(kCopy, 4) compact_move_kernel(const Pool P, const __grid_constant__ Planes<N> L, const Moves M, const int32_t* live_in,
-                                                             int parts) {
+__global__ void __launch_bounds__(kCopy, 4) compact_move_kernel(const Pool P, const __grid_constant__ Planes<N> L, const Moves M, int parts) {
   griddep_wait();
-  const int moves = *M.count, live = *live_in;
+  const int moves = *M.count;
   const long long ctas = gridDim.x;
   const long long items = static_cast<long long>(moves) * parts;
   for (int plane = 0; plane < L.n; ++plane)
@@ -584,11 +590,10 @@ __global__ void __launch_bounds__(kCopy, 4) compact_move_kernel(const Pool P, co
     const int n = P.pages(l);
     for (int k = threadIdx.x; k < n; k += kCopy) {
       const int page = row[k];
-      if (page >= 0 && page < live) continue;
       const int to = page >= 0 && page < P.num_blocks ? M.to[page] : -1;
-      if (to < 0)
+      if (to < 0)  // (no used page: below `live` it may hold another sequence's tokens now)
         flag_error(P.err);
-      else
+      else if (to != page)
         row[k] = to;
     }
   }
@@ -790,7 +795,7 @@ qsa_status do_compact(const qsa_page_pool* pool, int32_t* live, void* ws, size_t
   if (grid > 4ll * sms) grid = 4ll * sms;
   return cuda_ok(with_planes(pool->planes, pool->n_planes, pool->page_size, [&](const auto& planes) {
     auto kernel = compact_move_kernel<sizeof(planes.p) / sizeof(Plane)>;
-    return launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), dim3(kCopy), 0, stream, true, P, planes, M, static_cast<const int32_t*>(live), parts);
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), dim3(kCopy), 0, stream, true, P, planes, M, parts);
   }));
 }
 

@@ -126,6 +126,7 @@ class Model:
         live = sum(r > 0 for r in self.refs)
         holes = [p for p in range(live) if self.refs[p] <= 0]
         movers = [p for p in range(live, len(self.refs)) if self.refs[p] > 0]
+        used = {p for p, r in enumerate(self.refs) if r > 0}
         to = dict(zip(movers, holes))
         for a, b in to.items():
             self.copy_tokens(a, b, self.page)
@@ -136,10 +137,8 @@ class Model:
                 continue
             for k in range(self.pages(l)):
                 p = self.table[r][k]
-                if 0 <= p < live:
-                    continue
-                if p in to:
-                    self.table[r][k] = to[p]
+                if p in used:
+                    self.table[r][k] = to.get(p, p)
                 else:
                     self.errors += 1
         return live
