@@ -647,14 +647,15 @@ typedef struct qsa_page_pool {
  * copied in every plane to a free page.  Free pages are the lowest ones, given
  * to the forks in order.
  *  tails  [n] int32 (out): the child's own copy of the last page; -1 where none
- *         was needed; -2 where the fork was refused, and counted: an index
+ *         was needed or the parent's is outside the pool; -2 where the fork was refused, and counted: an index
  *         outside the table, a child that is not empty (or that an earlier
  *         fork of the call names too), a parent's length that its row cannot
  *         hold, or no page left (a fork that needs one gets it iff it and all
  *         forks before it that need one could).  A refused child stays empty.
  *  A negative index of either list is padding: nothing happens, tails is -1.
  *  All lengths are read as they were before the call.  Entries of a parent
- *  outside the pool are counted, become -1 in the child and are not copied.
+ *  outside the pool are counted, become -1 in the child and are not copied (a
+ *  last page's too, which then takes no free page).
  *  reqs + 2 n <= 51200 (else QSA_ERR_UNSUPPORTED).
  */
 qsa_status qsa_pages_fork(const qsa_page_pool* pool, const int32_t* parents,

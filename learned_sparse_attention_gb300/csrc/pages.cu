@@ -265,7 +265,7 @@ __device__ __forceinline__ void copy_page(const Plane& L, int from, int to, int 
 
 // ---------------------------------------------------------------- fork
 // tails[i]: the page of the child's own copy of the last page, -1 none needed
-// (or padding), -2 refused.
+// (or padding, or the parent's is no page of the pool), -2 refused.
 __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const Pool P, const int32_t* parents, const int32_t* children, int n, int32_t* tails) {
   extern __shared__ int32_t sm[];
   __shared__ long long warps[33], slot[2];
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const Pool P, const in
   long long needed = 0;
   for (int i0 = 0; i0 < n; i0 += kPlan) {
     const int i = i0 + threadIdx.x;
-    int l = -1;
+    int l = -1, need = 0;
     if (i < n) {
       const int a = parents[i], c = children[i];
       if (a >= 0 && c >= 0) {
@@ -295,9 +295,12 @@ __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const Pool P, const in
         }
       }
       len[i] = l;
+      if (l > 0 && l % P.page != 0) {  // (a last page outside the pool is not copied)
+        const int last = P.row(a)[l / P.page];
+        need = last >= 0 && last < P.num_blocks;
+      }
     }
     long long total;
-    const int need = l > 0 && l % P.page != 0;
     const long long at = block_scan(need, &total, warps);
     if (i < n) sums[i] = static_cast<int32_t>(needed + at + need);
     needed += total;
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const Pool P, const in
   if (cluster.block_rank() == 0) {
     for (int i = threadIdx.x; i < n; i += kPlan) {
       const int l = len[i];
-      const bool need = l > 0 && l % P.page != 0;
+      const bool need = sums[i] > (i > 0 ? sums[i - 1] : 0);
       if (l == -2 || (need && sums[i] > got)) {
         tails[i] = -2;
         flag_error(P.err);
@@ -339,21 +342,18 @@ __global__ void __launch_bounds__(kCopy, 4) fork_copy_kernel(const Pool P, const
   const int l = P.lengths[c], full = l / P.page, used = l - full * P.page;
   const int32_t* from = P.row(a);
   if (plane < L.n) {
-    if (used == 0) return;
-    const int src = from[full];
-    if (src < 0 || src >= P.num_blocks) return;  // (counted below)
+    if (used == 0 || tail < 0) return;
     const Plane& pl = L.p[plane];
-    copy_page(pl, src, tail, (used + pl.per - 1) / pl.per, blockIdx.z, gridDim.z);
+    copy_page(pl, from[full], tail, (used + pl.per - 1) / pl.per, blockIdx.z, gridDim.z);
     return;
   }
   int32_t* to = P.row(c);
   for (int k = blockIdx.z * kCopy + threadIdx.x; k < P.bt_stride; k += gridDim.z * kCopy) {
-    if (k == full && used != 0) {  // (the planner's)
-      if (from[k] < 0 || from[k] >= P.num_blocks) flag_error(P.err);
-      continue;
-    }
+    if (k == full && tail >= 0) continue;  // (the planner's)
     int page = -1;
-    if (k < full) {
+    if (k == full && used != 0) {  // (the planner found no page of the pool there)
+      flag_error(P.err);
+    } else if (k < full) {
       page = from[k];
       if (page < 0 || page >= P.num_blocks) {
         page = -1;

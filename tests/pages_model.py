@@ -37,7 +37,8 @@ class Model:
             bad = a >= len(self.table) or c >= len(self.table) or c in named or old[c] != 0
             bad = bad or not 0 <= old[a] <= self.capacity
             named.add(c)
-            if not bad and old[a] % self.page:
+            tail = not bad and old[a] % self.page and self.inside(self.table[a][old[a] // self.page])
+            if tail:
                 bad = given >= len(free)
                 given += 1
             if bad:
@@ -54,12 +55,11 @@ class Model:
                 else:
                     self.errors += 1
             tails.append(-1)
-            if used:
+            if tail:
                 tails[-1] = row[full] = free[given - 1]
-                if self.inside(self.table[a][full]):
-                    copies.append((self.table[a][full], tails[-1], used))
-                else:
-                    self.errors += 1
+                copies.append((self.table[a][full], tails[-1], used))
+            elif used:
+                self.errors += 1
             self.lengths[c] = old[a]
             self.table[c] = row
         for p in shared:

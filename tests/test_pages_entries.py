@@ -54,3 +54,41 @@ def test_every_free_page_is_known(blocks):
         b.model.table[0] = list(range(blocks))
         b.lengths[0] = b.model.lengths[0] = 16 * blocks
         b.compact()
+
+
+@pytest.mark.parametrize("kind", ["none", "kv", "block"])
+@pytest.mark.parametrize("bad", [-1, -7, 20, 1 << 30])
+def test_forks_of_a_last_page_outside_the_pool(kind, bad):
+    """The child's entry is -1 as well: it takes no page, whose bytes would be
+    those of a sequence that has left, and its neighbours get theirs as if it were
+    not there."""
+    b = empty(20, 8, 4, 16, kind)
+    b.extend([40, 20, 32, 5, 0, 0, 0, 0])
+    put(b, 0, 2, bad)
+    b.fork([1, 0, 3], [4, 5, 6])
+    assert b.table[5].tolist() == b.table[0].tolist()[:2] + [-1, -1] and b.lengths[5] == 40
+    b.extend([0, 0, 0, 0, 1, 1, 1, 0])     # (a token on that page has no slot)
+    b.free([5])
+    b.fork([2, 0], [5, 7])
+
+
+def test_a_bad_last_page_leaves_the_last_free_one():
+    b = empty(4, 6, 4, 16)
+    b.extend([20, 5, 0, 0, 0, 0])          # three pages of four
+    put(b, 0, 1, 99)
+    b.fork([0, 1, 1], [2, 3, 4])           # the last free page is the second's, the third is refused
+    assert b.lengths.tolist() == [20, 5, 20, 5, 0, 0]
+
+
+def test_many_forks_some_of_bad_pages():
+    """More forks than a planner has threads."""
+    reqs = 2600
+    b = empty(9000, reqs, 3, 16, "none")
+    b.extend([(r * 7) % 41 if r < 600 else 0 for r in range(reqs)])
+    for r in range(0, 600, 5):
+        n = b.model.lengths[r]
+        if n % 16:
+            put(b, r, n // 16, -1 if r % 2 else 9000 + r)
+    children = list(range(600, reqs))
+    b.fork([(7 * c) % 600 for c in children], children)
+    b.extend([1] * reqs)
