@@ -242,7 +242,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) w4_rows_kernel(const ProjW4Par
 //   warps 2-9  a thread to a column: codes from shared memory, unpacked, to
 //              tensor memory, every other block each half; at the end the
 //              outputs.
-// Every wait is bounded (mbar_wait); a timeout sets the error word.
+// Every wait is bounded (mbar_wait); a timeout sets the error word, and the tile's
+// outputs stay as they were, or are NaNs where a cluster joins its sums.
 // kSplit: tiles of few rows leave the SMs without enough columns (13 440 make 105
 // tiles), so that clusters of CTAs share a tile's inputs and join their sums
 // through shared memory.  Measured: 64 rows with two CTAs a tile and two an SM 20.1
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(Tile<BN>::kThreads, Tile<BN>::kCtas)
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   uint8_t* sC = smem_raw + pad;
   uint8_t* sX = sC + T::CS * T::kC;
-  bool done = true;  // (a wait that gave up)
+  bool done = true;  // (false: a wait gave up)
   const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int rank = T::kSplit ? static_cast<int>(blockIdx.x) % splits : 0;
   const int n0 = static_cast<int>(blockIdx.x) / (T::kSplit ? splits : 1) * 128, r0 = blockIdx.y * BN;
@@ -332,13 +333,15 @@ __global__ void __launch_bounds__(Tile<BN>::kThreads, Tile<BN>::kCtas)
     for (int i = 0; i < nb; ++i) {
       if (i % kPer == 0) {
         const int cs = i / kPer % T::CS;
-        if (!all_ok(mbar_wait(&c_empty[cs], ((i / kPer / T::CS) & 1) ^ 1, P.err))) break;
+        done = all_ok(mbar_wait(&c_empty[cs], ((i / kPer / T::CS) & 1) ^ 1, P.err));
+        if (!done) break;
         if (lane == 0) mbar_arrive_expect_tx(&c_full[cs], T::kC);
         __syncwarp();
         tma_box(sC + cs * T::kC, &tmap_c, (b0 + i) * 32 * H, n0, &c_full[cs]);
       }
       const int xs = i % T::XS;
-      if (!all_ok(mbar_wait(&x_empty[xs], ((i / T::XS) & 1) ^ 1, P.err))) break;
+      done = all_ok(mbar_wait(&x_empty[xs], ((i / T::XS) & 1) ^ 1, P.err));
+      if (!done) break;
       if (lane == 0) mbar_arrive_expect_tx(&x_full[xs], T::kX);
       __syncwarp();
 #pragma unroll
@@ -350,7 +353,8 @@ __global__ void __launch_bounds__(Tile<BN>::kThreads, Tile<BN>::kCtas)
     const uint32_t x0 = desc_lo(smem_addr(sX), 16);
     for (int i = 0; i < nb; ++i) {
       const int xs = i % T::XS, as = i % T::AS;
-      if (!all_ok(mbar_wait(&x_full[xs], (i / T::XS) & 1, P.err) && mbar_wait(&a_full[as], (i / T::AS) & 1, P.err))) break;
+      done = all_ok(mbar_wait(&x_full[xs], (i / T::XS) & 1, P.err) && mbar_wait(&a_full[as], (i / T::AS) & 1, P.err));
+      if (!done) break;
       tc_fence_after_sync();
 #pragma unroll
       for (int kk = 0; kk < 4 * H; ++kk)
@@ -359,7 +363,7 @@ __global__ void __launch_bounds__(Tile<BN>::kThreads, Tile<BN>::kCtas)
       mma_commit(&x_empty[xs]);
       mma_commit(&a_empty[as]);
     }
-    mma_commit(&acc_full);
+    if (done) mma_commit(&acc_full);
   } else {
     const int quad = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
@@ -453,6 +457,8 @@ __global__ void __launch_bounds__(Tile<BN>::kThreads, Tile<BN>::kCtas)
   // ---- outputs, eight columns a thread
   if constexpr (T::kSplit) {
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    if (!good)  // (a wait gave up: no sum of these may pass for a result)
+      for (int i = threadIdx.x; i < BN * 128; i += T::kThreads) reinterpret_cast<float*>(sX)[i] = __int_as_float(0x7fffffff);
     cluster.sync();
     // the cluster's sums, in order: every CTA its share of the rows
     const int items = (rows - rank + splits - 1) / splits * 16;
