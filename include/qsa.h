@@ -328,7 +328,9 @@ qsa_status qsa_qkv_index_proj(const void* x, const void* w, int32_t rows, int32_
  *           the even one in the low nibble; OCP FP4 E2M1 (sign, 2 exponent
  *           bits, 1 mantissa bit: 0, .5, 1, 1.5, 2, 3, 4, 6)
  *  scales   QSA_W4_MX: [ncols, hidden / 32] bytes b that stand for 2^(b - 127),
- *           2^-60 .. 2^16 (67 .. 143); others are read as the nearest of them.
+ *           2^-60 .. 2^16 (67 .. 143); others are read as the nearest of them,
+ *           neither counted nor refused: above 143 weights come out smaller, and
+ *           255, a NaN elsewhere, is 2^16.  (A NaN e4m3 scale is one.)
  *           QSA_W4_NV: [ncols, hidden / 16] e4m3 values.  4-byte aligned
  *  scale    one finite factor for all weights
  * A code times its scale is a bf16 value exactly, so no weight is rounded.
@@ -684,7 +686,8 @@ qsa_status qsa_pages_extend(const qsa_page_pool* pool, const int32_t* query_star
  * each, their table entries become -1, their lengths 0.  Negative indices are
  * padding; one that is named twice is freed once; indices past the table,
  * lengths that a row cannot hold, entries outside the pool and pages that
- * nobody holds are counted.
+ * nobody holds are counted.  (A length that a row cannot hold becomes 0 as well;
+ * its row and the references of its pages stay as they were.)
  */
 qsa_status qsa_pages_free(const qsa_page_pool* pool, const int32_t* requests, int32_t n,
                           void* stream);
@@ -708,7 +711,9 @@ size_t qsa_pages_workspace_bytes(const qsa_page_pool* pool);
  * [ring_blocks, S, 1, D] is a plane of one unit of S * D elements a page, so
  * that a forked sequence's ring is copied likewise.  A pair with a negative index is
  * padding.  A pair with an index past the planes, or whose dst is an earlier
- * pair's dst or another pair's src, is counted and not copied.
+ * pair's dst or another pair's src, is counted and not copied.  (Every CTA reads
+ * the whole list to know: long lists of small pages are better given in parts,
+ * where no pair of a part depends on another part's.)
  */
 qsa_status qsa_pages_copy(const qsa_page_plane* planes, int32_t n_planes, int32_t page_size,
                           int32_t num_blocks, const int32_t* src, const int32_t* dst, int32_t n,

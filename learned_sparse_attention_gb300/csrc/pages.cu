@@ -22,13 +22,14 @@
 // and shared pages' counts follow in a grid of their own.  Every kernel starts
 // while the one before it in the stream ends and waits for it before it reads
 // anything; planners let their followers start at once (two children 16.4 -> 14.6
-// us; copies that do so too leave it at 15.5).
+// us, now 15.3; copies that do so too left it at 15.5).
 //
 // Bound: planners by latency (a few dependent loads, two scans, the cluster's
 // barriers), copies by HBM.  Measured: fork, a ring's copy, extend and free of two
-// children of a small model 14.5 to 15.7 us (five launches; the calls take the host 22), of
-// 240 children of 16 prompts of ~10 000 to 20 000 tokens 33.5 us, 15 of them the
-// copies of 66 MB of last pages; half of a pool of 48 sequences of ~4500 to 9000
+// children of a small model 15.3 us (five launches; the calls take the host 22), of
+// 240 children of 16 prompts of ~10 000 to 20 000 tokens 33 us, 15 of them the
+// copies of 66 MB of last pages (static e4m3 27.5, block scales 33: half the bytes, more
+// planes); half of a pool of 48 sequences of ~4500 to 9000
 // tokens packed in 246 us (1.32 GB read and written, 5.6 TB/s behind a planner of 9
 // us; 4 to 16 accesses of a thread in flight, 2 to 8 CTAs an SM and parts of 16 to
 // 128 KB took 246 to 294, streaming loads 263).  A planner that makes the copies
@@ -368,7 +369,10 @@ __global__ void __launch_bounds__(kCopy, 4) fork_copy_kernel(const Pool P, const
 
 // Pair i = blockIdx.x: page src[i] to dst[i] in plane blockIdx.y.  A pair whose
 // dst an earlier pair has too, or that is another pair's src, would race: it is
-// left out.  Every CTA of the pair asks that itself (n <= kMaxPairs).
+// left out.  Every CTA of the pair asks that itself (n <= kMaxPairs): without a
+// second launch or scratch, but n^2 reads.  Measured: 256 pages of 128 KB 15 us, 4096
+// 201 (5.3 TB/s); 256 rings of 2 KB 2.9 us, 4096 34, 16 384 428, where the reads of the
+// list are nearly all.
 template <int N>
 __global__ void __launch_bounds__(kCopy, 4) copy_kernel(const __grid_constant__ Planes<N> L, int num_blocks, const int32_t* src, const int32_t* dst,
                                                      int n, unsigned long long* err) {

@@ -18,11 +18,13 @@
 // fragments in the same order of inputs; the four warps of a CTA add up in
 // shared memory, in order.  More rows: tcgen05 (below).
 //
-// Bound: few rows by the instructions that unpack (17 for eight codes; HBM alone
-// would take 4.6 us for hidden 4096 and 13 440 columns, loads in this order alone
-// 5.8), tiles of few rows by those and by fixed costs, prefill by the tensor cores.
-// Measured there, ten calls on four sets of inputs: one row 11.1 us, 8 rows 12.5, 9
-// to 64 rows 18 to 20, 128 rows 22, 256 rows 30, 2048 rows 156 (1.44 PFLOP/s); 3
+// Bound: few rows by waits for loads beside the instructions that unpack (17 for
+// eight codes): 11 warps an SM with one stretch of codes ahead, issue slots 53 % used,
+// DRAM 29 %, 2.4 of 3.1 stall cycles an issue waits for loads (HBM alone would take 4.6
+// us for hidden 4096 and 13 440 columns, loads in this order alone 5.8); tiles of few
+// rows by unpacking and fixed costs, prefill by the tensor cores.
+// Measured there, ten calls on four sets of inputs: one row 11.1 us, 8 rows 12.7, 9
+// to 64 rows 18 to 20, 128 rows 23, 256 rows 30, 2048 rows 156 (1.44 PFLOP/s); 3
 // rows of hidden 1024 and 3456 columns 2.9.  Of the 20 us of 64 rows 8 remain
 // without products and sums.  Unpacking by two shifts instead of a multiplication
 // takes 18 cycles a word and scheduler instead of 15.6, by byte tables 20; more

@@ -69,9 +69,12 @@
 // Without the softmax the loads and products alone took 374 us for the 8192
 // rows.  Biased, an 8192-row prompt whose first 2048 tokens are seen from both
 // sides: 436 us with masks alone (1.34 PFLOP/s), 479 with slopes, 652 with a cap
-// (0.90; the FMA pipe's share of tanh, ~6 operations a score), 803 with a cap over
-// block scales; three requests of ~3000 to 4003 rows in documents of ~700 tokens,
-// slopes, block scales: 168 us (1020 CTAs of ~4.2 tiles and the fixed costs).
+// (0.90), over static e4m3 455, 500 and 705, over block scales 493, 519 and 801;
+// three requests of ~3000 to 4003 rows in documents of ~700 tokens, slopes: 164 us
+// on bf16, 143 on static e4m3, 168 with block scales (1020 CTAs of ~4.2 tiles and the
+// fixed costs).  With a cap no pipe is full (2048 rows: tensor 26 %, XU 28, FMA 21,
+// issue slots 49): ~6 operations a score for tanh lengthen the chain from scores to
+// weights, in which the warps wait for tensor memory and for each other.
 #include <cuda_fp16.h>
 
 #include <climits>
