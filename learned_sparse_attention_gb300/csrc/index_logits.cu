@@ -269,7 +269,8 @@ __global__ void __launch_bounds__(LogitsCfg<IDT, NPAD, G, TMA>::THREADS, 1)
       const int nbox = C::ATOMS * ppt;  // <= 32 for cpage >= 8
       const uint32_t box_bytes = static_cast<uint32_t>(cpage) * 128u;
       const int elems_per_atom = 128 / (IDT == 1 ? 1 : 2);
-      const int f = min(P.logical[P.qsl[req]], P.logical[row0]);
+      const int q0 = P.qsl[req];  // (behind this row, or before the call: counted by the compress kernel)
+      const int f = min(P.logical[q0 >= 0 && q0 <= row0 ? q0 : row0], P.logical[row0]);
       const int c_safe = f < 0 ? 0 : f / P.ratio;
       const int n_early = max(0, min(min(ntiles, C::STAGES), c_safe / 128 - t_begin));
       if (n_early == 0) griddep_wait();
